@@ -10,6 +10,9 @@ Names follow the C ABI: ``gemm_f16`` (raw pointers), ``gemm_f16_plan``,
 ``gemm_f16_set_config``, ``gemm_f16_strerror``, ``gemm_f16_device_status``;
 ``matmul(a, b, out_dtype)`` is the tensor-level call of the ``matmul(a, b,
 out_dtype)`` of "Quickstart: GPU", section "Pipelining: a matmul kernel".
+The layer operators (``linear``, ``gated_ffn``, ``linear_cross_entropy``, their
+``_backward`` calls and ``clip_grad_norm``; ``include/layer_ops.h``) are bound
+in ``layers.py``.
 """
 from __future__ import annotations
 
@@ -35,7 +38,12 @@ STATUS = {
 EXPORTED = ["add_matrices_f32", "gemm_f16", "gemm_f16_acc", "gemm_f16_ws", "gemm_f16_noalloc", "gemm_f16_workspace_size", "gemm_f16_plan",
             "gemm_f16_plan_ws",
             "gemm_f16_set_config", "gemm_f16_get_config", "gemm_f16_strerror", "gemm_f16_device_status",
-            "gemm_f16_abi_version"]
+            "gemm_f16_abi_version",
+            "linear_forward", "linear_backward", "linear_backward_workspace",
+            "gated_ffn_forward", "gated_ffn_backward", "gated_ffn_backward_workspace",
+            "linear_cross_entropy", "linear_cross_entropy_workspace",
+            "linear_cross_entropy_backward", "linear_cross_entropy_backward_workspace",
+            "grad_clip", "grad_clip_workspace"]
 
 
 class GemmPlan(ctypes.Structure):
@@ -101,6 +109,18 @@ def load_library(path: str = LIB_PATH):
             lib.gemm_f16_strerror.restype = ctypes.c_char_p
             lib.gemm_f16_device_status.argtypes = [ctypes.POINTER(ci), ci]
             lib.gemm_f16_device_status.restype = ci
+            sp = ctypes.POINTER(ctypes.c_size_t)
+            for name in ("linear_forward", "linear_backward", "gated_ffn_forward", "gated_ffn_backward",
+                         "linear_cross_entropy", "linear_cross_entropy_backward", "grad_clip"):
+                getattr(lib, name).argtypes = [vp, vp]
+                getattr(lib, name).restype = ci
+            for name in ("linear_backward_workspace", "gated_ffn_backward_workspace", "linear_cross_entropy_workspace"):
+                getattr(lib, name).argtypes = [vp, sp]
+                getattr(lib, name).restype = ci
+            lib.linear_cross_entropy_backward_workspace.argtypes = [vp, ctypes.c_longlong, sp]
+            lib.linear_cross_entropy_backward_workspace.restype = ci
+            lib.grad_clip_workspace.argtypes = [ctypes.c_longlong, sp]
+            lib.grad_clip_workspace.restype = ci
             lib.gemm_f16_abi_version.argtypes = []
             lib.gemm_f16_abi_version.restype = ci
             _lib = lib
@@ -298,3 +318,8 @@ def matmul(a, b, out_dtype=None, out=None, stream=None, workspace=None):
     if rc != 0:
         raise GemmError(rc)
     return out
+
+
+from .layers import (  # noqa: E402  (it uses the names above)
+    clip_grad_norm, gated_ffn, gated_ffn_backward, linear, linear_backward, linear_cross_entropy,
+    linear_cross_entropy_backward)

@@ -17,7 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtcgemm.so")
-SOURCES = [os.path.join(CSRC, "gemm_f16.cu")]
+SOURCES = [os.path.join(CSRC, "tcgemm.cu")]
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 # Debug variants of the same sources, each its own library beside the product:

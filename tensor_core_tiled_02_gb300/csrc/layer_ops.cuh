@@ -1,0 +1,842 @@
+// Host side of the layer operators (include/layer_ops.h): argument checks,
+// tensor maps, workspaces and launches.  Part of the library's one translation
+// unit (tcgemm.cu), behind gemm_f16.cu, whose device facts, tuning config and
+// status word it shares.
+#pragma once
+
+#include "layer_ops.h"
+
+#include "grad_clip_kernel.cuh"
+#include "layer_pair_kernel.cuh"
+#include "layer_small_kernels.cuh"
+
+namespace {
+
+constexpr long long kMaxDim = INT_MAX - 1024;
+
+// One matrix as the caller describes it.
+struct Mat {
+    const void* p;
+    long long rows, cols, ld;
+    int bytes;  // of an element
+};
+
+Mat mat16(const void* p, long long rows, long long cols, long long ld) { return Mat{p, rows, cols, ld, 2}; }
+
+bool empty(const Mat& m) { return m.rows == 0 || m.cols == 0; }
+
+// Bytes from the first to one past the last element.
+uint64_t extent(const Mat& m) { return ((uint64_t)(m.rows - 1) * m.ld + m.cols) * m.bytes; }
+
+int check_mat(const Mat& m) {
+    if (empty(m)) return GEMM_OK;
+    if (!m.p) return GEMM_ERR_NULL;
+    if (m.ld < m.cols) return GEMM_ERR_DIM;
+    // a tensor map's row stride stays below 2^40 bytes
+    if (((uintptr_t)m.p & 15) || (m.ld * m.bytes) % 16 != 0) return GEMM_ERR_ALIGN;
+    if (m.ld * m.bytes >= (1ll << 40)) return GEMM_ERR_DIM;
+    return GEMM_OK;
+}
+
+struct Span {
+    uint64_t lo, hi;
+};
+
+Span span_of(const Mat& m) {
+    if (!m.p || empty(m)) return Span{0, 0};
+    return Span{(uint64_t)(uintptr_t)m.p, (uint64_t)(uintptr_t)m.p + extent(m)};
+}
+
+Span span_of(const void* p, uint64_t bytes) {
+    if (!p || bytes == 0) return Span{0, 0};
+    return Span{(uint64_t)(uintptr_t)p, (uint64_t)(uintptr_t)p + bytes};
+}
+
+// Whether any of the `nw` written spans overlaps another of them or a read one.
+bool overlaps(const Span* w, int nw, const Span* r, int nr) {
+    auto meet = [](const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; };
+    for (int i = 0; i < nw; ++i) {
+        for (int j = i + 1; j < nw; ++j)
+            if (meet(w[i], w[j])) return true;
+        for (int j = 0; j < nr; ++j)
+            if (meet(w[i], r[j])) return true;
+    }
+    return false;
+}
+
+bool dims_ok(std::initializer_list<long long> positive, long long tokens) {
+    if (tokens < 0 || tokens > kMaxDim) return false;
+    for (long long d : positive)
+        if (d < 1 || d > kMaxDim) return false;
+    return true;
+}
+
+int check_dtype_act(long long dtype, long long act) {
+    if (dtype != LAYER_F16 && dtype != LAYER_BF16) return GEMM_ERR_DTYPE;
+    if (act < LAYER_ACT_NONE || act > LAYER_ACT_GELU_TANH) return GEMM_ERR_CONFIG;
+    return GEMM_OK;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+long long pad8(long long n) { return (n + 7) & ~7ll; }
+
+// What a call needs of the current device, once its arguments are checked.
+struct Ctx {
+    DeviceInfo* dev = nullptr;
+    int ordinal = 0;
+    long long wait_limit = 0;
+    int inject = 0;
+    cudaStream_t stream = nullptr;
+};
+
+int open_ctx(Ctx& c, gemm_stream_t stream) {
+    const gemm_config cfg = current_config();
+    const int rc = device_info(&c.dev);
+    if (rc != GEMM_OK) return rc;
+    if (c.dev->cc != 103) return GEMM_ERR_ARCH;
+    std::call_once(g_encode_once, init_encode);
+    if (!g_encode) return GEMM_ERR_CUDA;
+    c.ordinal = (int)(c.dev - g_dev);
+    c.wait_limit = cfg.wait_limit > 0 ? cfg.wait_limit : kDefaultWaitLimit;
+    c.inject = cfg.inject_stall;
+    c.stream = reinterpret_cast<cudaStream_t>(stream);
+    return GEMM_OK;
+}
+
+// A 128-byte-swizzled tensor map of a matrix with a row stride; outside the
+// matrix it reads zero and writes nothing.
+int encode_mat(CUtensorMap* out, const Mat& m, int dtype, uint32_t box_cols, uint32_t box_rows) {
+    const CUtensorMapDataType dt = m.bytes == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == LAYER_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    cuuint64_t dims[2] = {(cuuint64_t)m.cols, (cuuint64_t)m.rows};
+    cuuint64_t strides[1] = {(cuuint64_t)m.ld * m.bytes};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(out, dt, 2, const_cast<void*>(m.p), dims, strides, box, estr,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_TMAP;
+}
+
+template <typename... P, typename... A>
+int launch_pdl(void (*kern)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t stream, A&&... args) {
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = grid;
+    lc.blockDim = dim3(threads, 1, 1);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    lc.attrs = attr;
+    lc.numAttrs = cluster > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&lc, kern, std::forward<A>(args)...) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+// ---- one matrix product with its epilogue ------------------------------------------
+
+// The operands as stored: a is [M, K] (NN, NT) or [K, M] (TN), b [K, N] (NN, TN)
+// or [N, K] (NT).  A second pair continues K (b2 of kEpiGate: the second weight).
+struct Product {
+    Mat a, b, a2{nullptr, 0, 0, 0, 2}, b2{nullptr, 0, 0, 0, 2};
+    Mat out[3] = {};
+    int outs = 1;
+    Mat in[2] = {};
+    int ins = 0;
+    long long M, N, K;
+    LayerParams p{};
+};
+
+template <int LAY, int EPI, int DT>
+int run_product_pair(const Product& q, const Ctx& c) {
+    constexpr int PN = 256;
+    using L = LayerPairLayout<EPI, PN>;
+    constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
+    constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
+    LayerMaps tm;
+    std::memset(&tm, 0, sizeof(tm));
+    const Mat as[2] = {q.a, q.a2.p ? q.a2 : q.a}, bs[2] = {q.b, q.b2.p ? q.b2 : q.b};
+    int rc = GEMM_OK;
+    for (int i = 0; i < 2 && rc == GEMM_OK; ++i) {
+        if (i == 1 && !q.a2.p && !q.b2.p) {
+            tm.a[1] = tm.a[0];
+            tm.b[1] = tm.b[0];
+            break;
+        }
+        rc = encode_mat(&tm.a[i], as[i], dtype, 64, kAMN ? 64 : 128);
+        if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], bs[i], dtype, 64, kBMN ? 64 : PN / 2);
+    }
+    for (int i = 0; i < q.outs && rc == GEMM_OK && EPI != kEpiLossStats; ++i)
+        rc = encode_mat(&tm.out[i], q.out[i], dtype, 128 / q.out[i].bytes, 32);
+    for (int i = 0; i < q.ins && rc == GEMM_OK; ++i) rc = encode_mat(&tm.in[i], q.in[i], dtype, 128 / q.in[i].bytes, 32);
+    if (rc != GEMM_OK) return rc;
+
+    LayerParams p = q.p;
+    p.M = (int)q.M;
+    p.N = (int)q.N;
+    p.tiles_m = ceil_div(q.M, 256);
+    p.tiles_n = ceil_div(q.N, L::kOutN);
+    if ((long long)p.tiles_m * p.tiles_n > INT_MAX - 1024) return GEMM_ERR_DIM;
+    p.k_switch = ceil_div(q.K, 64);
+    p.k_steps = q.a2.p ? 2 * p.k_switch : p.k_switch;
+    p.raster_group = 8;
+    p.wait_limit = c.wait_limit;
+    p.inject = c.inject;
+    auto kern = layer_pair_kernel<LAY, EPI, DT, PN>;
+    static std::atomic<bool> ready[kMaxDevices];
+    rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
+    if (rc != GEMM_OK) return rc;
+    const int tiles = p.tiles_m * p.tiles_n, pairs = max_pairs_of(*c.dev);
+    return launch_pdl(kern, dim3(2 * (tiles < pairs ? tiles : pairs)), kThreads, L::kSmem, 2, c.stream, tm, p);
+}
+
+template <int LAY, int EPI>
+int run_product(const Product& q, int dtype, const Ctx& c) {
+    return dtype == LAYER_BF16 ? run_product_pair<LAY, EPI, kBF16>(q, c) : run_product_pair<LAY, EPI, kF16>(q, c);
+}
+
+// A weight gradient over no tokens is zero.
+int zero_mat(const Mat& m, const Ctx& c) {
+    if (!m.p || empty(m)) return GEMM_OK;
+    if (cudaMemset2DAsync(const_cast<void*>(m.p), (size_t)m.ld * m.bytes, 0, (size_t)m.cols * m.bytes, (size_t)m.rows,
+                          c.stream) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+int check_all(std::initializer_list<Mat> mats) {
+    for (const Mat& m : mats) {
+        const int rc = check_mat(m);
+        if (rc != GEMM_OK) return rc;
+    }
+    return GEMM_OK;
+}
+
+// ---- linear layer ---------------------------------------------------------------------
+
+int check_workspace(const void* ws, long long have, size_t need) {
+    if (need == 0) return GEMM_OK;
+    if (!ws) return GEMM_ERR_NULL;
+    if ((uintptr_t)ws & 255) return GEMM_ERR_ALIGN;
+    if (have < 0 || (size_t)have < need) return GEMM_ERR_WORKSPACE;
+    return GEMM_OK;
+}
+
+struct LinearGradPlan {
+    bool slope;     // dpre is a matrix of its own
+    bool sums;      // dbias
+    int row_blocks;
+    size_t dpre_at, partial_at, bytes;
+};
+
+LinearGradPlan linear_grad_plan(const linear_grad_args& a) {
+    LinearGradPlan g{};
+    g.slope = a.act != LAYER_ACT_NONE && (a.dx || a.dw);
+    g.sums = a.dbias != nullptr;
+    g.row_blocks = ceil_div(a.tokens, kSlopeRows);
+    g.partial_at = g.slope ? align256((size_t)a.tokens * pad8(a.n) * 2) : 0;
+    g.bytes = g.partial_at + (g.sums ? align256((size_t)g.row_blocks * a.n * 4) : 0);
+    return g;
+}
+
+template <int DT>
+int run_slope(const SlopeParams& sp, void* dbias, int row_blocks, const Ctx& c) {
+    int rc = launch_pdl(layer_slope_kernel<DT>, dim3(sp.col_blocks * row_blocks), 256, 0, 1, c.stream, sp);
+    if (rc == GEMM_OK && dbias)
+        rc = launch_pdl(layer_column_sum_kernel<DT>, dim3(ceil_div(sp.cols, 32)), 256, 0, 1, c.stream,
+                        (const float*)sp.partial, dbias, row_blocks, sp.cols);
+    return rc;
+}
+
+// ---- vocabulary cross entropy ------------------------------------------------------------
+
+constexpr int kLossPart = 256;  // vocabulary columns per part of the statistics: one tile
+
+struct LossPlan {
+    int parts;
+    size_t target_at, row_loss_at, bytes;
+};
+
+LossPlan loss_plan(const loss_args& a) {
+    LossPlan g{};
+    g.parts = ceil_div(a.vocab, kLossPart);
+    g.target_at = align256((size_t)g.parts * a.tokens * sizeof(float2));
+    g.row_loss_at = g.target_at + align256((size_t)a.tokens * 4);
+    g.bytes = g.row_loss_at + align256((size_t)a.tokens * 4);
+    return g;
+}
+
+// Backward: weights and the unscale factor, d of one piece, dh's running sum.
+struct LossGradPlan {
+    long long piece;
+    size_t unscale_at, d_at, sum_at, bytes;
+};
+
+LossGradPlan loss_grad_plan(const loss_grad_args& a, long long piece) {
+    LossGradPlan g{};
+    g.piece = piece < a.vocab ? piece : a.vocab;
+    g.unscale_at = align256((size_t)a.tokens * 4);
+    g.d_at = g.unscale_at + 256;
+    g.sum_at = g.d_at + align256((size_t)a.tokens * pad8(g.piece) * 2);
+    g.bytes = g.sum_at + (g.piece < a.vocab && a.dh ? align256((size_t)a.tokens * ((a.dim + 3) & ~3ll) * 4) : 0);
+    return g;
+}
+
+int check_loss_grad(const loss_grad_args& a) {
+    const int rc = check_dtype_act(a.dtype, 0);
+    if (rc != GEMM_OK) return rc;
+    if (a.reduction < LAYER_LOSS_NONE || a.reduction > LAYER_LOSS_SUM) return GEMM_ERR_CONFIG;
+    if (!dims_ok({a.dim, a.vocab}, a.tokens)) return GEMM_ERR_DIM;
+    return GEMM_OK;
+}
+
+// ---- gradient clipping -----------------------------------------------------------------------
+
+constexpr int kClipBig = 1000;     // tensors a launch takes; the small table travels faster
+constexpr int kClipSmall = 48;
+constexpr int kClipBlocksPerSm = 8;
+constexpr int kClipMaxBlocks = 256 * kClipBlocksPerSm;  // partial sums per launch
+
+template <int CAP>
+int run_clip(const grad_clip_args& a, const Ctx& c) {
+    double* partial = static_cast<double*>(a.workspace);
+    static_assert(sizeof(ClipTable<kClipBig>) < 32000, "kernel parameters");
+    const int max_blocks = c.dev->sms * kClipBlocksPerSm < kClipMaxBlocks ? c.dev->sms * kClipBlocksPerSm : kClipMaxBlocks;
+    int parts = 0;
+    ClipTable<CAP> t;
+    // both passes cut the tensors into the same tables, so `parts` ends alike
+    for (int pass = 0; pass < 2; ++pass) {
+        const int all_parts = parts;
+        long long i = 0;
+        int launches = 0;
+        while (i < a.tensors || (launches == 0)) {
+            t.tensors = 0;
+            t.chunks = 0;
+            while (i < a.tensors && t.tensors < CAP) {
+                const long long n = a.count[i];
+                if (n > 0) {
+                    const long long ch = (n + kClipChunk - 1) / kClipChunk;
+                    if (t.chunks + ch > INT_MAX / 2) {
+                        if (t.tensors == 0) return GEMM_ERR_DIM;
+                        break;
+                    }
+                    t.first[t.tensors] = t.chunks;
+                    t.e[t.tensors] = ClipEntry{a.src[i], a.dst[i], n * 4 + a.dtype[i]};
+                    t.chunks += (int)ch;
+                    ++t.tensors;
+                }
+                ++i;
+            }
+            ++launches;
+            const int blocks = t.chunks < 1 ? 1 : t.chunks < max_blocks ? t.chunks : max_blocks;
+            int rc;
+            if (pass == 0) {
+                rc = launch_pdl(clip_norm_kernel<CAP>, dim3(blocks), kClipThreads, 0, 1, c.stream, t, partial + parts);
+                parts += blocks;
+            } else {
+                rc = launch_pdl(clip_scale_kernel<CAP>, dim3(blocks), kClipThreads, 0, 1, c.stream, t,
+                                (const double*)partial, all_parts, a.max_norm, a.eps, launches == 1 ? a.norm : nullptr);
+            }
+            if (rc != GEMM_OK) return rc;
+        }
+    }
+    return GEMM_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int linear_forward(const linear_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const linear_args& a = *args;
+    int rc = check_dtype_act(a.dtype, a.act);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({a.k, a.n}, a.tokens)) return GEMM_ERR_DIM;
+    if (a.tokens == 0) return GEMM_OK;
+    const Mat x = mat16(a.x, a.tokens, a.k, a.ldx), w = mat16(a.w, a.k, a.n, a.ldw);
+    const Mat y = mat16(a.y, a.tokens, a.n, a.ldy);
+    const Mat r = mat16(a.residual, a.tokens, a.n, a.ldr), pre = mat16(a.preact, a.tokens, a.n, a.ldp);
+    if ((rc = check_all({x, w, y})) != GEMM_OK) return rc;
+    if (r.p && (rc = check_mat(r)) != GEMM_OK) return rc;
+    if (pre.p && (rc = check_mat(pre)) != GEMM_OK) return rc;
+    if ((uintptr_t)a.bias & 1) return GEMM_ERR_ALIGN;
+    const bool in_place = r.p == y.p && a.ldr == a.ldy;
+    const Span wr[] = {span_of(y), span_of(pre)};
+    const Span rd[] = {span_of(x), span_of(w), span_of(a.bias, (uint64_t)a.n * 2), in_place ? Span{0, 0} : span_of(r)};
+    if (overlaps(wr, 2, rd, 4)) return GEMM_ERR_ALIAS;
+    if (in_place && r.p) {
+        const Span p2[] = {span_of(pre)}, r2[] = {span_of(r)};
+        if (overlaps(p2, 1, r2, 1)) return GEMM_ERR_ALIAS;
+    }
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    Product q;
+    q.a = x;
+    q.b = w;
+    q.M = a.tokens;
+    q.N = a.n;
+    q.K = a.k;
+    q.out[0] = y;
+    if (pre.p) {
+        q.out[1] = pre;
+        q.outs = 2;
+        q.p.keep = 1;
+    }
+    if (r.p) {
+        q.in[0] = r;
+        q.ins = 1;
+        q.p.addend = 1;
+    }
+    q.p.bias = a.bias;
+    q.p.act = (int)a.act;
+    return run_product<kNN, kEpiStore>(q, (int)a.dtype, c);
+}
+
+int linear_backward_workspace(const linear_grad_args* args, size_t* bytes) {
+    if (!args || !bytes) return GEMM_ERR_NULL;
+    const int rc = check_dtype_act(args->dtype, args->act);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({args->k, args->n}, args->tokens)) return GEMM_ERR_DIM;
+    *bytes = linear_grad_plan(*args).bytes;
+    return GEMM_OK;
+}
+
+int linear_backward(const linear_grad_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const linear_grad_args& a = *args;
+    int rc = check_dtype_act(a.dtype, a.act);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({a.k, a.n}, a.tokens)) return GEMM_ERR_DIM;
+    const Mat dy = mat16(a.dy, a.tokens, a.n, a.lddy), x = mat16(a.x, a.tokens, a.k, a.ldx);
+    const Mat w = mat16(a.w, a.k, a.n, a.ldw), pre = mat16(a.preact, a.tokens, a.n, a.ldp);
+    const Mat dx = mat16(a.dx, a.tokens, a.k, a.lddx), dw = mat16(a.dw, a.k, a.n, a.lddw);
+    if ((rc = check_mat(dy)) != GEMM_OK) return rc;
+    if (a.act != LAYER_ACT_NONE && (rc = check_mat(pre)) != GEMM_OK) return rc;
+    if (a.dx && ((rc = check_all({w, dx})) != GEMM_OK)) return rc;
+    if (a.dw && ((rc = check_all({x, dw})) != GEMM_OK)) return rc;
+    if ((uintptr_t)a.dbias & 1) return GEMM_ERR_ALIGN;
+    const LinearGradPlan g = linear_grad_plan(a);
+    if ((long long)g.row_blocks * ceil_div(a.n, kSlopeCols) > INT_MAX) return GEMM_ERR_DIM;
+    if (a.tokens > 0 && (rc = check_workspace(a.workspace, a.workspace_bytes, g.bytes)) != GEMM_OK) return rc;
+    const Span wr[] = {span_of(dx), span_of(dw), span_of(a.dbias, (uint64_t)a.n * 2),
+                       span_of(g.bytes ? a.workspace : nullptr, g.bytes)};
+    const Span rd[] = {span_of(dy), a.dw ? span_of(x) : Span{0, 0}, a.dx ? span_of(w) : Span{0, 0},
+                       a.act != LAYER_ACT_NONE ? span_of(pre) : Span{0, 0}};
+    if (overlaps(wr, 4, rd, 4)) return GEMM_ERR_ALIAS;
+    if (!a.dx && !a.dw && !a.dbias) return GEMM_OK;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    if (a.tokens == 0) {
+        if ((rc = zero_mat(dw, c)) != GEMM_OK) return rc;
+        return a.dbias ? zero_mat(Mat{a.dbias, 1, a.n, a.n, 2}, c) : GEMM_OK;
+    }
+    char* ws = static_cast<char*>(a.workspace);
+    Mat dpre = dy;
+    if (g.slope) dpre = mat16(ws, a.tokens, a.n, pad8(a.n));
+    if (g.slope || g.sums) {
+        SlopeParams sp{};
+        sp.dy = a.dy;
+        sp.ld_dy = a.lddy;
+        sp.pre = a.act != LAYER_ACT_NONE ? a.preact : nullptr;
+        sp.ld_pre = a.ldp;
+        sp.dpre = g.slope ? ws : nullptr;
+        sp.ld_dpre = dpre.ld;
+        sp.partial = g.sums ? reinterpret_cast<float*>(ws + g.partial_at) : nullptr;
+        sp.rows = (int)a.tokens;
+        sp.cols = (int)a.n;
+        sp.act = (int)a.act;
+        sp.col_blocks = ceil_div(a.n, kSlopeCols);
+        rc = a.dtype == LAYER_BF16 ? run_slope<kBF16>(sp, a.dbias, g.row_blocks, c)
+                                   : run_slope<kF16>(sp, a.dbias, g.row_blocks, c);
+        if (rc != GEMM_OK) return rc;
+    }
+    if (a.dx) {
+        Product q;
+        q.a = dpre;
+        q.b = w;
+        q.M = a.tokens;
+        q.N = a.k;
+        q.K = a.n;
+        q.out[0] = dx;
+        if ((rc = run_product<kNT, kEpiStore>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
+    }
+    if (a.dw) {
+        Product q;
+        q.a = x;
+        q.b = dpre;
+        q.M = a.k;
+        q.N = a.n;
+        q.K = a.tokens;
+        q.out[0] = dw;
+        if ((rc = run_product<kTN, kEpiStore>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
+    }
+    return GEMM_OK;
+}
+
+int gated_ffn_forward(const gated_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const gated_args& a = *args;
+    int rc = check_dtype_act(a.dtype, a.act);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({a.dim, a.ffn, a.dim_out}, a.tokens)) return GEMM_ERR_DIM;
+    if (!a.gate != !a.up) return GEMM_ERR_NULL;
+    if (a.tokens == 0) return GEMM_OK;
+    const Mat x = mat16(a.x, a.tokens, a.dim, a.ldx);
+    const Mat wg = mat16(a.w_gate, a.dim, a.ffn, a.ldw_gate), wu = mat16(a.w_up, a.dim, a.ffn, a.ldw_up);
+    const Mat wd = mat16(a.w_down, a.ffn, a.dim_out, a.ldw_down);
+    const Mat y = mat16(a.y, a.tokens, a.dim_out, a.ldy), r = mat16(a.residual, a.tokens, a.dim_out, a.ldr);
+    const Mat h = mat16(a.hidden, a.tokens, a.ffn, a.ld_hidden);
+    const Mat g = mat16(a.gate, a.tokens, a.ffn, a.ld_gate), u = mat16(a.up, a.tokens, a.ffn, a.ld_up);
+    if ((rc = check_all({x, wg, wu, wd, y, h})) != GEMM_OK) return rc;
+    if (r.p && (rc = check_mat(r)) != GEMM_OK) return rc;
+    if (g.p && (rc = check_all({g, u})) != GEMM_OK) return rc;
+    const bool in_place = r.p == y.p && a.ldr == a.ldy;
+    const Span wr[] = {span_of(y), span_of(h), span_of(g), span_of(u)};
+    const Span rd[] = {span_of(x), span_of(wg), span_of(wu), span_of(wd), in_place ? Span{0, 0} : span_of(r)};
+    if (overlaps(wr, 4, rd, 5)) return GEMM_ERR_ALIAS;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    Product q;
+    q.a = x;
+    q.b = wg;
+    q.b2 = wu;
+    q.M = a.tokens;
+    q.N = a.ffn;
+    q.K = a.dim;
+    q.out[0] = h;
+    if (g.p) {
+        q.out[1] = g;
+        q.out[2] = u;
+        q.outs = 3;
+        q.p.keep = 1;
+    }
+    q.p.act = (int)a.act;
+    if ((rc = run_product<kNN, kEpiGate>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
+    Product d;
+    d.a = h;
+    d.b = wd;
+    d.M = a.tokens;
+    d.N = a.dim_out;
+    d.K = a.ffn;
+    d.out[0] = y;
+    if (r.p) {
+        d.in[0] = r;
+        d.ins = 1;
+        d.p.addend = 1;
+    }
+    return run_product<kNN, kEpiStore>(d, (int)a.dtype, c);
+}
+
+int gated_ffn_backward_workspace(const gated_grad_args* args, size_t* bytes) {
+    if (!args || !bytes) return GEMM_ERR_NULL;
+    const int rc = check_dtype_act(args->dtype, args->act);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({args->dim, args->ffn, args->dim_out}, args->tokens)) return GEMM_ERR_DIM;
+    *bytes = args->dx || args->dw_gate || args->dw_up ? 2 * align256((size_t)args->tokens * pad8(args->ffn) * 2) : 0;
+    return GEMM_OK;
+}
+
+int gated_ffn_backward(const gated_grad_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const gated_grad_args& a = *args;
+    size_t need = 0;
+    int rc = gated_ffn_backward_workspace(args, &need);
+    if (rc != GEMM_OK) return rc;
+    if (!a.dw_gate != !a.dw_up) return GEMM_ERR_NULL;
+    const long long T = a.tokens;
+    const Mat dy = mat16(a.dy, T, a.dim_out, a.lddy), x = mat16(a.x, T, a.dim, a.ldx);
+    const Mat wg = mat16(a.w_gate, a.dim, a.ffn, a.ldw_gate), wu = mat16(a.w_up, a.dim, a.ffn, a.ldw_up);
+    const Mat wd = mat16(a.w_down, a.ffn, a.dim_out, a.ldw_down);
+    const Mat gt = mat16(a.gate, T, a.ffn, a.ld_gate), up = mat16(a.up, T, a.ffn, a.ld_up);
+    const Mat hid = mat16(a.hidden, T, a.ffn, a.ld_hidden);
+    const Mat dx = mat16(a.dx, T, a.dim, a.lddx);
+    const Mat dwg = mat16(a.dw_gate, a.dim, a.ffn, a.lddw_gate), dwu = mat16(a.dw_up, a.dim, a.ffn, a.lddw_up);
+    const Mat dwd = mat16(a.dw_down, a.ffn, a.dim_out, a.lddw_down);
+    const bool inner = a.dx || a.dw_gate;  // dgate and dup are needed
+    if (!inner && !a.dw_down) return GEMM_OK;
+    if ((rc = check_mat(dy)) != GEMM_OK) return rc;
+    if (inner && (rc = check_all({wd, gt, up})) != GEMM_OK) return rc;
+    if (a.dx && (rc = check_all({wg, wu, dx})) != GEMM_OK) return rc;
+    if (a.dw_gate && (rc = check_all({x, dwg, dwu})) != GEMM_OK) return rc;
+    if (a.dw_down && (rc = check_all({hid, dwd})) != GEMM_OK) return rc;
+    if (T > 0 && (rc = check_workspace(a.workspace, a.workspace_bytes, need)) != GEMM_OK) return rc;
+    const Span none{0, 0};
+    const Span wr[] = {span_of(dx), span_of(dwg), span_of(dwu), span_of(dwd), span_of(need ? a.workspace : nullptr, need)};
+    const Span rd[] = {span_of(dy), a.dw_gate ? span_of(x) : none, a.dx ? span_of(wg) : none, a.dx ? span_of(wu) : none,
+                       inner ? span_of(wd) : none, inner ? span_of(gt) : none, inner ? span_of(up) : none,
+                       a.dw_down ? span_of(hid) : none};
+    if (overlaps(wr, 5, rd, 8)) return GEMM_ERR_ALIAS;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    if (T == 0) {
+        for (const Mat& m : {dwg, dwu, dwd})
+            if ((rc = zero_mat(m, c)) != GEMM_OK) return rc;
+        return GEMM_OK;
+    }
+    char* ws = static_cast<char*>(a.workspace);
+    const Mat dg = mat16(ws, T, a.ffn, pad8(a.ffn)), du = mat16(ws + need / 2, T, a.ffn, pad8(a.ffn));
+    const int dtype = (int)a.dtype;
+    if (inner) {
+        Product q;
+        q.a = dy;
+        q.b = wd;
+        q.M = T;
+        q.N = a.ffn;
+        q.K = a.dim_out;
+        q.out[0] = dg;
+        q.out[1] = du;
+        q.outs = 2;
+        q.in[0] = gt;
+        q.in[1] = up;
+        q.ins = 2;
+        q.p.act = (int)a.act;
+        if ((rc = run_product<kNT, kEpiGateGrad>(q, dtype, c)) != GEMM_OK) return rc;
+    }
+    if (a.dx) {
+        Product q;
+        q.a = dg;
+        q.a2 = du;
+        q.b = wg;
+        q.b2 = wu;
+        q.M = T;
+        q.N = a.dim;
+        q.K = a.ffn;
+        q.out[0] = dx;
+        if ((rc = run_product<kNT, kEpiStore>(q, dtype, c)) != GEMM_OK) return rc;
+    }
+    auto weight_grad = [&](const Mat& in, const Mat& d, const Mat& out) {
+        Product q;
+        q.a = in;
+        q.b = d;
+        q.M = in.cols;
+        q.N = d.cols;
+        q.K = T;
+        q.out[0] = out;
+        return run_product<kTN, kEpiStore>(q, dtype, c);
+    };
+    if (a.dw_gate) {
+        if ((rc = weight_grad(x, dg, dwg)) != GEMM_OK) return rc;
+        if ((rc = weight_grad(x, du, dwu)) != GEMM_OK) return rc;
+    }
+    if (a.dw_down && (rc = weight_grad(hid, dy, dwd)) != GEMM_OK) return rc;
+    return GEMM_OK;
+}
+
+int linear_cross_entropy_workspace(const loss_args* args, size_t* bytes) {
+    if (!args || !bytes) return GEMM_ERR_NULL;
+    const int rc = check_dtype_act(args->dtype, 0);
+    if (rc != GEMM_OK) return rc;
+    if (args->reduction < LAYER_LOSS_NONE || args->reduction > LAYER_LOSS_SUM) return GEMM_ERR_CONFIG;
+    if (!dims_ok({args->dim, args->vocab}, args->tokens)) return GEMM_ERR_DIM;
+    *bytes = args->tokens > 0 ? loss_plan(*args).bytes : 0;
+    return GEMM_OK;
+}
+
+int linear_cross_entropy(const loss_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const loss_args& a = *args;
+    size_t need = 0;
+    int rc = linear_cross_entropy_workspace(args, &need);
+    if (rc != GEMM_OK) return rc;
+    const Mat h = mat16(a.h, a.tokens, a.dim, a.ldh), w = mat16(a.w, a.vocab, a.dim, a.ldw);
+    const bool each = a.reduction == LAYER_LOSS_NONE;
+    if (!a.loss && (a.tokens > 0 || !each)) return GEMM_ERR_NULL;
+    if ((uintptr_t)a.loss & 3) return GEMM_ERR_ALIGN;
+    if (a.tokens > 0) {
+        if (!a.target || !a.lse) return GEMM_ERR_NULL;
+        if (((uintptr_t)a.target & 7) || ((uintptr_t)a.lse & 3)) return GEMM_ERR_ALIGN;
+        if ((rc = check_all({h, w})) != GEMM_OK) return rc;
+        if ((rc = check_workspace(a.workspace, a.workspace_bytes, need)) != GEMM_OK) return rc;
+        const Span wr[] = {span_of(a.loss, (uint64_t)(each ? a.tokens : 1) * 4), span_of(a.lse, (uint64_t)a.tokens * 4),
+                           span_of(a.workspace, need)};
+        const Span rd[] = {span_of(h), span_of(w), span_of(a.target, (uint64_t)a.tokens * 8)};
+        if (overlaps(wr, 3, rd, 3)) return GEMM_ERR_ALIAS;
+    }
+    Ctx c;
+    if (a.tokens == 0 && each) return GEMM_OK;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    if (a.tokens == 0) return zero_mat(Mat{a.loss, 1, 1, 1, 4}, c);
+    const LossPlan g = loss_plan(a);
+    char* ws = static_cast<char*>(a.workspace);
+    Product q;
+    q.a = h;
+    q.b = w;
+    q.M = a.tokens;
+    q.N = a.vocab;
+    q.K = a.dim;
+    q.p.stats = reinterpret_cast<float2*>(ws);
+    q.p.target_logit = reinterpret_cast<float*>(ws + g.target_at);
+    q.p.target = a.target;
+    if ((rc = run_product<kNT, kEpiLossStats>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
+    LossParams lp{};
+    lp.stats = q.p.stats;
+    lp.target_logit = q.p.target_logit;
+    lp.target = a.target;
+    lp.row_loss = each ? a.loss : reinterpret_cast<float*>(ws + g.row_loss_at);
+    lp.lse = a.lse;
+    lp.rows = (int)a.tokens;
+    lp.parts = g.parts;
+    lp.vocab = a.vocab;
+    lp.ignore_index = a.ignore_index;
+    if ((rc = launch_pdl(layer_loss_rows_kernel, dim3(ceil_div(a.tokens, 32)), 256, 0, 1, c.stream, lp)) != GEMM_OK) return rc;
+    if (each) return GEMM_OK;
+    return launch_pdl(layer_loss_sum_kernel, dim3(1), 1024, 0, 1, c.stream, (const float*)lp.row_loss, a.target, a.loss,
+                      (int)a.tokens, a.ignore_index, (int)(a.reduction == LAYER_LOSS_MEAN));
+}
+
+int linear_cross_entropy_backward_workspace(const loss_grad_args* args, long long piece, size_t* bytes) {
+    if (!args || !bytes) return GEMM_ERR_NULL;
+    const int rc = check_loss_grad(*args);
+    if (rc != GEMM_OK) return rc;
+    if (piece < 256 || piece % 256 != 0) return GEMM_ERR_DIM;
+    *bytes = args->tokens > 0 ? loss_grad_plan(*args, piece).bytes : 0;
+    return GEMM_OK;
+}
+
+int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const loss_grad_args& a = *args;
+    int rc = check_loss_grad(a);
+    if (rc != GEMM_OK) return rc;
+    if (!a.dh && !a.dw) return GEMM_OK;
+    const long long T = a.tokens;
+    const Mat h = mat16(a.h, T, a.dim, a.ldh), w = mat16(a.w, a.vocab, a.dim, a.ldw);
+    const Mat dh = mat16(a.dh, T, a.dim, a.lddh), dw = mat16(a.dw, a.vocab, a.dim, a.lddw);
+    if (a.dw && (rc = check_mat(dw)) != GEMM_OK) return rc;
+    Ctx c;
+    if (T == 0) {
+        if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+        return zero_mat(dw, c);
+    }
+    if (a.dh && (rc = check_mat(dh)) != GEMM_OK) return rc;
+    if ((rc = check_all({h, w})) != GEMM_OK) return rc;
+    if (!a.target || !a.lse || !a.grad_loss) return GEMM_ERR_NULL;
+    if (((uintptr_t)a.target & 7) || ((uintptr_t)a.lse & 3) || ((uintptr_t)a.grad_loss & 3)) return GEMM_ERR_ALIGN;
+    // the largest piece the workspace holds: all of the vocabulary, else a multiple of 256
+    if (!a.workspace) return GEMM_ERR_NULL;
+    if ((uintptr_t)a.workspace & 255) return GEMM_ERR_ALIGN;
+    const size_t have = a.workspace_bytes < 0 ? 0 : (size_t)a.workspace_bytes;
+    long long piece = a.vocab;
+    if (loss_grad_plan(a, piece).bytes > have) {
+        const size_t fixed = loss_grad_plan(a, 256 < a.vocab ? 256 : a.vocab).bytes;
+        if (256 >= a.vocab || fixed > have) return GEMM_ERR_WORKSPACE;
+        piece = 256 + (long long)((have - fixed) / ((size_t)T * 2)) / 256 * 256;
+        if (piece >= a.vocab) piece = (a.vocab - 1) / 256 * 256;
+        while (piece > 256 && loss_grad_plan(a, piece).bytes > have) piece -= 256;
+    }
+    const LossGradPlan g = loss_grad_plan(a, piece);
+    const Span wr[] = {span_of(dh), span_of(dw), span_of(a.workspace, g.bytes)};
+    const Span rd[] = {span_of(h), span_of(w), span_of(a.target, (uint64_t)T * 8), span_of(a.lse, (uint64_t)T * 4),
+                       span_of(a.grad_loss, (uint64_t)(a.reduction == LAYER_LOSS_NONE ? T : 1) * 4)};
+    if (overlaps(wr, 3, rd, 5)) return GEMM_ERR_ALIAS;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    char* ws = static_cast<char*>(a.workspace);
+    float* weight = reinterpret_cast<float*>(ws);
+    float* unscale = reinterpret_cast<float*>(ws + g.unscale_at);
+    const int dtype = (int)a.dtype;
+    rc = launch_pdl(layer_loss_weights_kernel, dim3(1), 1024, 0, 1, c.stream, a.grad_loss, a.target, weight, unscale, (int)T,
+                    a.vocab, a.ignore_index, (int)a.reduction);
+    if (rc != GEMM_OK) return rc;
+    const long long ldsum = (a.dim + 3) & ~3ll;
+    for (long long v0 = 0; v0 < a.vocab; v0 += piece) {
+        const long long n = a.vocab - v0 < piece ? a.vocab - v0 : piece;
+        const bool first = v0 == 0, last = v0 + n == a.vocab;
+        const Mat d = mat16(ws + g.d_at, T, n, pad8(g.piece));
+        const Mat wp = mat16(static_cast<const char*>(a.w) + (size_t)v0 * a.ldw * 2, n, a.dim, a.ldw);
+        Product q;
+        q.a = h;
+        q.b = wp;
+        q.M = T;
+        q.N = n;
+        q.K = a.dim;
+        q.out[0] = d;
+        q.p.target = a.target;
+        q.p.col0 = (int)v0;
+        q.p.lse = a.lse;
+        q.p.row_scale = weight;
+        if ((rc = run_product<kNT, kEpiLossGrad>(q, dtype, c)) != GEMM_OK) return rc;
+        if (a.dh) {
+            // dh = d w, over the pieces in fp32; the last sum is unscaled and rounded
+            const Mat sum = Mat{ws + g.sum_at, T, a.dim, ldsum, 4};
+            Product s;
+            s.a = d;
+            s.b = wp;
+            s.M = T;
+            s.N = a.dim;
+            s.K = n;
+            s.p.alpha = unscale;
+            s.out[0] = last ? dh : sum;
+            if (!first) {
+                s.in[0] = sum;
+                s.ins = 1;
+                s.p.addend = last ? 2 : 1;
+            }
+            rc = last ? run_product<kNN, kEpiStore>(s, dtype, c) : run_product<kNN, kEpiStoreF32>(s, dtype, c);
+            if (rc != GEMM_OK) return rc;
+        }
+        if (a.dw) {
+            Product s;
+            s.a = d;
+            s.b = h;
+            s.M = n;
+            s.N = a.dim;
+            s.K = T;
+            s.p.alpha = unscale;
+            s.out[0] = mat16(static_cast<char*>(a.dw) + (size_t)v0 * a.lddw * 2, n, a.dim, a.lddw);
+            if ((rc = run_product<kTN, kEpiStore>(s, dtype, c)) != GEMM_OK) return rc;
+        }
+    }
+    return GEMM_OK;
+}
+
+int grad_clip_workspace(long long tensors, size_t* bytes) {
+    if (!bytes) return GEMM_ERR_NULL;
+    if (tensors < 0 || tensors > (1ll << 40)) return GEMM_ERR_DIM;
+    const size_t launches = tensors <= kClipSmall ? 1 : (size_t)((tensors + kClipBig - 1) / kClipBig);
+    *bytes = launches * kClipMaxBlocks * sizeof(double);
+    return GEMM_OK;
+}
+
+int grad_clip(const grad_clip_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const grad_clip_args& a = *args;
+    size_t need = 0;
+    int rc = grad_clip_workspace(a.tensors, &need);
+    if (rc != GEMM_OK) return rc;
+    if (!(a.max_norm >= 0) || !(a.eps >= 0)) return GEMM_ERR_CONFIG;
+    if (a.tensors > 0 && (!a.src || !a.dst || !a.count || !a.dtype)) return GEMM_ERR_NULL;
+    if ((uintptr_t)a.norm & 3) return GEMM_ERR_ALIGN;
+    long long chunks = 0;
+    for (long long i = 0; i < a.tensors; ++i) {
+        if (a.count[i] < 0 || a.count[i] > (1ll << 44)) return GEMM_ERR_DIM;
+        if (a.dtype[i] < LAYER_F16 || a.dtype[i] > LAYER_F32) return GEMM_ERR_DTYPE;
+        if (a.count[i] == 0) continue;
+        if (!a.src[i] || !a.dst[i]) return GEMM_ERR_NULL;
+        const int b = a.dtype[i] == LAYER_F32 ? 4 : 2;
+        if (((uintptr_t)a.src[i] | (uintptr_t)a.dst[i]) & (b - 1)) return GEMM_ERR_ALIGN;
+        if (a.src[i] != a.dst[i]) {
+            const Span s[] = {span_of(a.src[i], (uint64_t)a.count[i] * b)}, d[] = {span_of(a.dst[i], (uint64_t)a.count[i] * b)};
+            if (overlaps(d, 1, s, 1)) return GEMM_ERR_ALIAS;
+        }
+        chunks += (a.count[i] + kClipChunk - 1) / kClipChunk;
+        if (chunks > INT_MAX / 2) return GEMM_ERR_DIM;
+    }
+    if ((rc = check_workspace(a.workspace, a.workspace_bytes, need)) != GEMM_OK) return rc;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    return a.tensors <= kClipSmall ? run_clip<kClipSmall>(a, c) : run_clip<kClipBig>(a, c);
+}
+
+}  // extern "C"

@@ -1,0 +1,671 @@
+// The layer operators' matrix product on CTA pairs: D = A B on 256 x PN tiles
+// (tcgen05.mma.cta_group::2, M = 256), fp16 or bf16 operands, each in either
+// major order, fp32 accumulation in Tensor Memory, and the operator's own
+// elementwise work in the epilogue, on the fp32 accumulator.
+//
+//   layout  A              B               products
+//   NN      [M, K]         [K, N]          x w
+//   NT      [M, K]         [N, K]          dy w^T, h W^T (vocabulary rows)
+//   TN      [K, M]         [K, N]          x^T dy
+//
+//   epilogue        what it computes of the tile's values v
+//   kEpiStore       y = act(alpha v + bias) + addend; keeps alpha v + bias on request.
+//                   The addend is the residual, or the fp32 sum so far
+//   kEpiGate        the tile's first PN/2 columns come from w_gate, the others
+//                   from w_up (each CTA of the pair loads one of them), so a
+//                   thread holds both g and u of an element: h = act(g) u
+//   kEpiGateGrad    v = dh: dg = dh u act'(g), du = dh act(g), with g and u loaded
+//   kEpiLossStats   v = logits: per row and tile the maximum and the sum of
+//                   exp(v - maximum), and the target's logit; no logit is stored
+//   kEpiLossGrad    v = logits again: (exp(v - lse) - [column = target]) times the row's
+//                   weight, in 16 bits, operand of the two products that follow
+//
+// Two operand pairs may follow one another along K (dx = dg Wg^T + du Wu^T is
+// one product whose K is both halves): K steps from k_switch on read a[1], b[1].
+//
+// Bound by the tensor pipe at the sizes that matter: a 256 x 256 pair tile
+// reads 32 KiB of operands per SM per 64 of K, 512 cycles of MMA.  Persistent
+// pairs walk the tiles in the grouped raster of gemm_common.cuh; the TMEM
+// accumulator is double-buffered, so a tile's epilogue (arithmetic of 15 to 40
+// instructions an element on 4 warps) runs under the next tile's products.
+// What an epilogue reads and writes per tile moves by TMA through four 4 KiB
+// buffers per warp (in-place where it reads), leaving five 32 KiB stages.
+//
+// Roles as in gemm_pair_kernel.cuh: warp 0 loads, warp 1 issues MMAs (even CTA),
+// warps 2-5 drain; every wait is bounded and reports through the status word.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace tcgemm {
+
+enum LayerLayout { kNN = 0, kNT = 1, kTN = 2 };
+enum LayerEpilogue {
+    kEpiStore = 0,
+    kEpiStoreF32 = 1,
+    kEpiGate = 2,
+    kEpiGateGrad = 3,
+    kEpiLossStats = 4,
+    kEpiLossGrad = 5,
+};
+
+struct LayerMaps {
+    CUtensorMap a[2], b[2];
+    CUtensorMap out[3];
+    CUtensorMap in[2];
+};
+
+struct LayerParams {
+    int M, N;              // of the output (kEpiGate: N of h, half the product's)
+    int tiles_m, tiles_n;
+    int k_steps, k_switch; // 64-deep; steps >= k_switch read a[1], b[1] from their start
+    int raster_group;
+    int act;
+    int addend;            // kEpiStore*: 0 none, 1 of the output's type, 2 fp32 under a 16-bit output
+    int keep;              // kEpiStore: keep alpha v + bias in out[1]; kEpiGate: keep g and u in out[1], out[2]
+    const void* bias;      // N values of the operands' type, or NULL
+    const float* alpha;    // device scalar, or NULL for 1
+    float2* stats;         // kEpiLossStats: [tiles_n][M] (maximum, sum of exponentials)
+    float* target_logit;   // kEpiLossStats: [M], written where the target's column is met
+    const long long* target;  // kEpiLoss*: [M]
+    int col0;              // kEpiLossGrad: vocabulary index of the tile grid's first column
+    const float* lse;      // kEpiLossGrad: [M]
+    const float* row_scale;// kEpiLossGrad: [M], 0 for a row that takes no part
+    long long wait_limit;
+    int inject;
+};
+
+template <int EPI, int PN>
+struct LayerPairLayout {
+    static_assert(PN == 256 || PN == 128, "tile columns");
+    static constexpr int kABytes = 128 * 64 * 2;         // this CTA's 128 rows of one K step
+    static constexpr int kBBytes = (PN / 2) * 64 * 2;    // this CTA's PN/2 columns
+    static constexpr int kStageBytes = kABytes + kBBytes;
+    static constexpr int kBufs = EPI == kEpiLossStats ? 0 : 4;  // 4 KiB staging buffers per epilogue warp
+    static constexpr int kWarpStaging = kBufs * 4096;
+    // full[8], empty[8], tmem_full[2], tmem_empty[2], drain, aux[4 warps][2]
+    static constexpr int kNumBars = 2 * kMaxStages + 5 + 8;
+    static constexpr int kBiasBytes = 4 * 64 * 4;        // 64 fp32 per epilogue warp
+    static constexpr int kFixedBytes = 4 * kWarpStaging + kBiasBytes + ((kNumBars * 8 + 15) & ~15) + 16;
+    static constexpr int kLimit = 232448;
+    static constexpr int kFit = (kLimit - 1024 - kFixedBytes) / kStageBytes;
+    static constexpr int kSlots = kFit < kMaxStages ? kFit : kMaxStages;
+    static constexpr int kSmem = 1024 + kSlots * kStageBytes + kFixedBytes;
+    static constexpr int kTmemCols = 2 * PN;             // two accumulators
+    static constexpr int kOutN = EPI == kEpiGate ? PN / 2 : PN;      // output columns of a tile
+    static constexpr int kChunk = EPI == kEpiStoreF32 || EPI == kEpiLossStats ? 32 : 64;  // columns drained at a time
+};
+
+__device__ __forceinline__ void layer_tile_coords(int t, const LayerParams& p, int& mb, int& nb) {
+    const int g = p.raster_group;
+    const int per_group = g * p.tiles_n;
+    const int grp = t / per_group;
+    const int first_m = grp * g;
+    const int gm = min(p.tiles_m - first_m, g);
+    const int r = t - grp * per_group;
+    mb = first_m + r % gm;
+    nb = r / gm;
+    if (grp & 1) nb = p.tiles_n - 1 - nb;
+}
+
+// 16 bytes of this lane's row `lane` of a 32-row, 128-byte-swizzled buffer.
+__device__ __forceinline__ uint32_t swz(uint32_t buf, int lane, int piece) {
+    return buf + (uint32_t)(lane * 128) + ((uint32_t)(piece ^ (lane & 7)) << 4);
+}
+
+template <int LAY, int EPI, int DT, int PN>
+__global__ void __launch_bounds__(kThreads, 1)
+    layer_pair_kernel(const __grid_constant__ LayerMaps tm, const LayerParams p) {
+    using L = LayerPairLayout<EPI, PN>;
+    constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
+    constexpr int S = L::kSlots;
+    constexpr int kHalf = PN / 2;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t base = (raw + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - raw);
+    const uint32_t sA = base;
+    const uint32_t sB = sA + S * L::kABytes;
+    const uint32_t sC = sB + S * L::kBBytes;
+    const uint32_t sBias = sC + 4 * L::kWarpStaging;
+    const uint32_t bar0 = sBias + L::kBiasBytes;
+    const uint32_t misc = bar0 + ((L::kNumBars * 8 + 15) & ~15);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base_ptr + (misc - base));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(base_ptr + (misc - base) + 4);
+#ifdef TCGEMM_CHECK
+    if (misc + 16 > raw + ptx::dynamic_smem_size()) {
+        if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
+        return;
+    }
+#endif
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
+    const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
+    auto aux_bar = [&](int q, int set) { return bar0 + 8u * (2 * kMaxStages + 5 + 2 * q + set); };
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(tfull_bar(a), 1);
+            ptx::mbar_init(tempty_bar(a), 8);  // 4 epilogue warps in each CTA
+        }
+        ptx::mbar_init(drain_bar, 1);
+        for (int i = 0; i < 8; ++i) ptx::mbar_init(aux_bar(i >> 1, i & 1), 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        ptx::prefetch_tmap(&tm.a[0]);
+        ptx::prefetch_tmap(&tm.b[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr((const void*)tmem_slot), L::kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
+    ptx::tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const int cluster = blockIdx.x >> 1;
+    const int clusters = gridDim.x >> 1;
+    const int tiles = p.tiles_m * p.tiles_n;
+    const int KB = p.k_steps;
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        if (lane == 0 && p.inject == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+            bool ok = true;
+            // the previous kernel's writes of the operands are done from here on
+            ptx::grid_dependency_wait();
+            ptx::grid_launch_dependents();
+            for (int t = cluster; ok && t < tiles; t += clusters) {
+                int mb, nb;
+                layer_tile_coords(t, p, mb, nb);
+                const int m0 = mb * 256 + (int)rank * 128;
+                // kEpiGate: this CTA's columns are the tile's PN/2 of one weight
+                const int n0 = EPI == kEpiGate ? nb * kHalf : nb * PN + (int)rank * kHalf;
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb_local = full_bar(stage);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, 2 * L::kStageBytes);
+                    const uint32_t fb = ptx::mapa(fb_local, 0);
+                    const int second = kb >= p.k_switch;
+                    const int k0 = (second ? kb - p.k_switch : kb) * 64;
+                    const CUtensorMap* ta = &tm.a[second];
+                    const CUtensorMap* tb = &tm.b[EPI == kEpiGate ? (int)rank : second];
+                    const uint32_t a = sA + stage * L::kABytes, b = sB + stage * L::kBBytes;
+                    if constexpr (kAMN) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            ptx::tma_load_2d_pair(a + j * kBoxBytes, ta, fb, m0 + j * 64, k0);
+                    } else {
+                        ptx::tma_load_2d_pair(a, ta, fb, k0, m0);
+                    }
+                    if constexpr (kBMN) {
+#pragma unroll
+                        for (int j = 0; j < kHalf / 64; ++j)
+                            ptx::tma_load_2d_pair(b + j * kBoxBytes, tb, fb, n0 + j * 64, k0);
+                    } else {
+                        ptx::tma_load_2d_pair(b, tb, fb, k0, n0);
+                    }
+                    issued_mask |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // both CTAs' bytes land before shared memory goes away
+            if (rank == 0)
+                for (int s = 0; s < S; ++s)
+                    if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader only) ----------------
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = layer_idesc(DT, kAMN, kBMN, 256, PN);
+            int stage = 0;
+            uint32_t phase = 0;
+            int tl = 0;
+            bool ok = true;
+            for (int t = cluster; ok && t < tiles; t += clusters) {
+                const int acc = tl & 1;
+                const uint32_t aph = (tl >> 1) & 1;
+                ++tl;
+                if (!wait_bounded<true>(tempty_bar(acc), aph ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
+                for (int kb = 0; kb < KB; ++kb) {
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint64_t ad0 = operand_desc<kAMN>(sA + stage * L::kABytes);
+                    const uint64_t bd0 = operand_desc<kBMN>(sB + stage * L::kBBytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_f16_ss_pair(d_tmem, ad0 + k * kSliceStep<kAMN>, bd0 + k * kSliceStep<kBMN>, idesc,
+                                             (kb | k) != 0);
+                    ptx::mma_commit_pair_multicast(empty_bar(stage), 0x3);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit_pair_multicast(tfull_bar(acc), 0x3);
+            }
+            ptx::mma_commit_pair(drain_bar);
+            wait_drain(drain_bar, 0, p.wait_limit);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs): own 128 rows x PN columns ----------------
+        const int q = warp & 3;
+        const uint32_t stg = sC + (uint32_t)(q * L::kWarpStaging);
+        const uint32_t sbias = sBias + (uint32_t)(q * 256);
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
+        // the previous kernel's reads and writes of what this one touches are done from here on
+        ptx::grid_dependency_wait();
+        ptx::grid_launch_dependents();
+        constexpr bool kLoads = EPI == kEpiStore || EPI == kEpiStoreF32 || EPI == kEpiGateGrad;
+        const bool loads = kLoads && (EPI == kEpiGateGrad || p.addend != 0);
+        float alpha = 1.0f;
+        if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32)
+            if (p.alpha != nullptr) alpha = *p.alpha;
+
+        // chunks [0, n) of the tile hold columns below N; rows from M on are no one's
+        auto chunks_of = [&](int nb) {
+            const int left = p.N - nb * L::kOutN;
+            return min(L::kOutN / L::kChunk, (left + L::kChunk - 1) / L::kChunk);
+        };
+        // the loads of one chunk (lane 0): into the chunk's set of two buffers
+        auto issue_loads = [&](int row0, int x, int set) {
+            const uint32_t bar = aux_bar(q, set), buf = stg + (uint32_t)(set * 8192);
+            if constexpr (EPI == kEpiGateGrad) {
+                ptx::mbar_arrive_expect_tx(bar, 8192);
+                ptx::tma_load_2d(buf, &tm.in[0], bar, x, row0);
+                ptx::tma_load_2d(buf + 4096, &tm.in[1], bar, x, row0);
+            } else if (EPI == kEpiStore && p.addend == 2) {
+                ptx::mbar_arrive_expect_tx(bar, 8192);
+                ptx::tma_load_2d(buf, &tm.in[0], bar, x, row0);
+                ptx::tma_load_2d(buf + 4096, &tm.in[0], bar, x + 32, row0);
+            } else {
+                ptx::mbar_arrive_expect_tx(bar, 4096);
+                ptx::tma_load_2d(buf, &tm.in[0], bar, x, row0);
+            }
+        };
+        unsigned n_chunk = 0;           // chunks this warp has drained: set = n_chunk & 1, phase = n_chunk >> 1
+        bool pending = false;           // loads of chunk n_chunk are under way
+        int tl = 0;
+        for (int t = cluster; t < tiles; t += clusters) {
+            int mb, nb;
+            layer_tile_coords(t, p, mb, nb);
+            const int acc = tl & 1;
+            const uint32_t aph = (tl >> 1) & 1;
+            ++tl;
+            const int row0 = mb * 256 + (int)rank * 128 + q * 32;
+            const int row = row0 + lane;
+            const int n0 = nb * L::kOutN;
+            const bool rows_here = row0 < p.M;
+            const int nch = rows_here ? chunks_of(nb) : 0;
+            const bool last_tile = t + clusters >= tiles;
+            if constexpr (kLoads) {
+                if (loads && rows_here && !pending) {
+                    if (lane == 0) {
+                        ptx::bulk_wait_group_read<0>();
+                        issue_loads(row0, n0, n_chunk & 1);
+                    }
+                    pending = true;
+                }
+            }
+            // per-row values of the loss epilogues
+            float lse = 0.0f, scale = 0.0f, best = -INFINITY, sum = 0.0f;
+            int tcol = -1;  // the target's column, relative to the tile grid
+            if constexpr (EPI == kEpiLossStats || EPI == kEpiLossGrad) {
+                if (row < p.M) {
+                    const long long tg = p.target[row];
+                    if (tg >= p.col0 && tg - p.col0 < p.N) tcol = (int)(tg - p.col0);
+                    if constexpr (EPI == kEpiLossGrad) {
+                        lse = p.lse[row];
+                        scale = p.row_scale[row];
+                    }
+                }
+            }
+            if (!warp_wait(tfull_bar(acc), aph, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
+            ptx::tc_fence_after();
+            const uint32_t trow = lane_base + (uint32_t)(acc * PN);
+            auto hand_back = [&]() {
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && !last_tile) ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), 0));
+            };
+            if (nch == 0) hand_back();
+            bool failed = false;
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c) {
+                const int x = n0 + c * L::kChunk;
+                const int set = n_chunk & 1;
+                const uint32_t buf0 = stg + (uint32_t)(set * 8192), buf1 = buf0 + 4096;
+                if constexpr (EPI == kEpiLossStats) {
+                    __syncwarp();  // the lanes part where one of them meets its target
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
+                    ptx::tmem_ld_wait();
+                    if (c == nch - 1) hand_back();
+                    if (p.N - x < 32) {  // columns from N on are no words
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i >= p.N - x) v[i] = 0xFF800000u;  // -inf
+                    }
+                    float m = best;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(v[i]));
+                    sum *= best == m ? 1.0f : exp2f((best - m) * 1.4426950408889634f);
+                    // the difference before the factor: a maximum near the type's lowest times log2(e)
+                    // would overflow.  (While all is -inf the terms are exp(-inf - 0) = 0.)
+                    const float mf = m == -INFINITY ? 0.0f : m;
+                    float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        s0 += exp2f((__uint_as_float(v[i]) - mf) * 1.4426950408889634f);
+                        s1 += exp2f((__uint_as_float(v[i + 1]) - mf) * 1.4426950408889634f);
+                    }
+                    sum += s0 + s1;
+                    best = m;
+                    const int rel = tcol - x;
+                    if (rel >= 0 && rel < 32) {
+                        float tv = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i == rel) tv = __uint_as_float(v[i]);
+                        p.target_logit[row] = tv;
+                    }
+                } else {
+                    if constexpr (kLoads) {
+                        if (loads) {
+                            if (!warp_wait(aux_bar(q, set), (n_chunk >> 1) & 1, abort_flag, p.wait_limit, kSiteAuxLoad,
+                                           lane)) {
+                                failed = true;
+                                break;
+                            }
+                            pending = false;
+                        }
+                    }
+                    // without loads: the stores issued from these buffers two chunks ago (kEpiGate
+                    // that keeps g and u: one chunk ago) have read them
+                    if (!loads) {
+                        if (lane == 0) {
+                            if (EPI == kEpiGate && p.keep)
+                                ptx::bulk_wait_group_read<0>();
+                            else
+                                ptx::bulk_wait_group_read<1>();
+                        }
+                        __syncwarp();
+                    }
+                    if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32) {
+                        constexpr int C = L::kChunk;
+                        if (p.bias != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < C / 32; ++i) {
+                                const int col = x + i * 32 + lane;
+                                st_shared_f32(sbias + (uint32_t)((i * 32 + lane) * 4),
+                                              col < p.N ? load1<DT>(p.bias, col) : 0.0f);
+                            }
+                            __syncwarp();
+                        }
+                        uint32_t v[C];
+                        ptx::tmem_ld_32x32b_x32(trow + c * C, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                        if constexpr (C == 64)
+                            ptx::tmem_ld_32x32b_x32(trow + c * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[C - 32]));
+                        ptx::tmem_ld_wait();
+                        if (c == nch - 1) hand_back();
+                        float f[C];
+#pragma unroll
+                        for (int i = 0; i < C; ++i) f[i] = __uint_as_float(v[i]) * alpha;
+                        if (p.bias != nullptr) {
+#pragma unroll
+                            for (int i = 0; i < C; i += 4) {
+                                float b0, b1, b2, b3;
+                                ld_shared_f4(sbias + (uint32_t)(i * 4), b0, b1, b2, b3);
+                                f[i] += b0;
+                                f[i + 1] += b1;
+                                f[i + 2] += b2;
+                                f[i + 3] += b3;
+                            }
+                        }
+                        if constexpr (EPI == kEpiStore) {
+                            if (p.keep) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j)
+                                    ptx::st_shared_v4(swz(buf1, lane, j), pack2<DT>(f[8 * j], f[8 * j + 1]),
+                                                      pack2<DT>(f[8 * j + 2], f[8 * j + 3]),
+                                                      pack2<DT>(f[8 * j + 4], f[8 * j + 5]),
+                                                      pack2<DT>(f[8 * j + 6], f[8 * j + 7]));
+                            }
+                            if (p.act != kActNone)
+                                with_act(p.act, [&](auto tag) {
+                                constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+                                    for (int i = 0; i < C; ++i) f[i] = act_value<ACT>(f[i]);
+                                });
+                            if (p.addend == 1) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    uint32_t w[4];
+                                    ptx::ld_shared_v4(swz(buf0, lane, j), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 r = unpack2<DT>(w[e]);
+                                        f[8 * j + 2 * e] += r.x;
+                                        f[8 * j + 2 * e + 1] += r.y;
+                                    }
+                                }
+                            } else if (p.addend == 2) {
+                                // both buffers are read before the first is written
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    float r0, r1, r2, r3;
+                                    ld_shared_f4(swz(j < 8 ? buf0 : buf1, lane, j & 7), r0, r1, r2, r3);
+                                    f[4 * j] += r0;
+                                    f[4 * j + 1] += r1;
+                                    f[4 * j + 2] += r2;
+                                    f[4 * j + 3] += r3;
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                ptx::st_shared_v4(swz(buf0, lane, j), pack2<DT>(f[8 * j], f[8 * j + 1]),
+                                                  pack2<DT>(f[8 * j + 2], f[8 * j + 3]),
+                                                  pack2<DT>(f[8 * j + 4], f[8 * j + 5]),
+                                                  pack2<DT>(f[8 * j + 6], f[8 * j + 7]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                if (p.addend != 0) {
+                                    float r0, r1, r2, r3;
+                                    ld_shared_f4(swz(buf0, lane, j), r0, r1, r2, r3);
+                                    f[4 * j] += r0;
+                                    f[4 * j + 1] += r1;
+                                    f[4 * j + 2] += r2;
+                                    f[4 * j + 3] += r3;
+                                }
+                                ptx::st_shared_v4(swz(buf0, lane, j), __float_as_uint(f[4 * j]),
+                                                  __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                                                  __float_as_uint(f[4 * j + 3]));
+                            }
+                        }
+                    } else if constexpr (EPI == kEpiGate) {
+                        const uint32_t hbuf = p.keep ? stg : stg + (uint32_t)((n_chunk & 1) * 4096);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t g[32], u[32];
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, g);
+                            ptx::tmem_ld_32x32b_x32(trow + kHalf + c * 64 + half * 32, u);
+                            ptx::tmem_ld_wait();
+                            if (c == nch - 1 && half == 1) hand_back();
+                            if (p.keep) {
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    auto at = [&](const uint32_t(&r)[32], int i) { return __uint_as_float(r[8 * j + i]); };
+                                    ptx::st_shared_v4(swz(stg + 4096, lane, half * 4 + j), pack2<DT>(at(g, 0), at(g, 1)),
+                                                      pack2<DT>(at(g, 2), at(g, 3)), pack2<DT>(at(g, 4), at(g, 5)),
+                                                      pack2<DT>(at(g, 6), at(g, 7)));
+                                    ptx::st_shared_v4(swz(stg + 8192, lane, half * 4 + j), pack2<DT>(at(u, 0), at(u, 1)),
+                                                      pack2<DT>(at(u, 2), at(u, 3)), pack2<DT>(at(u, 4), at(u, 5)),
+                                                      pack2<DT>(at(u, 6), at(u, 7)));
+                                }
+                            }
+                            float h[32];
+                            with_act(p.act, [&](auto tag) {
+                                constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    h[i] = act_value<ACT>(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+                            });
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ptx::st_shared_v4(swz(hbuf, lane, half * 4 + j), pack2<DT>(h[8 * j], h[8 * j + 1]),
+                                                  pack2<DT>(h[8 * j + 2], h[8 * j + 3]),
+                                                  pack2<DT>(h[8 * j + 4], h[8 * j + 5]),
+                                                  pack2<DT>(h[8 * j + 6], h[8 * j + 7]));
+                        }
+                    } else if constexpr (EPI == kEpiGateGrad) {
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, v);
+                            ptx::tmem_ld_wait();
+                            if (c == nch - 1 && half == 1) hand_back();
+                            with_act(p.act, [&](auto tag) {
+                                constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    // this lane's row of g and u, replaced by dg and du
+                                    uint32_t g[4], u[4];
+                                    const uint32_t ag = swz(buf0, lane, half * 4 + j), au = ag + 4096;
+                                    ptx::ld_shared_v4(ag, g[0], g[1], g[2], g[3]);
+                                    ptx::ld_shared_v4(au, u[0], u[1], u[2], u[3]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const float2 gf = unpack2<DT>(g[e]), uf = unpack2<DT>(u[e]);
+                                        const float d0 = __uint_as_float(v[8 * j + 2 * e]);
+                                        const float d1 = __uint_as_float(v[8 * j + 2 * e + 1]);
+                                        g[e] = pack2<DT>(d0 * uf.x * act_slope<ACT>(gf.x), d1 * uf.y * act_slope<ACT>(gf.y));
+                                        u[e] = pack2<DT>(d0 * act_value<ACT>(gf.x), d1 * act_value<ACT>(gf.y));
+                                    }
+                                    ptx::st_shared_v4(ag, g[0], g[1], g[2], g[3]);
+                                    ptx::st_shared_v4(au, u[0], u[1], u[2], u[3]);
+                                }
+                            });
+                        }
+                    } else {  // kEpiLossGrad
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, v);
+                            ptx::tmem_ld_wait();
+                            if (c == nch - 1 && half == 1) hand_back();
+                            const int rel = tcol - x - half * 32;
+                            float f[32];
+                            // a row of weight 0 is 0 whatever its logits hold
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                float e = exp2f((__uint_as_float(v[i]) - lse) * 1.4426950408889634f);
+                                if (i == rel) e -= 1.0f;
+                                f[i] = scale == 0.0f ? 0.0f : e * scale;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ptx::st_shared_v4(swz(buf0, lane, half * 4 + j), pack2<DT>(f[8 * j], f[8 * j + 1]),
+                                                  pack2<DT>(f[8 * j + 2], f[8 * j + 3]),
+                                                  pack2<DT>(f[8 * j + 4], f[8 * j + 5]),
+                                                  pack2<DT>(f[8 * j + 6], f[8 * j + 7]));
+                        }
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (EPI == kEpiGate) {
+                            ptx::tma_store_2d(&tm.out[0], p.keep ? stg : stg + (uint32_t)((n_chunk & 1) * 4096), x, row0);
+                            if (p.keep) {
+                                ptx::tma_store_2d(&tm.out[1], stg + 4096, x, row0);
+                                ptx::tma_store_2d(&tm.out[2], stg + 8192, x, row0);
+                            }
+                        } else {
+                            ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
+                            if (EPI == kEpiGateGrad || (EPI == kEpiStore && p.keep))
+                                ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
+                        }
+                        ptx::bulk_commit_group();
+                    }
+                    if constexpr (kLoads) {
+                        if (loads) {
+                            // the next chunk's loads, into the set whose stores have been read
+                            int nx = x + L::kChunk, nrow = row0;
+                            bool more = c + 1 < nch;
+                            if (!more && !last_tile) {
+                                int mb2, nb2;
+                                layer_tile_coords(t + clusters, p, mb2, nb2);
+                                nrow = mb2 * 256 + (int)rank * 128 + q * 32;
+                                nx = nb2 * L::kOutN;
+                                more = nrow < p.M;
+                            }
+                            if (more) {
+                                if (lane == 0) {
+                                    ptx::bulk_wait_group_read<1>();
+                                    issue_loads(nrow, nx, set ^ 1);
+                                }
+                                pending = true;
+                            }
+                        }
+                    }
+                    ++n_chunk;
+                }
+            }
+            if (failed) break;
+            if constexpr (EPI == kEpiLossStats)
+                if (nch > 0 && row < p.M) p.stats[(size_t)nb * p.M + row] = make_float2(best, sum);
+        }
+        if (lane == 0) {
+            // after an abort: loads under way land before shared memory goes away
+            if (pending) wait_drain(aux_bar(q, n_chunk & 1), (n_chunk >> 1) & 1, p.wait_limit);
+            ptx::bulk_wait_group_read<0>();
+        }
+        __syncwarp();
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    // neither CTA leaves while the other may still signal into it
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem_base, L::kTmemCols);
+    }
+}
+
+}  // namespace tcgemm
