@@ -8,6 +8,7 @@
 
 #include "grad_clip_kernel.cuh"
 #include "layer_pair_kernel.cuh"
+#include "layer_skinny_kernel.cuh"
 #include "layer_small_kernels.cuh"
 
 namespace {
@@ -199,8 +200,77 @@ int run_product_pair(const Product& q, const Ctx& c) {
     return launch_pdl(kern, dim3(2 * (tiles < pairs ? tiles : pairs)), kThreads, L::kSmem, 2, c.stream, tm, p);
 }
 
+// Few tokens: weight tiles of 128 columns, split along K over clusters.
+template <bool WMN, bool GATE, int DT>
+int run_product_skinny(const Product& q, const Ctx& c) {
+    constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
+    SkinnyMaps tm;
+    std::memset(&tm, 0, sizeof(tm));
+    SkinnyParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.T = (int)q.M;
+    p.N = (int)q.N;
+    p.nt = (p.T + 15) / 16 * 16;
+    int rc = encode_mat(&tm.w[0], q.b, dtype, 64, WMN ? 64 : 128);
+    if (rc == GEMM_OK) rc = encode_mat(&tm.x[0], q.a, dtype, 64, p.nt);
+    if (rc == GEMM_OK && q.b2.p) rc = encode_mat(&tm.w[1], q.b2, dtype, 64, WMN ? 64 : 128);
+    if (rc == GEMM_OK && q.a2.p) rc = encode_mat(&tm.x[1], q.a2, dtype, 64, p.nt);
+    if (rc != GEMM_OK) return rc;
+    p.k_switch = ceil_div(q.K, 64);
+    p.k_steps = q.a2.p ? 2 * p.k_switch : p.k_switch;
+    // Shared memory: two CTAs an SM up to 64 tokens (one's set-up and epilogue run
+    // under the other's stream), else one.  Tensor Memory follows: at most 128
+    // columns a CTA in the first case, 256 in the second.
+    const bool two = p.nt <= 64;
+    const int budget = (two ? 115712 : kSmemLimit) - 1024 - 8 * (2 * kSkinnySlots + 1) - 16;
+    p.stage_bytes = (GATE ? 2 : 1) * kSkinnyTileBytes + p.nt * 128;
+    p.slots = budget / p.stage_bytes < kSkinnySlots ? budget / p.stage_bytes : kSkinnySlots;
+    const int cols = (GATE ? 2 : 1) * p.nt;
+    p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    int smem = p.slots * p.stage_bytes + 1024 + 8 * (2 * kSkinnySlots + 1) + 16;
+    if (two && smem < 78848) smem = 78848;  // never three CTAs an SM
+    // The split that comes nearest two CTAs on every SM (one beyond 64 tokens),
+    // at least four K steps each.
+    const int tiles = ceil_div(q.N, 128);
+    int split = (two ? 2 : 1) * c.dev->sms / tiles;
+    if (split > p.k_steps / 4) split = p.k_steps / 4;
+    if (split > kMaxSplit) split = kMaxSplit;
+    if (split < 1) split = 1;
+    p.split = split;
+    if ((long long)tiles * split > INT_MAX) return GEMM_ERR_DIM;
+    p.act = q.p.act;
+    p.bias = q.p.bias;
+    p.alpha = q.p.alpha;
+    if (q.ins > 0) {
+        p.addend = q.in[0].p;
+        p.ld_addend = q.in[0].ld;
+        p.addend_f32 = q.in[0].bytes == 4;
+    }
+    p.out = const_cast<void*>(q.out[0].p);
+    p.ld_out = q.out[0].ld;
+    p.out_f32 = q.out[0].bytes == 4;
+    p.keep0 = const_cast<void*>(q.out[1].p);
+    p.ld_keep0 = q.out[1].ld;
+    p.keep1 = const_cast<void*>(q.out[2].p);
+    p.ld_keep1 = q.out[2].ld;
+    p.wait_limit = c.wait_limit;
+    p.inject = c.inject;
+    auto kern = layer_skinny_kernel<WMN, GATE, DT>;
+    static std::atomic<bool> ready[kMaxDevices];
+    rc = ensure_smem_limit(kern, kSmemLimit, ready[c.ordinal]);
+    if (rc != GEMM_OK) return rc;
+    return launch_pdl(kern, dim3(tiles * split), kThreads, smem, split, c.stream, tm, p);
+}
+
 template <int LAY, int EPI>
 int run_product(const Product& q, int dtype, const Ctx& c) {
+    if constexpr (LAY != kTN && (EPI == kEpiStore || EPI == kEpiStoreF32 || EPI == kEpiGate)) {
+        if (q.M <= kSkinnyTokens) {
+            constexpr bool gate = EPI == kEpiGate;
+            return dtype == LAYER_BF16 ? run_product_skinny<LAY == kNN, gate, kBF16>(q, c)
+                                       : run_product_skinny<LAY == kNN, gate, kF16>(q, c);
+        }
+    }
     return dtype == LAYER_BF16 ? run_product_pair<LAY, EPI, kBF16>(q, c) : run_product_pair<LAY, EPI, kF16>(q, c);
 }
 

@@ -1,0 +1,313 @@
+// The layer operators' matrix product for few tokens: y = x w with x [T, K],
+// T <= 128, where the time is that of streaming the weights once.
+//
+// The tile is computed transposed: the MMA's M is 128 weight columns and its N
+// the tokens (rounded up to 16), so one token costs one sixteenth of a
+// 256-row tile's products and none of the weights' bandwidth.  Weights come as
+// [K, N] (the MMA's A operand MN-major) or [N, K] (K-major), as TMA loads them;
+// x is the B operand, K-major.
+//
+// Memory-bound: what counts is enough bytes in flight on every SM.  N / 128
+// column tiles alone rarely fill 152 SMs, so a thread-block cluster of up to 8
+// CTAs shares each tile along K; up to 64 tokens two CTAs fit an SM, one's
+// set-up and epilogue under the other's stream.  Each CTA leaves its fp32
+// partial tile in shared memory; then the CTAs of the cluster each sum a share
+// of the tile over distributed shared memory, in rank order (the same bits
+// every time), apply the epilogue and store.  kGate runs both weights' tiles
+// side by side and stores h = act(g) u.
+//
+// Roles: warp 0 lane 0 loads, warp 1 lane 0 issues MMAs, warps 2-5 read the
+// accumulator; all six reduce and store.  Every wait is bounded.
+#pragma once
+
+#include "layer_common.cuh"
+
+namespace tcgemm {
+
+constexpr int kSkinnyTokens = 128;   // most tokens of one launch
+constexpr int kSkinnySlots = 12;     // most ring slots
+constexpr int kSkinnyTileBytes = 128 * 64 * 2;  // one weight tile of one K step
+
+struct SkinnyMaps {
+    CUtensorMap w[2], x[2];
+};
+
+struct SkinnyParams {
+    int T, N, nt;            // nt: tokens rounded up to 16, the MMA's N
+    int k_steps, k_switch;   // 64-deep; steps >= k_switch read w[1], x[1] from their start (not kGate)
+    int split, slots, stage_bytes, tmem_cols;
+    int act;
+    const void* bias;
+    const float* alpha;
+    const void* addend;      // [T, N]: residual, or an fp32 running sum
+    long long ld_addend;
+    int addend_f32, out_f32;
+    void* out;
+    long long ld_out;
+    void *keep0, *keep1;     // x w + bias; kGate: g and u
+    long long ld_keep0, ld_keep1;
+    long long wait_limit;
+    int inject;
+};
+
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32"
+        " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// Four neighbouring values of a row, those from `left` on absent (0, not stored).
+template <int DT>
+__device__ __forceinline__ void load4(const void* p, long long at, int left, float (&f)[4]) {
+    if (left >= 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const unsigned short*>(p) + at);
+        const float2 a = unpack2<DT>(w.x), b = unpack2<DT>(w.y);
+        f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) f[i] = i < left ? load1<DT>(p, at + i) : 0.0f;
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(void* p, long long at, int left, const float (&f)[4]) {
+    if (left >= 4) {
+        *reinterpret_cast<uint2*>(static_cast<unsigned short*>(p) + at) =
+            make_uint2(pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < left) static_cast<unsigned short*>(p)[at + i] = pack1<DT>(f[i]);
+    }
+}
+
+template <bool WMN, bool GATE, int DT>
+__global__ void __launch_bounds__(kThreads, 2)
+    layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
+    constexpr int kTiles = GATE ? 2 : 1;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t ring = (raw + 1023u) & ~1023u;
+    const int S = p.slots;
+    const uint32_t bar0 = ring + (uint32_t)(S * p.stage_bytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bar0 - raw) + 8 * (2 * kSkinnySlots + 1));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+#ifdef TCGEMM_CHECK
+    if (bar0 + 8u * (2 * kSkinnySlots + 1) + 8u > raw + ptx::dynamic_smem_size() ||
+        kTiles * p.nt * 512 > S * p.stage_bytes) {
+        if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
+        return;  // every CTA decides alike
+    }
+#endif
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kSkinnySlots + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * kSkinnySlots);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int CS = p.split;
+    const int rank = (int)blockIdx.x % CS;
+    const int n0 = ((int)blockIdx.x / CS) * 128;
+    const int k0 = (int)((long long)p.k_steps * rank / CS), k1 = (int)((long long)p.k_steps * (rank + 1) / CS);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        ptx::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm.w[0]);
+        ptx::prefetch_tmap(&tm.x[0]);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr((const void*)tmem_slot), p.tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0 && p.inject == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+            ptx::grid_dependency_wait();
+            ptx::grid_launch_dependents();
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) break;
+                const uint32_t fb = full_bar(stage), dst = ring + (uint32_t)(stage * p.stage_bytes);
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)p.stage_bytes);
+                const int second = !GATE && kb >= p.k_switch;
+                const int k = (second ? kb - p.k_switch : kb) * 64;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    const CUtensorMap* tw = &tm.w[GATE ? i : second];
+                    const uint32_t d = dst + i * kSkinnyTileBytes;
+                    if constexpr (WMN) {
+                        ptx::tma_load_2d(d, tw, fb, n0, k);
+                        ptx::tma_load_2d(d + kBoxBytes, tw, fb, n0 + 64, k);
+                    } else {
+                        ptx::tma_load_2d(d, tw, fb, k, n0);
+                    }
+                }
+                ptx::tma_load_2d(dst + kTiles * kSkinnyTileBytes, &tm.x[second], fb, k, 0);
+                issued_mask |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            for (int s = 0; s < S; ++s)
+                if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint32_t idesc = layer_idesc(DT, WMN, false, 128, p.nt);
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) break;
+                ptx::tc_fence_after();
+                const uint32_t src = ring + (uint32_t)(stage * p.stage_bytes);
+                const uint64_t xd = operand_desc<false>(src + kTiles * kSkinnyTileBytes);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    const uint64_t wd = operand_desc<WMN>(src + i * kSkinnyTileBytes);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        ptx::mma_f16_ss(tmem + (uint32_t)(i * p.nt), wd + k * kSliceStep<WMN>, xd + k * kSliceStep<false>,
+                                        idesc, ((kb - k0) | k) != 0);
+                }
+                ptx::mma_commit(empty_bar(stage));
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            ptx::mma_commit(done_bar);  // also after an abort: no MMA outlives the accumulator
+            wait_drain(done_bar, 0, p.wait_limit);
+        }
+    } else {
+        // ---------------- this CTA's partial: TMEM -> shared memory ----------------
+        // (the ring is idle: every load was consumed by an MMA, and every MMA is complete)
+        const int q = warp & 3;
+        if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0) {
+            ptx::tc_fence_after();
+            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+            const uint32_t col = ring + (uint32_t)((q * 32 + lane) * 4);
+#pragma unroll 1
+            for (int c = 0; c < kTiles * p.nt; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(trow + c, v);
+                ptx::tmem_ld_wait();
+                // [token][128 columns] fp32
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(col + (uint32_t)((c + i) * 512)), "r"(v[i]) : "memory");
+            }
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, p.tmem_cols);
+    }
+    if (CS > 1) {
+        __syncwarp();
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    }
+    if (*abort_flag == 0) {
+        // the previous kernel's reads and writes of what is read and written below are done
+        ptx::grid_dependency_wait();
+        const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
+        const int items = p.T * 32;  // four columns of one token each
+        const int lo = (int)((long long)items * rank / CS), hi = (int)((long long)items * (rank + 1) / CS);
+        for (int it = lo + (int)threadIdx.x; it < hi; it += kThreads) {
+            const int t = it >> 5, c = (it & 31) * 4;
+            const int n = n0 + c, left = p.N - n;
+            if (left <= 0) continue;
+            float f[kTiles][4];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const uint32_t src = ring + (uint32_t)((i * p.nt + t) * 512 + c * 4);
+                if (CS == 1) {
+                    ld_shared_f4(src, f[i][0], f[i][1], f[i][2], f[i][3]);
+                } else {
+                    f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0.0f;
+#pragma unroll 4
+                    for (int r = 0; r < CS; ++r) {
+                        uint32_t w[4];
+                        ptx::ld_cluster_v4(ptx::mapa(src, r), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[i][e] += __uint_as_float(w[e]);
+                    }
+                }
+            }
+            float o[4];
+            if constexpr (GATE) {
+                if (p.keep0 != nullptr) {
+                    store4<DT>(p.keep0, t * p.ld_keep0 + n, left, f[0]);
+                    store4<DT>(p.keep1, t * p.ld_keep1 + n, left, f[1]);
+                }
+                with_act(p.act, [&](auto tag) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(tag)::value>(f[0][e]) * f[1][e];
+                });
+                store4<DT>(p.out, t * p.ld_out + n, left, o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    o[e] = f[0][e] * alpha;
+                    if (p.bias != nullptr && e < left) o[e] += load1<DT>(p.bias, n + e);
+                }
+                if (p.keep0 != nullptr) store4<DT>(p.keep0, t * p.ld_keep0 + n, left, o);
+                if (p.act != kActNone)
+                    with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] = act_value<decltype(tag)::value>(o[e]);
+                    });
+                if (p.addend != nullptr) {
+                    if (p.addend_f32) {
+                        const float* a = static_cast<const float*>(p.addend) + t * p.ld_addend + n;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (e < left) o[e] += a[e];
+                    } else {
+                        float a[4];
+                        load4<DT>(p.addend, t * p.ld_addend + n, left, a);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[e] += a[e];
+                    }
+                }
+                if (p.out_f32) {
+                    float* d = static_cast<float*>(p.out) + t * p.ld_out + n;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < left) d[e] = o[e];
+                } else {
+                    store4<DT>(p.out, t * p.ld_out + n, left, o);
+                }
+            }
+        }
+    }
+    if (CS > 1) {
+        // no CTA leaves while another still reads its partial
+        __syncwarp();
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
+}
+
+}  // namespace tcgemm
