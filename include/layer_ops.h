@@ -72,10 +72,10 @@ int linear_forward(const linear_args *args, gemm_stream_t stream);
 typedef struct {
     const void *dy, *x, *w, *preact;
     void *dx, *dw, *dbias;
-    void *workspace;
     long long lddy, ldx, ldw, ldp, lddx, lddw;
     long long tokens, k, n;
     long long dtype, act;
+    void *workspace;
     long long workspace_bytes;
 } linear_grad_args;
 int linear_backward(const linear_grad_args *args, gemm_stream_t stream);
@@ -110,11 +110,11 @@ int gated_ffn_forward(const gated_args *args, gemm_stream_t stream);
 typedef struct {
     const void *dy, *x, *w_gate, *w_up, *w_down, *gate, *up, *hidden;
     void *dx, *dw_gate, *dw_up, *dw_down;
-    void *workspace;
     long long lddy, ldx, ldw_gate, ldw_up, ldw_down, ld_gate, ld_up, ld_hidden;
     long long lddx, lddw_gate, lddw_up, lddw_down;
     long long tokens, dim, ffn, dim_out;
     long long dtype, act;
+    void *workspace;
     long long workspace_bytes;
 } gated_grad_args;
 int gated_ffn_backward(const gated_grad_args *args, gemm_stream_t stream);
@@ -135,10 +135,10 @@ typedef struct {
     const void *h, *w;
     const long long *target;
     float *loss, *lse;
-    void *workspace;
     long long ldh, ldw;
     long long tokens, dim, vocab;
     long long dtype, ignore_index, reduction;
+    void *workspace;
     long long workspace_bytes;
 } loss_args;
 int linear_cross_entropy(const loss_args *args, gemm_stream_t stream);
@@ -162,10 +162,10 @@ typedef struct {
     const long long *target;
     const float *lse, *grad_loss;
     void *dh, *dw;
-    void *workspace;
     long long ldh, ldw, lddh, lddw;
     long long tokens, dim, vocab;
     long long dtype, ignore_index, reduction;
+    void *workspace;
     long long workspace_bytes;
 } loss_grad_args;
 int linear_cross_entropy_backward(const loss_grad_args *args, gemm_stream_t stream);

@@ -7,8 +7,11 @@
 // scaled, so the gradients are read twice (the second time in the opposite
 // order, so that what the norm pass read last is found in L2) and written
 // once.  The tensors' table travels in the kernel's parameters; a block
-// takes chunks of kClipChunk entries of one tensor.  Squares are summed in fp32
-// per thread and chunk (64 to 128 terms), in fp64 from there, in a fixed order.
+// takes chunks of up to kClipMostChunk entries of one tensor.  Squares are summed in fp32:
+// 64 terms per thread and chunk, then chunk by chunk, then pairwise over the
+// threads and blocks, in a fixed order (fp64 at this GPU's rate made the two
+// passes over 400,000 entries take 22 us instead of 9).  Norms between 1e-19 and
+// 1e19 are what fp32 squares can hold.
 #pragma once
 
 #include "layer_common.cuh"
@@ -16,7 +19,8 @@
 namespace tcgemm {
 
 constexpr int kClipThreads = 256;
-constexpr int kClipChunk = 32768;   // entries
+constexpr int kClipMostChunk = 32768;  // entries; fewer where the tensors are few and small, so that
+constexpr int kClipLeastChunk = 2048;  // every SM has some (400,000 entries: 19 us in 32768s, 11 in 2048s)
 constexpr int kClipF32 = 2;         // ElemType's continuation
 
 struct ClipEntry {
@@ -27,7 +31,7 @@ struct ClipEntry {
 
 template <int CAP>
 struct ClipTable {
-    int tensors, chunks;
+    int tensors, chunks, chunk;     // chunk: entries
     int first[CAP];                 // first chunk of each tensor
     ClipEntry e[CAP];
 };
@@ -97,33 +101,38 @@ __device__ __forceinline__ float clip_squares(const void* src, int n) {
     return s0 + s1;
 }
 
+// The sum of every thread's v, in a fixed order; all threads get it.
+__device__ __forceinline__ float clip_block_sum(float v, float* scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kClipThreads / 32; ++i) v += scratch[i];
+    return v;
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_norm_kernel(const __grid_constant__ ClipTable<CAP> t, double* partial) {
-    __shared__ double sums[kClipThreads / 32];
+    clip_norm_kernel(const __grid_constant__ ClipTable<CAP> t, float* partial) {
+    __shared__ float sums[kClipThreads / 32];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    double total = 0.0;
+    float total = 0.0f;
     for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
         const int k = clip_find(t, c);
         const ClipEntry& e = t.e[k];
-        const long long at = (long long)(c - t.first[k]) * kClipChunk;
+        const long long at = (long long)(c - t.first[k]) * t.chunk;
         const long long left = (e.count_type >> 2) - at;
-        const int n = (int)(left < kClipChunk ? left : kClipChunk);
+        const int n = (int)(left < t.chunk ? left : t.chunk);
         const int ty = (int)(e.count_type & 3);
         const char* src = static_cast<const char*>(e.src) + at * (ty == kClipF32 ? 4 : 2);
-        total += (double)(ty == kClipF32 ? clip_squares<kClipF32>(src, n)
+        total += (ty == kClipF32 ? clip_squares<kClipF32>(src, n)
                           : ty == kBF16 ? clip_squares<kBF16>(src, n) : clip_squares<kF16>(src, n));
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        total = 0.0;
-        for (int i = 0; i < kClipThreads / 32; ++i) total += sums[i];
-        partial[blockIdx.x] = total;
-    }
+    total = clip_block_sum(total, sums);
+    if (threadIdx.x == 0) partial[blockIdx.x] = total;
 }
 
 template <int TY>
@@ -167,32 +176,27 @@ __device__ __forceinline__ void clip_scale(const void* src, void* dst, int n, fl
 // Every block sums the partials itself, in order (a few KiB from L2).
 template <int CAP>
 __global__ void __launch_bounds__(kClipThreads)
-    clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const double* partial, int parts, double max_norm,
-                      double eps, float* norm_out) {
-    __shared__ double sums[kClipThreads / 32];
+    clip_scale_kernel(const __grid_constant__ ClipTable<CAP> t, const float* partial, int parts, float max_norm,
+                      float eps, float* norm_out) {
+    __shared__ float sums[kClipThreads / 32];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    double total = 0.0;
+    float total = 0.0f;
+#pragma unroll 4
     for (int i = threadIdx.x; i < parts; i += kClipThreads) total += partial[i];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = total;
-    __syncthreads();
-    total = 0.0;
-    for (int i = 0; i < kClipThreads / 32; ++i) total += sums[i];
-    const double norm = sqrt(total);
-    if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = (float)norm;
-    const double c = max_norm / (norm + eps);
-    const float coef = c < 1.0 ? (float)c : c == c ? 1.0f : (float)c;  // a NaN norm makes every entry NaN
+    const float norm = sqrtf(clip_block_sum(total, sums));
+    if (blockIdx.x == 0 && threadIdx.x == 0 && norm_out != nullptr) *norm_out = norm;
+    const float c = max_norm / (norm + eps);
+    const float coef = c < 1.0f ? c : c == c ? 1.0f : c;  // a NaN norm makes every entry NaN
     for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
         const int ch = t.chunks - 1 - k;
         const int i = clip_find(t, ch);
         const ClipEntry& e = t.e[i];
         // in place and nothing to clip: the entries stay as they are
         if (coef == 1.0f && e.src == e.dst) continue;
-        const long long at = (long long)(ch - t.first[i]) * kClipChunk;
+        const long long at = (long long)(ch - t.first[i]) * t.chunk;
         const long long left = (e.count_type >> 2) - at;
-        const int n = (int)(left < kClipChunk ? left : kClipChunk);
+        const int n = (int)(left < t.chunk ? left : t.chunk);
         const int ty = (int)(e.count_type & 3);
         const char* src = static_cast<const char*>(e.src) + at * (ty == kClipF32 ? 4 : 2);
         char* dst = static_cast<char*>(e.dst) + at * (ty == kClipF32 ? 4 : 2);

@@ -57,11 +57,30 @@ __device__ __forceinline__ float gelu_tanh_2z(float x) {
     return 1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f);
 }
 
+// The normal distribution's function Phi(x) = (1 + erf(x / sqrt 2)) / 2 and
+// exp(-x^2 / 2), by Abramowitz and Stegun's formula 7.1.26: erfc(z) =
+// t (a1 + t (a2 + ...)) exp(-z^2) with t = 1 / (1 + p z), off by at most
+// 1.5e-7 for z >= 0.  Its exponential is the one the slope needs, and below 0 it is
+// the small tail itself, without the cancellation of 1 + erf.
+__device__ __forceinline__ float normal_cdf(float x, float& e) {
+    const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(x), 1.0f));
+    e = __expf(-0.5f * x * x);
+    float q = fmaf(t, 1.061405429f, -1.453152027f);
+    q = fmaf(t, q, 1.421413741f);
+    q = fmaf(t, q, -0.284496736f);
+    q = fmaf(t, q, 0.254829592f);
+    const float tail = 0.5f * t * q * e;
+    return x < 0.0f ? tail : 1.0f - tail;
+}
+
 template <int ACT>
 __device__ __forceinline__ float act_value(float x) {
     if constexpr (ACT == kActRelu) return x > 0.0f ? x : (x == x ? 0.0f : x);  // NaN stays NaN
     if constexpr (ACT == kActSilu) return __fdividef(x, 1.0f + __expf(-x));
-    if constexpr (ACT == kActGelu) return 0.5f * x * (1.0f + erff(x * 0.70710678118654752f));
+    if constexpr (ACT == kActGelu) {
+        float e;
+        return x * normal_cdf(x, e);
+    }
     if constexpr (ACT == kActGeluTanh) return __fdividef(x, 1.0f + __expf(-gelu_tanh_2z(x)));
     return x;
 }
@@ -73,8 +92,11 @@ __device__ __forceinline__ float act_slope(float x) {
         const float s = sigmoid(x);
         return s * fmaf(x, 1.0f - s, 1.0f);
     }
-    if constexpr (ACT == kActGelu)
-        return fmaf(x * 0.39894228040143268f, __expf(-0.5f * x * x), 0.5f * (1.0f + erff(x * 0.70710678118654752f)));
+    if constexpr (ACT == kActGelu) {
+        float e;
+        const float c = normal_cdf(x, e);
+        return fmaf(x * 0.39894228040143268f, e, c);
+    }
     if constexpr (ACT == kActGeluTanh) {
         // the slope is 0 or 1 to the last bit beyond |x| = 12; x^3 stays finite (NaN passes through)
         const float c = x > 12.0f ? 12.0f : x < -12.0f ? -12.0f : x;
@@ -116,8 +138,8 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kSliceStep = MN ? (kUmmaK * 128) >> 4 : (kUmmaK * 2) >> 4;  // descriptor units of 16 bytes
 
-__device__ __forceinline__ void st_shared_f32(uint32_t addr, float v) {
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_shared_b16(uint32_t addr, unsigned short v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
 __device__ __forceinline__ void ld_shared_f4(uint32_t addr, float& a, float& b, float& c, float& d) {

@@ -7,6 +7,7 @@
 #include "layer_ops.h"
 
 #include "grad_clip_kernel.cuh"
+#include "layer_grads_kernel.cuh"
 #include "layer_pair_kernel.cuh"
 #include "layer_skinny_kernel.cuh"
 #include "layer_small_kernels.cuh"
@@ -154,13 +155,55 @@ struct Product {
     Mat in[2] = {};
     int ins = 0;
     long long M, N, K;
+    // the kernel before this one on the stream is this call's own (and so began when everything
+    // before it was complete), and it does not write b
+    bool after_own = false;
     LayerParams p{};
 };
 
-template <int LAY, int EPI, int DT>
-int run_product_pair(const Product& q, const Ctx& c) {
+// CTA pairs: 256 x 256 tiles (kEpiGate 256 x 128 of h), and for the store
+// epilogue a split along K over clusters of 2 to 4 pairs.
+struct PairPlan {
+    int tiles, pairs, split, k_steps;
+};
+
+// Cycles a product is expected to take, to choose between the kernels and their
+// splits.  A pair takes about 545 a 64-deep step of a tile, 8,500 around the steps
+// and 8,500 more to exchange partials; HBM gives 3,300 bytes a cycle.  (Over 66
+// products of 1 to 1024 tokens with K, N from 1024 to 14336, the choice by these two
+// estimates cost 0.1 % on average and 3 % at worst against the better of the two.)
+long long product_bytes(const Product& q, int weights) {
+    return 2 * (weights * q.K * q.N + q.M * (q.K + q.N));
+}
+
+long long pair_cycles(const PairPlan& g, const Product& q, int weights) {
+    const int waves = g.split > 1 ? 1 : ceil_div(g.tiles, g.pairs);
+    const long long steps = 8500 + (long long)waves * ceil_div(g.k_steps, g.split) * 545 + (g.split > 1 ? 8500 : 0);
+    const long long bytes = 9500 + product_bytes(q, weights) / 3300;
+    return steps > bytes ? steps : bytes;
+}
+
+PairPlan pair_plan(const Product& q, int epi, const Ctx& c) {
+    PairPlan g{};
+    g.k_steps = ceil_div(q.K, 64) * (q.a2.p ? 2 : 1);
+    const long long tiles = (long long)ceil_div(q.M, 256) * ceil_div(q.N, epi == kEpiGate ? 128 : 256);
+    g.tiles = tiles > INT_MAX - 1024 ? INT_MAX : (int)tiles;
+    g.pairs = max_pairs_of(*c.dev);
+    g.split = 1;
+    if (epi != kEpiStore) return g;
+    PairPlan best = g;
+    for (int s = 2; s <= kLayerMaxSplit; ++s) {
+        g.split = s;
+        if (g.k_steps / s < 4 || g.tiles > max_clusters_of(*c.dev, 2 * s)) break;
+        if (pair_cycles(g, q, 1) < pair_cycles(best, q, 1)) best = g;
+    }
+    return best;
+}
+
+template <int LAY, int EPI, int DT, bool SPLIT>
+int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
     constexpr int PN = 256;
-    using L = LayerPairLayout<EPI, PN>;
+    using L = LayerPairLayout<EPI, PN, SPLIT>;
     constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
     constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
     LayerMaps tm;
@@ -192,17 +235,110 @@ int run_product_pair(const Product& q, const Ctx& c) {
     p.raster_group = 8;
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
-    auto kern = layer_pair_kernel<LAY, EPI, DT, PN>;
+    p.split = g.split;
+    auto kern = layer_pair_kernel<LAY, EPI, DT, PN, SPLIT>;
     static std::atomic<bool> ready[kMaxDevices];
     rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
     if (rc != GEMM_OK) return rc;
-    const int tiles = p.tiles_m * p.tiles_n, pairs = max_pairs_of(*c.dev);
-    return launch_pdl(kern, dim3(2 * (tiles < pairs ? tiles : pairs)), kThreads, L::kSmem, 2, c.stream, tm, p);
+    const int clusters = SPLIT || g.tiles < g.pairs ? g.tiles : g.pairs;
+    return launch_pdl(kern, dim3(2 * g.split * clusters), L::kThreads, L::kSmem, 2 * g.split, c.stream, tm, p);
 }
 
-// Few tokens: weight tiles of 128 columns, split along K over clusters.
-template <bool WMN, bool GATE, int DT>
-int run_product_skinny(const Product& q, const Ctx& c) {
+constexpr int kSkinnyTwoSmem = 115712;  // two such CTAs fill an SM's 228 KiB
+
+// How the kernel for few tokens runs a product: tokens a tile, split along K,
+// shared memory.
+struct SkinnyPlan {
+    int nt, t_tiles, tiles, split, slots, stage_bytes, smem, tmem_cols, waves, k_steps;
+};
+
+// As pair_cycles.  An SM takes in about 58 bytes a cycle of operands that hit L2; 8,000
+// cycles around the steps, 45 a token of the tile for its way through shared memory.
+long long skinny_cycles(const SkinnyPlan& g, const Product& q, int weights) {
+    const long long steps = 8000 + (long long)g.waves * ceil_div(g.k_steps, g.split) * (g.stage_bytes / 58) +
+                            45ll * g.nt * weights;
+    const long long bytes = 6500 + product_bytes(q, weights) / 3300;
+    return steps > bytes ? steps : bytes;
+}
+
+SkinnyPlan skinny_plan(const Product& q, bool gate, int sms, const int* held) {
+    SkinnyPlan g{};
+    const int most = gate ? 128 : 256;  // the fp32 partials of a tile have to fit the ring
+    g.t_tiles = ceil_div(q.M, most);
+    g.nt = (ceil_div(q.M, g.t_tiles) + 15) / 16 * 16;
+    g.tiles = ceil_div(q.N, 128) * g.t_tiles;
+    const int weights = gate ? 2 : 1, k_steps = ceil_div(q.K, 64) * (q.a2.p ? 2 : 1);
+    g.stage_bytes = weights * kSkinnyTileBytes + g.nt * 128;
+    const int cols = weights * g.nt;
+    g.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : cols <= 256 ? 256 : 512;
+    // Two CTAs an SM where their accumulators are small and the ring still holds some
+    // 80 KB of weights (64 KB of a gated tile's).  An SM takes in about 64 GB/s of weights
+    // missing L2, so HBM's rate needs four SMs in five busy: one CTA on each, or two of a
+    // gated tile's shallow rings.  The split is the least that gives so many CTAs, among
+    // those whose clusters all fit at once, at two K steps each at least (one token,
+    // K = N = 4096: 1, 2, 4, 6 and 8 CTAs a tile 19.8, 12.1, 8.6, 8.8 and 9.0 us; 8 tokens,
+    // K = 32768, N = 1024: 8, 12 and 16 CTAs a tile 21.2, 17.4 and 15.8 us; the gated product
+    // of 4096 x 14336: 2, 3 and 4 CTAs a tile 36.5, 44 and 40.5 us, the last two in two waves).
+    const int fixed = 1024 + 8 * (2 * kSkinnySlots + 1) + 16;
+    const int in_flight = (kSkinnyTwoSmem - fixed) / g.stage_bytes * weights * kSkinnyTileBytes;
+    const bool two = cols <= 128 && in_flight >= (gate ? 65536 : 81920);
+    // (After this call's own kernel the weights' first loads run under that kernel's
+    // end, and twice the CTAs start more of them: worth it where 16 steps each remain.
+    // Gated block for one token, 4096 x 14336: 62.7 -> 58.3 us.)
+    const int each = sms * 4 / 5;
+    const bool twice = two && (gate || (q.after_own && (long long)k_steps * g.tiles >= 32ll * each));
+    const int want = twice ? 2 * each : each;
+    int split = 1;
+    for (int s = 2; s <= kSkinnySplit && s * 2 <= k_steps && g.tiles * split < want; ++s)
+        if (g.tiles <= held[s] * (two ? 2 : 1)) split = s;
+    g.split = split;
+    g.slots = ((two ? kSkinnyTwoSmem : kSmemLimit) - fixed) / g.stage_bytes;
+    if (g.slots > kSkinnySlots) g.slots = kSkinnySlots;
+    g.smem = g.slots * g.stage_bytes + fixed;
+    const int floor_smem = two ? 78848 : 118784;  // never three CTAs an SM, or two
+    if (g.smem < floor_smem) g.smem = floor_smem;
+    g.waves = ceil_div((long long)g.tiles * g.split, sms);
+    g.k_steps = k_steps;
+    return g;
+}
+
+// [s]: how many clusters of s CTAs, one CTA an SM, the device holds at once (a
+// cluster's CTAs share a GPC, so not every size packs the SMs).  Asked once per
+// device and kernel.  cudaOccupancyMaxActiveClusters gives the same numbers for CTAs
+// that fit an SM twice; twice as many of them run at once all the same.
+template <bool WMN, int EPI, int DT>
+const int* skinny_clusters(const Ctx& c) {
+    static int held[kMaxDevices][kSkinnySplit + 1];
+    static std::atomic<bool> known[kMaxDevices];
+    if (known[c.ordinal].load(std::memory_order_acquire)) return held[c.ordinal];
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    if (known[c.ordinal].load(std::memory_order_relaxed)) return held[c.ordinal];
+    auto kern = layer_skinny_kernel<WMN, EPI, DT>;
+    bool can = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
+    for (int s = 1; s <= kSkinnySplit; ++s) {
+        if (s == kMaxSplit + 1)
+            can = can && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(s * 64, 1, 1);
+        lc.blockDim = dim3(kThreads, 1, 1);
+        lc.dynamicSmemBytes = kSmemLimit;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = s;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        lc.attrs = attr;
+        lc.numAttrs = 1;
+        int n = 0;
+        held[c.ordinal][s] = can && cudaOccupancyMaxActiveClusters(&n, kern, &lc) == cudaSuccess ? n : 0;
+    }
+    cudaGetLastError();
+    known[c.ordinal].store(true, std::memory_order_release);
+    return held[c.ordinal];
+}
+
+template <bool WMN, int EPI, int DT>
+int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
     SkinnyMaps tm;
     std::memset(&tm, 0, sizeof(tm));
@@ -210,34 +346,21 @@ int run_product_skinny(const Product& q, const Ctx& c) {
     std::memset(&p, 0, sizeof(p));
     p.T = (int)q.M;
     p.N = (int)q.N;
-    p.nt = (p.T + 15) / 16 * 16;
+    p.nt = g.nt;
+    p.t_tiles = g.t_tiles;
     int rc = encode_mat(&tm.w[0], q.b, dtype, 64, WMN ? 64 : 128);
-    if (rc == GEMM_OK) rc = encode_mat(&tm.x[0], q.a, dtype, 64, p.nt);
+    if (rc == GEMM_OK) rc = encode_mat(&tm.x[0], q.a, dtype, 64, g.nt);
     if (rc == GEMM_OK && q.b2.p) rc = encode_mat(&tm.w[1], q.b2, dtype, 64, WMN ? 64 : 128);
-    if (rc == GEMM_OK && q.a2.p) rc = encode_mat(&tm.x[1], q.a2, dtype, 64, p.nt);
+    if (rc == GEMM_OK && q.a2.p) rc = encode_mat(&tm.x[1], q.a2, dtype, 64, g.nt);
     if (rc != GEMM_OK) return rc;
     p.k_switch = ceil_div(q.K, 64);
     p.k_steps = q.a2.p ? 2 * p.k_switch : p.k_switch;
-    // Shared memory: two CTAs an SM up to 64 tokens (one's set-up and epilogue run
-    // under the other's stream), else one.  Tensor Memory follows: at most 128
-    // columns a CTA in the first case, 256 in the second.
-    const bool two = p.nt <= 64;
-    const int budget = (two ? 115712 : kSmemLimit) - 1024 - 8 * (2 * kSkinnySlots + 1) - 16;
-    p.stage_bytes = (GATE ? 2 : 1) * kSkinnyTileBytes + p.nt * 128;
-    p.slots = budget / p.stage_bytes < kSkinnySlots ? budget / p.stage_bytes : kSkinnySlots;
-    const int cols = (GATE ? 2 : 1) * p.nt;
-    p.tmem_cols = cols <= 32 ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
-    int smem = p.slots * p.stage_bytes + 1024 + 8 * (2 * kSkinnySlots + 1) + 16;
-    if (two && smem < 78848) smem = 78848;  // never three CTAs an SM
-    // The split that comes nearest two CTAs on every SM (one beyond 64 tokens),
-    // at least four K steps each.
-    const int tiles = ceil_div(q.N, 128);
-    int split = (two ? 2 : 1) * c.dev->sms / tiles;
-    if (split > p.k_steps / 4) split = p.k_steps / 4;
-    if (split > kMaxSplit) split = kMaxSplit;
-    if (split < 1) split = 1;
-    p.split = split;
-    if ((long long)tiles * split > INT_MAX) return GEMM_ERR_DIM;
+    p.split = g.split;
+    p.weights_early = q.after_own;
+    p.slots = g.slots;
+    p.stage_bytes = g.stage_bytes;
+    p.tmem_cols = g.tmem_cols;
+    if ((long long)g.tiles * g.split > INT_MAX) return GEMM_ERR_DIM;
     p.act = q.p.act;
     p.bias = q.p.bias;
     p.alpha = q.p.alpha;
@@ -253,25 +376,159 @@ int run_product_skinny(const Product& q, const Ctx& c) {
     p.ld_keep0 = q.out[1].ld;
     p.keep1 = const_cast<void*>(q.out[2].p);
     p.ld_keep1 = q.out[2].ld;
+    p.stats = q.p.stats;
+    p.target_logit = q.p.target_logit;
+    p.target = q.p.target;
+    p.col0 = q.p.col0;
+    p.lse = q.p.lse;
+    p.row_scale = q.p.row_scale;
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
-    auto kern = layer_skinny_kernel<WMN, GATE, DT>;
+    const int smem = g.smem, split = g.split, tiles = g.tiles;
+    auto kern = layer_skinny_kernel<WMN, EPI, DT>;
     static std::atomic<bool> ready[kMaxDevices];
     rc = ensure_smem_limit(kern, kSmemLimit, ready[c.ordinal]);
     if (rc != GEMM_OK) return rc;
     return launch_pdl(kern, dim3(tiles * split), kThreads, smem, split, c.stream, tm, p);
 }
 
-template <int LAY, int EPI>
-int run_product(const Product& q, int dtype, const Ctx& c) {
-    if constexpr (LAY != kTN && (EPI == kEpiStore || EPI == kEpiStoreF32 || EPI == kEpiGate)) {
-        if (q.M <= kSkinnyTokens) {
-            constexpr bool gate = EPI == kEpiGate;
-            return dtype == LAYER_BF16 ? run_product_skinny<LAY == kNN, gate, kBF16>(q, c)
-                                       : run_product_skinny<LAY == kNN, gate, kF16>(q, c);
+// The kernel whose expected time is less; beyond kFewTokens always the pairs'.
+constexpr long long kFewTokens = 1024;
+
+template <int LAY, int EPI, int DT>
+int run_product_as(const Product& q, const Ctx& c) {
+    const PairPlan g = pair_plan(q, EPI, c);
+    if constexpr (LAY != kTN && EPI != kEpiGateGrad) {
+        constexpr int epi = EPI == kEpiStoreF32 ? kEpiStore : EPI;  // the output's type is a parameter there
+        if (q.M <= kFewTokens) {
+            const SkinnyPlan f = skinny_plan(q, EPI == kEpiGate, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c));
+            constexpr int weights = EPI == kEpiGate ? 2 : 1;
+            if (skinny_cycles(f, q, weights) <= pair_cycles(g, q, weights)) return run_product_skinny<LAY == kNN, epi, DT>(q, f, c);
         }
     }
-    return dtype == LAYER_BF16 ? run_product_pair<LAY, EPI, kBF16>(q, c) : run_product_pair<LAY, EPI, kF16>(q, c);
+    if constexpr (EPI == kEpiStore)
+        if (g.split > 1) return run_product_pair<LAY, EPI, DT, true>(q, g, c);
+    return run_product_pair<LAY, EPI, DT, false>(q, g, c);
+}
+
+template <int LAY, int EPI>
+int run_product(const Product& q, int dtype, const Ctx& c) {
+    return dtype == LAYER_BF16 ? run_product_as<LAY, EPI, kBF16>(q, c) : run_product_as<LAY, EPI, kF16>(q, c);
+}
+
+// ---- several products of a backward pass together -----------------------------------------
+
+struct GradProduct {
+    Product q;
+    int layout;
+};
+
+template <int DT>
+int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
+    constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
+    using L = LayerPairLayout<kEpiStore, 256, false>;
+    GradsMaps tm;
+    std::memset(&tm, 0, sizeof(tm));
+    GradsParams p;
+    std::memset(&p, 0, sizeof(p));
+    int rc = GEMM_OK;
+    for (int i = 0; i < n && rc == GEMM_OK; ++i) {
+        const Product& q = list[i].q;
+        GradsProblem& g = p.q[i];
+        g.a_mn = list[i].layout == kTN;
+        g.b_mn = list[i].layout != kNT;
+        g.M = (int)q.M;
+        g.N = (int)q.N;
+        g.tiles_m = ceil_div(q.M, 256);
+        g.tiles_n = ceil_div(q.N, 256);
+        g.k_switch = ceil_div(q.K, 64);
+        g.k_steps = q.a2.p ? 2 * g.k_switch : g.k_switch;
+        rc = encode_mat(&tm.a[i], q.a, dtype, 64, g.a_mn ? 64 : 128);
+        if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], q.b, dtype, 64, g.b_mn ? 64 : 128);
+        if (rc == GEMM_OK && q.a2.p) {
+            rc = encode_mat(&tm.a[kGradsProblems], q.a2, dtype, 64, g.a_mn ? 64 : 128);
+            if (rc == GEMM_OK) rc = encode_mat(&tm.b[kGradsProblems], q.b2, dtype, 64, g.b_mn ? 64 : 128);
+        }
+        if (rc == GEMM_OK) rc = encode_mat(&tm.out[i], q.out[0], dtype, 64, 32);
+    }
+    if (rc != GEMM_OK) return rc;
+    p.problems = n;
+    p.longs = longs;
+    for (int i = 0; i < n; ++i) p.tiles[i < p.longs ? 0 : 1] += p.q[i].tiles_m * p.q[i].tiles_n;
+    const int pairs = max_pairs_of(*c.dev);
+    p.rounds = p.tiles[0] / pairs;
+    p.rem = p.tiles[0] % pairs;
+    if (p.rem > 0) {
+        const int shorter = p.q[longs].k_steps;
+        p.d = (p.q[0].k_steps + shorter / 2) / shorter;
+        const int most = p.tiles[1] / (pairs - p.rem);
+        if (p.d > most) p.d = most;
+    }
+    p.raster_group = 8;
+    p.alpha = list[0].q.p.alpha;
+    p.wait_limit = c.wait_limit;
+    p.inject = c.inject;
+    auto kern = layer_grads_kernel<DT>;
+    static std::atomic<bool> ready[kMaxDevices];
+    rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
+    if (rc != GEMM_OK) return rc;
+    return launch_pdl(kern, dim3(2 * pairs), kThreads, L::kSmem, 2, c.stream, tm, p);
+}
+
+// Products with the plain store epilogue, of which list[0] has its own K and the
+// others share theirs: together where that is expected to take less than one after
+// the other.
+int run_grads(GradProduct* list, int n, int dtype, const Ctx& c) {
+    auto alone = [&](const GradProduct& g) {
+        switch (g.layout) {
+            case kNN: return run_product<kNN, kEpiStore>(g.q, dtype, c);
+            case kNT: return run_product<kNT, kEpiStore>(g.q, dtype, c);
+            default: return run_product<kTN, kEpiStore>(g.q, dtype, c);
+        }
+    };
+    bool together = n > 1;
+    if (together) {
+        // The same estimates as above, with at least 6,000 cycles a tile for writing it: a
+        // weight gradient over few tokens is all writing.  (Over 54 backward passes of 8 to
+        // 4096 tokens, widths 512 to 14336, the choice cost 0.4 % on average.)
+        const int pairs = max_pairs_of(*c.dev);
+        long long apart = 0, cycles = 0, longest = 0, tiles = 0;
+        for (int i = 0; i < n; ++i) {
+            const Product& q = list[i].q;
+            const PairPlan g = pair_plan(q, kEpiStore, c);
+            const long long share = ceil_div(g.k_steps, g.split) * 545ll, whole = g.k_steps * 545ll;
+            long long cost = 8500 + (g.split > 1 ? 8500 : 0) +
+                             (g.split > 1 ? 1 : ceil_div(g.tiles, g.pairs)) * (share > 6000 ? share : 6000);
+            const long long bytes = 9500 + product_bytes(q, 1) / 3300;
+            if (cost < bytes) cost = bytes;
+            if (list[i].layout != kTN && q.M <= kFewTokens) {
+                const SkinnyPlan f = skinny_plan(q, false, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c));
+                const long long few = skinny_cycles(f, q, 1);
+                if (few < cost) cost = few;
+            }
+            apart += cost;
+            tiles += g.tiles;
+            const long long tile = whole > 6000 ? whole : 6000;
+            cycles += (long long)g.tiles * tile;
+            if (longest < tile) longest = tile;
+        }
+        const long long spread = (cycles + pairs - 1) / pairs;
+        together = tiles < INT_MAX / 2 && 8500 + (spread > longest ? spread : longest) < apart;
+    }
+    if (!together) {
+        for (int i = 0; i < n; ++i) {
+            const int rc = alone(list[i]);
+            if (rc != GEMM_OK) return rc;
+        }
+        return GEMM_OK;
+    }
+    // the group of the larger K goes first
+    int longs = 1;
+    if (list[0].q.K * (list[0].q.a2.p ? 2 : 1) < list[1].q.K) {
+        std::rotate(list, list + 1, list + n);
+        longs = n - 1;
+    }
+    return dtype == LAYER_BF16 ? run_grads_as<kBF16>(list, n, longs, c) : run_grads_as<kF16>(list, n, longs, c);
 }
 
 // A weight gradient over no tokens is zero.
@@ -331,7 +588,7 @@ int run_slope(const SlopeParams& sp, void* dbias, int row_blocks, const Ctx& c) 
 
 // ---- vocabulary cross entropy ------------------------------------------------------------
 
-constexpr int kLossPart = 256;  // vocabulary columns per part of the statistics: one tile
+constexpr int kLossPart = 128;  // vocabulary columns per part of the statistics
 
 struct LossPlan {
     int parts;
@@ -379,12 +636,14 @@ constexpr int kClipBlocksPerSm = 8;
 constexpr int kClipMaxBlocks = 256 * kClipBlocksPerSm;  // partial sums per launch
 
 template <int CAP>
-int run_clip(const grad_clip_args& a, const Ctx& c) {
-    double* partial = static_cast<double*>(a.workspace);
+int run_clip(const grad_clip_args& a, long long entries, const Ctx& c) {
+    float* partial = static_cast<float*>(a.workspace);
     static_assert(sizeof(ClipTable<kClipBig>) < 32000, "kernel parameters");
     const int max_blocks = c.dev->sms * kClipBlocksPerSm < kClipMaxBlocks ? c.dev->sms * kClipBlocksPerSm : kClipMaxBlocks;
     int parts = 0;
     ClipTable<CAP> t;
+    t.chunk = kClipMostChunk;
+    while (t.chunk > kClipLeastChunk && entries / t.chunk < 4ll * c.dev->sms) t.chunk /= 2;
     // both passes cut the tensors into the same tables, so `parts` ends alike
     for (int pass = 0; pass < 2; ++pass) {
         const int all_parts = parts;
@@ -396,7 +655,7 @@ int run_clip(const grad_clip_args& a, const Ctx& c) {
             while (i < a.tensors && t.tensors < CAP) {
                 const long long n = a.count[i];
                 if (n > 0) {
-                    const long long ch = (n + kClipChunk - 1) / kClipChunk;
+                    const long long ch = (n + t.chunk - 1) / t.chunk;
                     if (t.chunks + ch > INT_MAX / 2) {
                         if (t.tensors == 0) return GEMM_ERR_DIM;
                         break;
@@ -416,7 +675,7 @@ int run_clip(const grad_clip_args& a, const Ctx& c) {
                 parts += blocks;
             } else {
                 rc = launch_pdl(clip_scale_kernel<CAP>, dim3(blocks), kClipThreads, 0, 1, c.stream, t,
-                                (const double*)partial, all_parts, a.max_norm, a.eps, launches == 1 ? a.norm : nullptr);
+                                (const float*)partial, all_parts, (float)a.max_norm, (float)a.eps, launches == 1 ? a.norm : nullptr);
             }
             if (rc != GEMM_OK) return rc;
         }
@@ -532,27 +791,30 @@ int linear_backward(const linear_grad_args* args, gemm_stream_t stream) {
                                    : run_slope<kF16>(sp, a.dbias, g.row_blocks, c);
         if (rc != GEMM_OK) return rc;
     }
+    GradProduct list[2];
+    int n = 0;
     if (a.dx) {
-        Product q;
+        Product& q = list[n].q;
+        list[n++].layout = kNT;
         q.a = dpre;
         q.b = w;
         q.M = a.tokens;
         q.N = a.k;
         q.K = a.n;
         q.out[0] = dx;
-        if ((rc = run_product<kNT, kEpiStore>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
+        q.after_own = g.slope || g.sums;
     }
     if (a.dw) {
-        Product q;
+        Product& q = list[n].q;
+        list[n++].layout = kTN;
         q.a = x;
         q.b = dpre;
         q.M = a.k;
         q.N = a.n;
         q.K = a.tokens;
         q.out[0] = dw;
-        if ((rc = run_product<kTN, kEpiStore>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
     }
-    return GEMM_OK;
+    return run_grads(list, n, (int)a.dtype, c);
 }
 
 int gated_ffn_forward(const gated_args* args, gemm_stream_t stream) {
@@ -595,6 +857,7 @@ int gated_ffn_forward(const gated_args* args, gemm_stream_t stream) {
     q.p.act = (int)a.act;
     if ((rc = run_product<kNN, kEpiGate>(q, (int)a.dtype, c)) != GEMM_OK) return rc;
     Product d;
+    d.after_own = true;
     d.a = h;
     d.b = wd;
     d.M = a.tokens;
@@ -674,8 +937,12 @@ int gated_ffn_backward(const gated_grad_args* args, gemm_stream_t stream) {
         q.p.act = (int)a.act;
         if ((rc = run_product<kNT, kEpiGateGrad>(q, dtype, c)) != GEMM_OK) return rc;
     }
+    GradProduct list[4];
+    int n = 0;
     if (a.dx) {
-        Product q;
+        Product& q = list[n].q;
+        list[n++].layout = kNT;
+        q.after_own = true;
         q.a = dg;
         q.a2 = du;
         q.b = wg;
@@ -684,24 +951,23 @@ int gated_ffn_backward(const gated_grad_args* args, gemm_stream_t stream) {
         q.N = a.dim;
         q.K = a.ffn;
         q.out[0] = dx;
-        if ((rc = run_product<kNT, kEpiStore>(q, dtype, c)) != GEMM_OK) return rc;
     }
     auto weight_grad = [&](const Mat& in, const Mat& d, const Mat& out) {
-        Product q;
+        Product& q = list[n].q;
+        list[n++].layout = kTN;
         q.a = in;
         q.b = d;
         q.M = in.cols;
         q.N = d.cols;
         q.K = T;
         q.out[0] = out;
-        return run_product<kTN, kEpiStore>(q, dtype, c);
     };
     if (a.dw_gate) {
-        if ((rc = weight_grad(x, dg, dwg)) != GEMM_OK) return rc;
-        if ((rc = weight_grad(x, du, dwu)) != GEMM_OK) return rc;
+        weight_grad(x, dg, dwg);
+        weight_grad(x, du, dwu);
     }
-    if (a.dw_down && (rc = weight_grad(hid, dy, dwd)) != GEMM_OK) return rc;
-    return GEMM_OK;
+    if (a.dw_down) weight_grad(hid, dy, dwd);
+    return run_grads(list, n, dtype, c);
 }
 
 int linear_cross_entropy_workspace(const loss_args* args, size_t* bytes) {
@@ -760,8 +1026,12 @@ int linear_cross_entropy(const loss_args* args, gemm_stream_t stream) {
     lp.parts = g.parts;
     lp.vocab = a.vocab;
     lp.ignore_index = a.ignore_index;
-    if ((rc = launch_pdl(layer_loss_rows_kernel, dim3(ceil_div(a.tokens, 32)), 256, 0, 1, c.stream, lp)) != GEMM_OK) return rc;
-    if (each) return GEMM_OK;
+    if (!each && a.tokens <= 32) {
+        lp.total = a.loss;
+        lp.mean = a.reduction == LAYER_LOSS_MEAN;
+    }
+    if ((rc = launch_pdl(layer_loss_rows_kernel, dim3(ceil_div(a.tokens, 32)), 1024, 0, 1, c.stream, lp)) != GEMM_OK) return rc;
+    if (each || lp.total) return GEMM_OK;
     return launch_pdl(layer_loss_sum_kernel, dim3(1), 1024, 0, 1, c.stream, (const float*)lp.row_loss, a.target, a.loss,
                       (int)a.tokens, a.ignore_index, (int)(a.reduction == LAYER_LOSS_MEAN));
 }
@@ -826,6 +1096,7 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
         const Mat d = mat16(ws + g.d_at, T, n, pad8(g.piece));
         const Mat wp = mat16(static_cast<const char*>(a.w) + (size_t)v0 * a.ldw * 2, n, a.dim, a.ldw);
         Product q;
+        q.after_own = true;
         q.a = h;
         q.b = wp;
         q.M = T;
@@ -837,10 +1108,14 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
         q.p.lse = a.lse;
         q.p.row_scale = weight;
         if ((rc = run_product<kNT, kEpiLossGrad>(q, dtype, c)) != GEMM_OK) return rc;
+        GradProduct list[2];
+        int count = 0;
         if (a.dh) {
             // dh = d w, over the pieces in fp32; the last sum is unscaled and rounded
             const Mat sum = Mat{ws + g.sum_at, T, a.dim, ldsum, 4};
-            Product s;
+            Product& s = list[0].q;
+            list[0].layout = kNN;
+            s.after_own = true;
             s.a = d;
             s.b = wp;
             s.M = T;
@@ -853,11 +1128,16 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
                 s.ins = 1;
                 s.p.addend = last ? 2 : 1;
             }
-            rc = last ? run_product<kNN, kEpiStore>(s, dtype, c) : run_product<kNN, kEpiStoreF32>(s, dtype, c);
-            if (rc != GEMM_OK) return rc;
+            if (first && last)
+                count = 1;
+            else if ((rc = last ? run_product<kNN, kEpiStore>(s, dtype, c) : run_product<kNN, kEpiStoreF32>(s, dtype, c)) !=
+                     GEMM_OK)
+                return rc;
         }
         if (a.dw) {
-            Product s;
+            Product& s = list[count].q;
+            s = Product();
+            list[count++].layout = kTN;
             s.a = d;
             s.b = h;
             s.M = n;
@@ -865,8 +1145,8 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
             s.K = T;
             s.p.alpha = unscale;
             s.out[0] = mat16(static_cast<char*>(a.dw) + (size_t)v0 * a.lddw * 2, n, a.dim, a.lddw);
-            if ((rc = run_product<kTN, kEpiStore>(s, dtype, c)) != GEMM_OK) return rc;
         }
+        if ((rc = run_grads(list, count, dtype, c)) != GEMM_OK) return rc;
     }
     return GEMM_OK;
 }
@@ -875,7 +1155,7 @@ int grad_clip_workspace(long long tensors, size_t* bytes) {
     if (!bytes) return GEMM_ERR_NULL;
     if (tensors < 0 || tensors > (1ll << 40)) return GEMM_ERR_DIM;
     const size_t launches = tensors <= kClipSmall ? 1 : (size_t)((tensors + kClipBig - 1) / kClipBig);
-    *bytes = launches * kClipMaxBlocks * sizeof(double);
+    *bytes = launches * kClipMaxBlocks * sizeof(float);
     return GEMM_OK;
 }
 
@@ -888,7 +1168,7 @@ int grad_clip(const grad_clip_args* args, gemm_stream_t stream) {
     if (!(a.max_norm >= 0) || !(a.eps >= 0)) return GEMM_ERR_CONFIG;
     if (a.tensors > 0 && (!a.src || !a.dst || !a.count || !a.dtype)) return GEMM_ERR_NULL;
     if ((uintptr_t)a.norm & 3) return GEMM_ERR_ALIGN;
-    long long chunks = 0;
+    long long entries = 0;
     for (long long i = 0; i < a.tensors; ++i) {
         if (a.count[i] < 0 || a.count[i] > (1ll << 44)) return GEMM_ERR_DIM;
         if (a.dtype[i] < LAYER_F16 || a.dtype[i] > LAYER_F32) return GEMM_ERR_DTYPE;
@@ -900,13 +1180,13 @@ int grad_clip(const grad_clip_args* args, gemm_stream_t stream) {
             const Span s[] = {span_of(a.src[i], (uint64_t)a.count[i] * b)}, d[] = {span_of(a.dst[i], (uint64_t)a.count[i] * b)};
             if (overlaps(d, 1, s, 1)) return GEMM_ERR_ALIAS;
         }
-        chunks += (a.count[i] + kClipChunk - 1) / kClipChunk;
-        if (chunks > INT_MAX / 2) return GEMM_ERR_DIM;
+        entries += a.count[i];
+        if (entries > (1ll << 44)) return GEMM_ERR_DIM;
     }
     if ((rc = check_workspace(a.workspace, a.workspace_bytes, need)) != GEMM_OK) return rc;
     Ctx c;
     if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
-    return a.tensors <= kClipSmall ? run_clip<kClipSmall>(a, c) : run_clip<kClipBig>(a, c);
+    return a.tensors <= kClipSmall ? run_clip<kClipSmall>(a, entries, c) : run_clip<kClipBig>(a, entries, c);
 }
 
 }  // extern "C"

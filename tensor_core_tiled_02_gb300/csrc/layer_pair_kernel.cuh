@@ -27,12 +27,20 @@
 // reads 32 KiB of operands per SM per 64 of K, 512 cycles of MMA.  Persistent
 // pairs walk the tiles in the grouped raster of gemm_common.cuh; the TMEM
 // accumulator is double-buffered, so a tile's epilogue (arithmetic of 15 to 40
-// instructions an element on 4 warps) runs under the next tile's products.
-// What an epilogue reads and writes per tile moves by TMA through four 4 KiB
-// buffers per warp (in-place where it reads), leaving five 32 KiB stages.
+// instructions an element on four warps) runs under the next tile's products.
+// (Eight warps drain a tile sooner, but cost the products 2 %: 8192 tokens of the
+// gated block at 4096 x 14336 1519 us on four, 1542 on eight.)  What an epilogue reads
+// and writes moves by TMA through four 4 KiB buffers per warp (in place where it
+// reads), leaving five 32 KiB stages.
+//
+// SPLIT (kEpiStore, few tiles): a cluster of 2 to 4 pairs shares a tile along K.
+// Each CTA leaves its 128 rows of fp32 partials in its idle ring; then every
+// pair drains a share of the tile's columns, summing the partials of its rows over
+// distributed shared memory in rank order.  Nothing else hides that drain, so eight
+// warps run it, two on each quarter of the rows.
 //
 // Roles as in gemm_pair_kernel.cuh: warp 0 loads, warp 1 issues MMAs (even CTA),
-// warps 2-5 drain; every wait is bounded and reports through the status word.
+// the others drain; every wait is bounded and reports through the status word.
 #pragma once
 
 #include "layer_common.cuh"
@@ -49,6 +57,8 @@ enum LayerEpilogue {
     kEpiLossGrad = 5,
 };
 
+constexpr int kLayerMaxSplit = 4;
+
 struct LayerMaps {
     CUtensorMap a[2], b[2];
     CUtensorMap out[3];
@@ -60,12 +70,13 @@ struct LayerParams {
     int tiles_m, tiles_n;
     int k_steps, k_switch; // 64-deep; steps >= k_switch read a[1], b[1] from their start
     int raster_group;
+    int split;             // SPLIT: pairs sharing a tile along K
     int act;
     int addend;            // kEpiStore*: 0 none, 1 of the output's type, 2 fp32 under a 16-bit output
     int keep;              // kEpiStore: keep alpha v + bias in out[1]; kEpiGate: keep g and u in out[1], out[2]
     const void* bias;      // N values of the operands' type, or NULL
     const float* alpha;    // device scalar, or NULL for 1
-    float2* stats;         // kEpiLossStats: [tiles_n][M] (maximum, sum of exponentials)
+    float2* stats;         // kEpiLossStats: [ceil(N / 128)][M] (maximum, sum of exponentials)
     float* target_logit;   // kEpiLossStats: [M], written where the target's column is met
     const long long* target;  // kEpiLoss*: [M]
     int col0;              // kEpiLossGrad: vocabulary index of the tile grid's first column
@@ -75,21 +86,23 @@ struct LayerParams {
     int inject;
 };
 
-template <int EPI, int PN>
+template <int EPI, int PN, bool SPLIT>
 struct LayerPairLayout {
     static_assert(PN == 256 || PN == 128, "tile columns");
     static constexpr int kABytes = 128 * 64 * 2;         // this CTA's 128 rows of one K step
     static constexpr int kBBytes = (PN / 2) * 64 * 2;    // this CTA's PN/2 columns
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kBufs = EPI == kEpiLossStats ? 0 : 4;  // 4 KiB staging buffers per epilogue warp
-    static constexpr int kWarpStaging = kBufs * 4096;
-    // full[8], empty[8], tmem_full[2], tmem_empty[2], drain, aux[4 warps][2]
-    static constexpr int kNumBars = 2 * kMaxStages + 5 + 8;
-    static constexpr int kBiasBytes = 4 * 64 * 4;        // 64 fp32 per epilogue warp
-    static constexpr int kFixedBytes = 4 * kWarpStaging + kBiasBytes + ((kNumBars * 8 + 15) & ~15) + 16;
+    static constexpr int kWarps = SPLIT ? 8 : 4;         // epilogue warps
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr int kWarpStaging = EPI == kEpiLossStats ? 0 : 65536 / kWarps;  // staging per epilogue warp
+    // full[8], empty[8], tmem_full[2], tmem_empty[2], drain, aux[warps][2]
+    static constexpr int kNumBars = 2 * kMaxStages + 5 + 2 * kWarps;
+    static constexpr int kBiasBytes = kWarps * 64 * 2;   // 64 values per epilogue warp
+    static constexpr int kFixedBytes = kWarps * kWarpStaging + kBiasBytes + ((kNumBars * 8 + 15) & ~15) + 16;
     static constexpr int kLimit = 232448;
     static constexpr int kFit = (kLimit - 1024 - kFixedBytes) / kStageBytes;
     static constexpr int kSlots = kFit < kMaxStages ? kFit : kMaxStages;
+    static_assert(kSlots >= 5, "ring depth");
     static constexpr int kSmem = 1024 + kSlots * kStageBytes + kFixedBytes;
     static constexpr int kTmemCols = 2 * PN;             // two accumulators
     static constexpr int kOutN = EPI == kEpiGate ? PN / 2 : PN;      // output columns of a tile
@@ -113,13 +126,14 @@ __device__ __forceinline__ uint32_t swz(uint32_t buf, int lane, int piece) {
     return buf + (uint32_t)(lane * 128) + ((uint32_t)(piece ^ (lane & 7)) << 4);
 }
 
-template <int LAY, int EPI, int DT, int PN>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int LAY, int EPI, int DT, int PN, bool SPLIT>
+__global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
     layer_pair_kernel(const __grid_constant__ LayerMaps tm, const LayerParams p) {
-    using L = LayerPairLayout<EPI, PN>;
+    using L = LayerPairLayout<EPI, PN, SPLIT>;
     constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
     constexpr int S = L::kSlots;
     constexpr int kHalf = PN / 2;
+    static_assert(!SPLIT || (EPI == kEpiStore && S * L::kStageBytes >= 128 * PN * 4), "partials fit the ring");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -127,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sA = base;
     const uint32_t sB = sA + S * L::kABytes;
     const uint32_t sC = sB + S * L::kBBytes;
-    const uint32_t sBias = sC + 4 * L::kWarpStaging;
+    const uint32_t sBias = sC + L::kWarps * L::kWarpStaging;
     const uint32_t bar0 = sBias + L::kBiasBytes;
     const uint32_t misc = bar0 + ((L::kNumBars * 8 + 15) & ~15);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(base_ptr + (misc - base));
@@ -143,11 +157,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
     const uint32_t drain_bar = bar0 + 8u * (2 * kMaxStages + 4);
-    auto aux_bar = [&](int q, int set) { return bar0 + 8u * (2 * kMaxStages + 5 + 2 * q + set); };
+    auto aux_bar = [&](int e, int set) { return bar0 + 8u * (2 * kMaxStages + 5 + 2 * e + set); };
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = ptx::cluster_ctarank();
+    const uint32_t cta = ptx::cluster_ctarank();
+    const uint32_t rank = cta & 1;         // in its pair: 0 issues the MMAs
+    const uint32_t leader = cta & ~1u;
+    const uint16_t both = (uint16_t)(3u << leader);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -156,10 +173,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < 2; ++a) {
             ptx::mbar_init(tfull_bar(a), 1);
-            ptx::mbar_init(tempty_bar(a), 8);  // 4 epilogue warps in each CTA
+            ptx::mbar_init(tempty_bar(a), 2 * L::kWarps);  // every epilogue warp of both CTAs
         }
         ptx::mbar_init(drain_bar, 1);
-        for (int i = 0; i < 8; ++i) ptx::mbar_init(aux_bar(i >> 1, i & 1), 1);
+        for (int i = 0; i < 2 * L::kWarps; ++i) ptx::mbar_init(aux_bar(i >> 1, i & 1), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
     }
@@ -178,11 +195,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    const int cluster = blockIdx.x >> 1;
-    const int clusters = gridDim.x >> 1;
+    // this cluster's tiles: cluster, cluster + clusters, ... (SPLIT: one), and its K steps [kb0, kb1)
+    const int cluster = SPLIT ? (int)blockIdx.x / (2 * p.split) : (int)blockIdx.x >> 1;
+    const int clusters = SPLIT ? (int)gridDim.x / (2 * p.split) : (int)gridDim.x >> 1;
     const int tiles = p.tiles_m * p.tiles_n;
-    const int KB = p.k_steps;
+    const int share = SPLIT ? (int)(cta >> 1) : 0;
+    const int kb0 = SPLIT ? (int)((long long)p.k_steps * share / p.split) : 0;
+    const int kb1 = SPLIT ? (int)((long long)p.k_steps * (share + 1) / p.split) : p.k_steps;
 
+    bool split_met = false;
+    (void)split_met;
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
         if (lane == 0 && p.inject == 0) {
@@ -198,14 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int m0 = mb * 256 + (int)rank * 128;
                 // kEpiGate: this CTA's columns are the tile's PN/2 of one weight
                 const int n0 = EPI == kEpiGate ? nb * kHalf : nb * PN + (int)rank * kHalf;
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) {
                         ok = false;
                         break;
                     }
                     const uint32_t fb_local = full_bar(stage);
                     if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, 2 * L::kStageBytes);
-                    const uint32_t fb = ptx::mapa(fb_local, 0);
+                    const uint32_t fb = ptx::mapa(fb_local, leader);
                     const int second = kb >= p.k_switch;
                     const int k0 = (second ? kb - p.k_switch : kb) * 64;
                     const CUtensorMap* ta = &tm.a[second];
@@ -256,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
-                for (int kb = 0; kb < KB; ++kb) {
+                for (int kb = kb0; kb < kb1; ++kb) {
                     if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
                         ok = false;
                         break;
@@ -267,24 +289,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         ptx::mma_f16_ss_pair(d_tmem, ad0 + k * kSliceStep<kAMN>, bd0 + k * kSliceStep<kBMN>, idesc,
-                                             (kb | k) != 0);
-                    ptx::mma_commit_pair_multicast(empty_bar(stage), 0x3);
+                                             (kb - kb0) | k);
+                    ptx::mma_commit_pair_multicast(empty_bar(stage), both);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                ptx::mma_commit_pair_multicast(tfull_bar(acc), 0x3);
+                ptx::mma_commit_pair_multicast(tfull_bar(acc), both);
             }
             ptx::mma_commit_pair(drain_bar);
             wait_drain(drain_bar, 0, p.wait_limit);
         }
     } else {
-        // ---------------- epilogue (both CTAs): own 128 rows x PN columns ----------------
-        const int q = warp & 3;
-        const uint32_t stg = sC + (uint32_t)(q * L::kWarpStaging);
-        const uint32_t sbias = sBias + (uint32_t)(q * 256);
+        // ---------------- epilogue (both CTAs): 32 rows a warp, all columns or (SPLIT) half ----------------
+        const int ew = warp - 2;
+        const int q = warp & 3;                  // TMEM lanes 32 q ..
+        const int half = SPLIT ? ew >> 2 : 0;    // of the pair's share of columns
+        const uint32_t stg = sC + (uint32_t)(ew * L::kWarpStaging);
+        const uint32_t sbias = sBias + (uint32_t)(ew * 128);
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16);
         // the previous kernel's reads and writes of what this one touches are done from here on
         ptx::grid_dependency_wait();
@@ -295,14 +319,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32)
             if (p.alpha != nullptr) alpha = *p.alpha;
 
-        // chunks [0, n) of the tile hold columns below N; rows from M on are no one's
-        auto chunks_of = [&](int nb) {
-            const int left = p.N - nb * L::kOutN;
-            return min(L::kOutN / L::kChunk, (left + L::kChunk - 1) / L::kChunk);
+        // A chunk takes one buffer, or two where two matrices move (kEpiGate that keeps g and
+        // u: three); while the staging holds two such sets they alternate, and the
+        // next chunk's loads run under this one's work.
+        constexpr bool kAlwaysTwo = EPI == kEpiGateGrad;
+        const bool two_bufs = kAlwaysTwo || (EPI == kEpiStore && (p.keep || p.addend == 2));
+        const bool one_set = (EPI == kEpiGate && p.keep) || (SPLIT && two_bufs);
+        const bool four_sets = !SPLIT && !loads && !two_bufs && !one_set;  // nothing to load: all four in turn
+        auto set_of = [&](unsigned n) {
+            return one_set ? stg : four_sets ? stg + (n & 3) * 4096u : stg + (n & 1) * (two_bufs ? 8192u : 4096u);
         };
-        // the loads of one chunk (lane 0): into the chunk's set of two buffers
-        auto issue_loads = [&](int row0, int x, int set) {
-            const uint32_t bar = aux_bar(q, set), buf = stg + (uint32_t)(set * 8192);
+        auto wait_stores = [&]() {  // lane 0: the set about to be used is no longer read by a store
+            if (one_set)
+                ptx::bulk_wait_group_read<0>();
+            else if (four_sets)
+                ptx::bulk_wait_group_read<3>();
+            else
+                ptx::bulk_wait_group_read<1>();
+        };
+        // this warp's chunks of a tile, those with columns below N; rows from M on are no one's
+        constexpr int kChunks = L::kOutN / L::kChunk;
+        const int share0 = SPLIT ? kChunks * share / p.split : 0;
+        const int share1 = SPLIT ? kChunks * (share + 1) / p.split : kChunks;
+        const int mid = share0 + (share1 - share0 + 1) / 2;
+        const int c0 = SPLIT && half ? mid : share0;
+        auto chunk_end = [&](int nb) {
+            return min(SPLIT && !half ? mid : share1, (p.N - nb * L::kOutN + L::kChunk - 1) / L::kChunk);
+        };
+        // the loads of one chunk (lane 0)
+        auto issue_loads = [&](int row0, int x, unsigned n) {
+            const uint32_t bar = aux_bar(ew, n & 1), buf = set_of(n);
             if constexpr (EPI == kEpiGateGrad) {
                 ptx::mbar_arrive_expect_tx(bar, 8192);
                 ptx::tma_load_2d(buf, &tm.in[0], bar, x, row0);
@@ -316,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tma_load_2d(buf, &tm.in[0], bar, x, row0);
             }
         };
-        unsigned n_chunk = 0;           // chunks this warp has drained: set = n_chunk & 1, phase = n_chunk >> 1
+        unsigned n_chunk = 0;           // chunks this warp has drained: barrier n_chunk & 1, phase n_chunk >> 1
         bool pending = false;           // loads of chunk n_chunk are under way
         int tl = 0;
         for (int t = cluster; t < tiles; t += clusters) {
@@ -329,13 +375,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row = row0 + lane;
             const int n0 = nb * L::kOutN;
             const bool rows_here = row0 < p.M;
-            const int nch = rows_here ? chunks_of(nb) : 0;
+            const int c1 = rows_here ? chunk_end(nb) : 0;
             const bool last_tile = t + clusters >= tiles;
             if constexpr (kLoads) {
-                if (loads && rows_here && !pending) {
+                if (loads && c0 < c1 && !pending) {
                     if (lane == 0) {
                         ptx::bulk_wait_group_read<0>();
-                        issue_loads(row0, n0, n_chunk & 1);
+                        issue_loads(row0, n0 + c0 * L::kChunk, n_chunk);
                     }
                     pending = true;
                 }
@@ -359,21 +405,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto hand_back = [&]() {
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && !last_tile) ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), 0));
+                if (lane == 0 && !last_tile) ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), leader));
             };
-            if (nch == 0) hand_back();
+            if constexpr (SPLIT) {
+                // this CTA's partial into its ring (idle: every load was consumed by an MMA, every
+                // MMA is complete): 16-byte groups of four columns, [group][row], read below
+                for (int c = half * (PN / 64); c < (half + 1) * (PN / 64); ++c) {  // 32 columns
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int g = 0; g < 8; ++g)
+                        ptx::st_shared_v4(sA + (uint32_t)(((c * 8 + g) * 128 + q * 32 + lane) * 16), v[4 * g], v[4 * g + 1],
+                                          v[4 * g + 2], v[4 * g + 3]);
+                }
+                // every epilogue thread of the cluster; the other warps arrived at once
+                __syncwarp();
+                ptx::cluster_arrive();
+                ptx::cluster_wait();
+                split_met = true;
+            }
+            if (!SPLIT && c0 >= c1) hand_back();
             bool failed = false;
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (int c = c0; c < c1; ++c) {
                 const int x = n0 + c * L::kChunk;
-                const int set = n_chunk & 1;
-                const uint32_t buf0 = stg + (uint32_t)(set * 8192), buf1 = buf0 + 4096;
+                const uint32_t buf0 = set_of(n_chunk), buf1 = buf0 + 4096;
                 if constexpr (EPI == kEpiLossStats) {
                     __syncwarp();  // the lanes part where one of them meets its target
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
                     ptx::tmem_ld_wait();
-                    if (c == nch - 1) hand_back();
+                    if (!SPLIT && c == c1 - 1) hand_back();
                     if (p.N - x < 32) {  // columns from N on are no words
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
@@ -394,6 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     sum += s0 + s1;
                     best = m;
+                    if ((c & 3) == 3 || c == c1 - 1) {  // a part of 128 columns is whole
+                        if (row < p.M) p.stats[(size_t)(x >> 7) * p.M + row] = make_float2(best, sum);
+                        best = -INFINITY;
+                        sum = 0.0f;
+                    }
                     const int rel = tcol - x;
                     if (rel >= 0 && rel < 32) {
                         float tv = 0.0f;
@@ -405,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     if constexpr (kLoads) {
                         if (loads) {
-                            if (!warp_wait(aux_bar(q, set), (n_chunk >> 1) & 1, abort_flag, p.wait_limit, kSiteAuxLoad,
+                            if (!warp_wait(aux_bar(ew, n_chunk & 1), (n_chunk >> 1) & 1, abort_flag, p.wait_limit, kSiteAuxLoad,
                                            lane)) {
                                 failed = true;
                                 break;
@@ -413,15 +481,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             pending = false;
                         }
                     }
-                    // without loads: the stores issued from these buffers two chunks ago (kEpiGate
-                    // that keeps g and u: one chunk ago) have read them
+                    // without loads: the stores issued from these buffers have read them
                     if (!loads) {
-                        if (lane == 0) {
-                            if (EPI == kEpiGate && p.keep)
-                                ptx::bulk_wait_group_read<0>();
-                            else
-                                ptx::bulk_wait_group_read<1>();
-                        }
+                        if (lane == 0) wait_stores();
                         __syncwarp();
                     }
                     if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32) {
@@ -430,29 +492,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < C / 32; ++i) {
                                 const int col = x + i * 32 + lane;
-                                st_shared_f32(sbias + (uint32_t)((i * 32 + lane) * 4),
-                                              col < p.N ? load1<DT>(p.bias, col) : 0.0f);
+                                st_shared_b16(sbias + (uint32_t)((i * 32 + lane) * 2),
+                                              col < p.N ? static_cast<const unsigned short*>(p.bias)[col] : 0);
                             }
                             __syncwarp();
                         }
-                        uint32_t v[C];
-                        ptx::tmem_ld_32x32b_x32(trow + c * C, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-                        if constexpr (C == 64)
-                            ptx::tmem_ld_32x32b_x32(trow + c * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[C - 32]));
-                        ptx::tmem_ld_wait();
-                        if (c == nch - 1) hand_back();
                         float f[C];
+                        if constexpr (SPLIT) {
 #pragma unroll
-                        for (int i = 0; i < C; ++i) f[i] = __uint_as_float(v[i]) * alpha;
+                            for (int i = 0; i < C; ++i) f[i] = 0.0f;
+#pragma unroll 1
+                            for (int r = 0; r < p.split; ++r) {
+                                const uint32_t from = ptx::mapa(sA + (uint32_t)((c * 16 * 128 + q * 32 + lane) * 16),
+                                                                2 * (uint32_t)r + rank);
+#pragma unroll
+                                for (int g = 0; g < C / 4; ++g) {
+                                    uint32_t w[4];
+                                    ptx::ld_cluster_v4(from + (uint32_t)(g * 2048), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) f[4 * g + e] += __uint_as_float(w[e]);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < C; ++i) f[i] *= alpha;
+                        } else {
+                            uint32_t v[C];
+                            ptx::tmem_ld_32x32b_x32(trow + c * C, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+                            if constexpr (C == 64)
+                                ptx::tmem_ld_32x32b_x32(trow + c * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[C - 32]));
+                            ptx::tmem_ld_wait();
+                            if (c == c1 - 1) hand_back();
+#pragma unroll
+                            for (int i = 0; i < C; ++i) f[i] = __uint_as_float(v[i]) * alpha;
+                        }
                         if (p.bias != nullptr) {
 #pragma unroll
-                            for (int i = 0; i < C; i += 4) {
-                                float b0, b1, b2, b3;
-                                ld_shared_f4(sbias + (uint32_t)(i * 4), b0, b1, b2, b3);
-                                f[i] += b0;
-                                f[i + 1] += b1;
-                                f[i + 2] += b2;
-                                f[i + 3] += b3;
+                            for (int i = 0; i < C; i += 8) {
+                                uint32_t w[4];
+                                ptx::ld_shared_v4(sbias + (uint32_t)(i * 2), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 b = unpack2<DT>(w[e]);
+                                    f[i + 2 * e] += b.x;
+                                    f[i + 2 * e + 1] += b.y;
+                                }
                             }
                         }
                         if constexpr (EPI == kEpiStore) {
@@ -517,22 +600,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
                     } else if constexpr (EPI == kEpiGate) {
-                        const uint32_t hbuf = p.keep ? stg : stg + (uint32_t)((n_chunk & 1) * 4096);
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
+                        for (int part = 0; part < 2; ++part) {
                             uint32_t g[32], u[32];
-                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, g);
-                            ptx::tmem_ld_32x32b_x32(trow + kHalf + c * 64 + half * 32, u);
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + part * 32, g);
+                            ptx::tmem_ld_32x32b_x32(trow + kHalf + c * 64 + part * 32, u);
                             ptx::tmem_ld_wait();
-                            if (c == nch - 1 && half == 1) hand_back();
+                            if (c == c1 - 1 && part == 1) hand_back();
                             if (p.keep) {
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     auto at = [&](const uint32_t(&r)[32], int i) { return __uint_as_float(r[8 * j + i]); };
-                                    ptx::st_shared_v4(swz(stg + 4096, lane, half * 4 + j), pack2<DT>(at(g, 0), at(g, 1)),
+                                    ptx::st_shared_v4(swz(buf0 + 4096, lane, part * 4 + j), pack2<DT>(at(g, 0), at(g, 1)),
                                                       pack2<DT>(at(g, 2), at(g, 3)), pack2<DT>(at(g, 4), at(g, 5)),
                                                       pack2<DT>(at(g, 6), at(g, 7)));
-                                    ptx::st_shared_v4(swz(stg + 8192, lane, half * 4 + j), pack2<DT>(at(u, 0), at(u, 1)),
+                                    ptx::st_shared_v4(swz(buf0 + 8192, lane, part * 4 + j), pack2<DT>(at(u, 0), at(u, 1)),
                                                       pack2<DT>(at(u, 2), at(u, 3)), pack2<DT>(at(u, 4), at(u, 5)),
                                                       pack2<DT>(at(u, 6), at(u, 7)));
                                 }
@@ -546,25 +628,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             });
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                ptx::st_shared_v4(swz(hbuf, lane, half * 4 + j), pack2<DT>(h[8 * j], h[8 * j + 1]),
+                                ptx::st_shared_v4(swz(buf0, lane, part * 4 + j), pack2<DT>(h[8 * j], h[8 * j + 1]),
                                                   pack2<DT>(h[8 * j + 2], h[8 * j + 3]),
                                                   pack2<DT>(h[8 * j + 4], h[8 * j + 5]),
                                                   pack2<DT>(h[8 * j + 6], h[8 * j + 7]));
                         }
                     } else if constexpr (EPI == kEpiGateGrad) {
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
+                        for (int part = 0; part < 2; ++part) {
                             uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, v);
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + part * 32, v);
                             ptx::tmem_ld_wait();
-                            if (c == nch - 1 && half == 1) hand_back();
+                            if (c == c1 - 1 && part == 1) hand_back();
                             with_act(p.act, [&](auto tag) {
                                 constexpr int ACT = decltype(tag)::value;
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) {
                                     // this lane's row of g and u, replaced by dg and du
                                     uint32_t g[4], u[4];
-                                    const uint32_t ag = swz(buf0, lane, half * 4 + j), au = ag + 4096;
+                                    const uint32_t ag = swz(buf0, lane, part * 4 + j), au = ag + 4096;
                                     ptx::ld_shared_v4(ag, g[0], g[1], g[2], g[3]);
                                     ptx::ld_shared_v4(au, u[0], u[1], u[2], u[3]);
 #pragma unroll
@@ -582,12 +664,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     } else {  // kEpiLossGrad
 #pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
+                        for (int part = 0; part < 2; ++part) {
                             uint32_t v[32];
-                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + half * 32, v);
+                            ptx::tmem_ld_32x32b_x32(trow + c * 64 + part * 32, v);
                             ptx::tmem_ld_wait();
-                            if (c == nch - 1 && half == 1) hand_back();
-                            const int rel = tcol - x - half * 32;
+                            if (c == c1 - 1 && part == 1) hand_back();
+                            const int rel = tcol - x - part * 32;
                             float f[32];
                             // a row of weight 0 is 0 whatever its logits hold
 #pragma unroll
@@ -598,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                ptx::st_shared_v4(swz(buf0, lane, half * 4 + j), pack2<DT>(f[8 * j], f[8 * j + 1]),
+                                ptx::st_shared_v4(swz(buf0, lane, part * 4 + j), pack2<DT>(f[8 * j], f[8 * j + 1]),
                                                   pack2<DT>(f[8 * j + 2], f[8 * j + 3]),
                                                   pack2<DT>(f[8 * j + 4], f[8 * j + 5]),
                                                   pack2<DT>(f[8 * j + 6], f[8 * j + 7]));
@@ -607,35 +689,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        if constexpr (EPI == kEpiGate) {
-                            ptx::tma_store_2d(&tm.out[0], p.keep ? stg : stg + (uint32_t)((n_chunk & 1) * 4096), x, row0);
-                            if (p.keep) {
-                                ptx::tma_store_2d(&tm.out[1], stg + 4096, x, row0);
-                                ptx::tma_store_2d(&tm.out[2], stg + 8192, x, row0);
-                            }
-                        } else {
-                            ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
-                            if (EPI == kEpiGateGrad || (EPI == kEpiStore && p.keep))
-                                ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
+                        ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
+                        if (EPI == kEpiGateGrad || (EPI == kEpiStore && p.keep))
+                            ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
+                        if (EPI == kEpiGate && p.keep) {
+                            ptx::tma_store_2d(&tm.out[1], buf0 + 4096, x, row0);
+                            ptx::tma_store_2d(&tm.out[2], buf0 + 8192, x, row0);
                         }
                         ptx::bulk_commit_group();
                     }
                     if constexpr (kLoads) {
                         if (loads) {
-                            // the next chunk's loads, into the set whose stores have been read
+                            // the next chunk's loads, into buffers whose stores have been read
                             int nx = x + L::kChunk, nrow = row0;
-                            bool more = c + 1 < nch;
+                            bool more = c + 1 < c1;
                             if (!more && !last_tile) {
                                 int mb2, nb2;
                                 layer_tile_coords(t + clusters, p, mb2, nb2);
                                 nrow = mb2 * 256 + (int)rank * 128 + q * 32;
-                                nx = nb2 * L::kOutN;
-                                more = nrow < p.M;
+                                nx = nb2 * L::kOutN + c0 * L::kChunk;
+                                more = nrow < p.M && c0 < chunk_end(nb2);
                             }
                             if (more) {
                                 if (lane == 0) {
-                                    ptx::bulk_wait_group_read<1>();
-                                    issue_loads(nrow, nx, set ^ 1);
+                                    wait_stores();
+                                    issue_loads(nrow, nx, n_chunk + 1);
                                 }
                                 pending = true;
                             }
@@ -645,17 +723,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (failed) break;
-            if constexpr (EPI == kEpiLossStats)
-                if (nch > 0 && row < p.M) p.stats[(size_t)nb * p.M + row] = make_float2(best, sum);
         }
         if (lane == 0) {
             // after an abort: loads under way land before shared memory goes away
-            if (pending) wait_drain(aux_bar(q, n_chunk & 1), (n_chunk >> 1) & 1, p.wait_limit);
+            if (pending) wait_drain(aux_bar(ew, n_chunk & 1), (n_chunk >> 1) & 1, p.wait_limit);
             ptx::bulk_wait_group_read<0>();
         }
         __syncwarp();
     }
 
+    if constexpr (SPLIT) {
+        // the cluster's barrier before the partials are read takes every thread once:
+        // the warps without an epilogue, and epilogue warps that gave up a wait
+        if (!split_met) {
+            __syncwarp();
+            ptx::cluster_arrive();
+            ptx::cluster_wait();
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     // neither CTA leaves while the other may still signal into it

@@ -1,5 +1,5 @@
 // The layer operators' matrix product for few tokens: y = x w with x [T, K],
-// T <= 128, where the time is that of streaming the weights once.
+// where the time is that of streaming the weights once.
 //
 // The tile is computed transposed: the MMA's M is 128 weight columns and its N
 // the tokens (rounded up to 16), so one token costs one sixteenth of a
@@ -8,24 +8,23 @@
 // x is the B operand, K-major.
 //
 // Memory-bound: what counts is enough bytes in flight on every SM.  N / 128
-// column tiles alone rarely fill 152 SMs, so a thread-block cluster of up to 8
-// CTAs shares each tile along K; up to 64 tokens two CTAs fit an SM, one's
-// set-up and epilogue under the other's stream.  Each CTA leaves its fp32
-// partial tile in shared memory; then the CTAs of the cluster each sum a share
-// of the tile over distributed shared memory, in rank order (the same bits
-// every time), apply the epilogue and store.  kGate runs both weights' tiles
-// side by side and stores h = act(g) u.
+// column tiles alone rarely fill 152 SMs, so a thread-block cluster of up to 16
+// CTAs shares each tile along K.  Each CTA leaves its fp32 partial tile in
+// shared memory; then the CTAs of the cluster each sum a share of the tile's
+// tokens over distributed shared memory, in rank order (the same bits every
+// time), a warp at a time on the 128 columns of one token, and apply the
+// epilogue (layer_pair_kernel.cuh names them).
 //
 // Roles: warp 0 lane 0 loads, warp 1 lane 0 issues MMAs, warps 2-5 read the
 // accumulator; all six reduce and store.  Every wait is bounded.
 #pragma once
 
-#include "layer_common.cuh"
+#include "layer_pair_kernel.cuh"
 
 namespace tcgemm {
 
-constexpr int kSkinnyTokens = 128;   // most tokens of one launch
 constexpr int kSkinnySlots = 12;     // most ring slots
+constexpr int kSkinnySplit = 16;     // most CTAs sharing a tile (above 8 a non-portable cluster)
 constexpr int kSkinnyTileBytes = 128 * 64 * 2;  // one weight tile of one K step
 
 struct SkinnyMaps {
@@ -33,9 +32,11 @@ struct SkinnyMaps {
 };
 
 struct SkinnyParams {
-    int T, N, nt;            // nt: tokens rounded up to 16, the MMA's N
+    int T, N, nt;            // nt: tokens a tile, a multiple of 16: the MMA's N
+    int t_tiles;             // ceil(T / nt)
     int k_steps, k_switch;   // 64-deep; steps >= k_switch read w[1], x[1] from their start (not kGate)
     int split, slots, stage_bytes, tmem_cols;
+    int weights_early;       // the previous kernel is this call's own and does not write the weights
     int act;
     const void* bias;
     const float* alpha;
@@ -46,6 +47,11 @@ struct SkinnyParams {
     long long ld_out;
     void *keep0, *keep1;     // x w + bias; kGate: g and u
     long long ld_keep0, ld_keep1;
+    float2* stats;           // kEpiLossStats: [ceil(N / 128)][T]
+    float* target_logit;
+    const long long* target; // kEpiLoss*
+    int col0;
+    const float *lse, *row_scale;
     long long wait_limit;
     int inject;
 };
@@ -85,9 +91,10 @@ __device__ __forceinline__ void store4(void* p, long long at, int left, const fl
     }
 }
 
-template <bool WMN, bool GATE, int DT>
+template <bool WMN, int EPI, int DT>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
+    constexpr bool GATE = EPI == kEpiGate;
     constexpr int kTiles = GATE ? 2 : 1;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -110,7 +117,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int lane = threadIdx.x & 31;
     const int CS = p.split;
     const int rank = (int)blockIdx.x % CS;
-    const int n0 = ((int)blockIdx.x / CS) * 128;
+    const int tile = (int)blockIdx.x / CS;
+    const int n0 = (tile / p.t_tiles) * 128, t0 = (tile % p.t_tiles) * p.nt;
     const int k0 = (int)((long long)p.k_steps * rank / CS), k1 = (int)((long long)p.k_steps * (rank + 1) / CS);
 
     if (threadIdx.x == 0) {
@@ -138,18 +146,20 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (lane == 0 && p.inject == 0) {
             int stage = 0;
             uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
-            ptx::grid_dependency_wait();
-            ptx::grid_launch_dependents();
-            for (int kb = k0; kb < k1; ++kb) {
-                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) break;
-                const uint32_t fb = full_bar(stage), dst = ring + (uint32_t)(stage * p.stage_bytes);
-                ptx::mbar_arrive_expect_tx(fb, (uint32_t)p.stage_bytes);
+            auto source = [&](int kb, int& k) {
                 const int second = !GATE && kb >= p.k_switch;
-                const int k = (second ? kb - p.k_switch : kb) * 64;
+                k = (second ? kb - p.k_switch : kb) * 64;
+                return second;
+            };
+            auto load_weights = [&](int kb, int st) {
+                int k;
+                const int second = source(kb, k);
+                const uint32_t fb = full_bar(st);
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)p.stage_bytes);
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
                     const CUtensorMap* tw = &tm.w[GATE ? i : second];
-                    const uint32_t d = dst + i * kSkinnyTileBytes;
+                    const uint32_t d = ring + (uint32_t)(st * p.stage_bytes) + i * kSkinnyTileBytes;
                     if constexpr (WMN) {
                         ptx::tma_load_2d(d, tw, fb, n0, k);
                         ptx::tma_load_2d(d + kBoxBytes, tw, fb, n0 + 64, k);
@@ -157,7 +167,25 @@ __global__ void __launch_bounds__(kThreads, 2)
                         ptx::tma_load_2d(d, tw, fb, k, n0);
                     }
                 }
-                ptx::tma_load_2d(dst + kTiles * kSkinnyTileBytes, &tm.x[second], fb, k, 0);
+            };
+            // Before the wait for the previous kernel, where that kernel is this call's own and
+            // does not write the weights: the first of them.  (Elsewhere, asking L2 for them
+            // before the wait measured slower: 8.7 -> 10.2 us for one token at K = N = 4096, the
+            // requests are as scarce as the bytes.)
+            const int pre = p.weights_early ? min(S, k1 - k0) : 0;
+            for (int i = 0; i < pre; ++i) load_weights(k0 + i, i);
+            ptx::grid_dependency_wait();
+            // after the wait: whoever starts on this may take it that all kernels before this one are complete
+            ptx::grid_launch_dependents();
+            for (int kb = k0; kb < k1; ++kb) {
+                if (kb - k0 >= pre) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) break;
+                    load_weights(kb, stage);
+                }
+                int k;
+                const int second = source(kb, k);
+                ptx::tma_load_2d(ring + (uint32_t)(stage * p.stage_bytes + kTiles * kSkinnyTileBytes), &tm.x[second],
+                                 full_bar(stage), k, t0);
                 issued_mask |= 1u << stage;
                 issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == S) {
@@ -232,31 +260,89 @@ __global__ void __launch_bounds__(kThreads, 2)
         // the previous kernel's reads and writes of what is read and written below are done
         ptx::grid_dependency_wait();
         const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
-        const int items = p.T * 32;  // four columns of one token each
-        const int lo = (int)((long long)items * rank / CS), hi = (int)((long long)items * (rank + 1) / CS);
-        for (int it = lo + (int)threadIdx.x; it < hi; it += kThreads) {
-            const int t = it >> 5, c = (it & 31) * 4;
-            const int n = n0 + c, left = p.N - n;
-            if (left <= 0) continue;
-            float f[kTiles][4];
+        // This CTA's tokens of the tile, a warp on each, a lane four columns.  First the
+        // sums over the cluster, kept in this CTA's own partial (nobody else reads these
+        // tokens of it): several tokens at a time, so that the reads of other CTAs' shared
+        // memory overlap (one at a time, 256 tokens at K = 2048, N = 8192 took 20.8 us, not
+        // 17.9), and apart from the epilogue, whose code four times over costs one token
+        // 0.4 us of instruction fetches.
+        const int tokens = min(p.nt, p.T - t0);
+        const int c = lane * 4, n = n0 + c, left = p.N - n;
+        const int tt_begin = tokens * rank / CS + warp, tt_end = tokens * (rank + 1) / CS;
+        constexpr int kWarps = kThreads / 32, kBatch = 4;
+        if (CS > 1) {
+#pragma unroll 1
+            for (int tb = tt_begin; tb < tt_end; tb += kWarps * kBatch) {
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                const uint32_t src = ring + (uint32_t)((i * p.nt + t) * 512 + c * 4);
-                if (CS == 1) {
-                    ld_shared_f4(src, f[i][0], f[i][1], f[i][2], f[i][3]);
-                } else {
-                    f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0.0f;
-#pragma unroll 4
+                for (int i = 0; i < kTiles; ++i) {
+                    float f[kBatch][4];
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) f[u][0] = f[u][1] = f[u][2] = f[u][3] = 0.0f;
+#pragma unroll 2
                     for (int r = 0; r < CS; ++r) {
-                        uint32_t w[4];
-                        ptx::ld_cluster_v4(ptx::mapa(src, r), w[0], w[1], w[2], w[3]);
+                        const uint32_t from = ptx::mapa(ring, r);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) f[i][e] += __uint_as_float(w[e]);
+                        for (int u = 0; u < kBatch; ++u) {
+                            const int tt = tb + u * kWarps;
+                            if (tt < tt_end) {
+                                uint32_t w[4];
+                                ptx::ld_cluster_v4(from + (uint32_t)((i * p.nt + tt) * 512 + c * 4), w[0], w[1], w[2], w[3]);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) f[u][e] += __uint_as_float(w[e]);
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int tt = tb + u * kWarps;
+                        if (tt < tt_end)
+                            ptx::st_shared_v4(ring + (uint32_t)((i * p.nt + tt) * 512 + c * 4), __float_as_uint(f[u][0]),
+                                              __float_as_uint(f[u][1]), __float_as_uint(f[u][2]), __float_as_uint(f[u][3]));
                     }
                 }
             }
+        }
+#pragma unroll 1
+        for (int tt = tt_begin; tt < tt_end; tt += kWarps) {
+            const int t = t0 + tt;
+            float f[kTiles][4];
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i)
+                ld_shared_f4(ring + (uint32_t)((i * p.nt + tt) * 512 + c * 4), f[i][0], f[i][1], f[i][2], f[i][3]);
             float o[4];
-            if constexpr (GATE) {
+            if constexpr (EPI == kEpiLossStats) {
+                float m = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (e >= left) f[0][e] = -INFINITY;  // columns from N on are no words
+                    m = fmaxf(m, f[0][e]);
+                }
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+                const float mf = m == -INFINITY ? 0.0f : m;
+                float sum = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum += exp2f((f[0][e] - mf) * 1.4426950408889634f);
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+                if (lane == 0) p.stats[(size_t)(n0 >> 7) * p.T + t] = make_float2(m, sum);
+                const long long rel = p.target[t] - n;
+                if (rel >= 0 && rel < 4 && rel < left)
+                    p.target_logit[t] = rel == 0 ? f[0][0] : rel == 1 ? f[0][1] : rel == 2 ? f[0][2] : f[0][3];
+                __syncwarp();
+                continue;
+            }
+            if (left <= 0) continue;
+            if constexpr (EPI == kEpiLossGrad) {
+                const float lse = p.lse[t], scale = p.row_scale[t];
+                const long long rel = p.target[t] - p.col0 - n;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float q = exp2f((f[0][e] - lse) * 1.4426950408889634f) - (rel == e ? 1.0f : 0.0f);
+                    o[e] = scale == 0.0f ? 0.0f : q * scale;
+                }
+                store4<DT>(p.out, t * p.ld_out + n, left, o);
+            } else if constexpr (GATE) {
                 if (p.keep0 != nullptr) {
                     store4<DT>(p.keep0, t * p.ld_keep0 + n, left, f[0]);
                     store4<DT>(p.keep1, t * p.ld_keep1 + n, left, f[1]);

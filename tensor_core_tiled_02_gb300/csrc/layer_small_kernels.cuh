@@ -13,7 +13,7 @@ namespace tcgemm {
 // A block takes kSlopeRows rows x 256 columns: 32 groups of 8 columns (16
 // bytes) x 8 rows at a time.  Reads dy and pre once, writes dpre once; the
 // block's column sums (of the unrounded products) go to partial[row block][N].
-constexpr int kSlopeRows = 64;
+constexpr int kSlopeRows = 32;
 constexpr int kSlopeCols = 256;
 
 struct SlopeParams {
@@ -41,45 +41,49 @@ __global__ void __launch_bounds__(256) layer_slope_kernel(const SlopeParams p) {
         const bool whole = col + 8 <= p.cols;
         with_act(p.pre ? p.act : kActNone, [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
-#pragma unroll 2
-            for (int r = r0 + rl; r < r1; r += 8) {
-                const unsigned short* dy = static_cast<const unsigned short*>(p.dy) + r * p.ld_dy + col;
-                const unsigned short* pre = static_cast<const unsigned short*>(p.pre) + r * p.ld_pre + col;
-                float d[8];
-                if (whole) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(dy);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+            constexpr int U = 4;  // rows under way per thread: 16-byte loads enough to keep HBM busy
+            if (whole) {
+                for (int rb = r0 + rl; rb < r1; rb += 8 * U) {
+                    uint4 w[U], z[U];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<DT>(ws[e]);
-                        d[2 * e] = f.x;
-                        d[2 * e + 1] = f.y;
+                    for (int u = 0; u < U; ++u) {
+                        const long long r = rb + 8 * u;
+                        if (r >= r1) continue;
+                        w[u] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(p.dy) + r * p.ld_dy + col);
+                        if constexpr (ACT != kActNone)
+                            z[u] = *reinterpret_cast<const uint4*>(static_cast<const unsigned short*>(p.pre) + r * p.ld_pre + col);
                     }
-                    if constexpr (ACT != kActNone) {
-                        const uint4 z = *reinterpret_cast<const uint4*>(pre);
-                        const uint32_t zs[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const long long r = rb + 8 * u;
+                        if (r >= r1) continue;
+                        const uint32_t ws[4] = {w[u].x, w[u].y, w[u].z, w[u].w}, zs[4] = {z[u].x, z[u].y, z[u].z, z[u].w};
+                        uint32_t os[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 f = unpack2<DT>(zs[e]);
-                            d[2 * e] *= act_slope<ACT>(f.x);
-                            d[2 * e + 1] *= act_slope<ACT>(f.y);
+                            float2 f = unpack2<DT>(ws[e]);
+                            if constexpr (ACT != kActNone) {
+                                const float2 g = unpack2<DT>(zs[e]);
+                                f.x *= act_slope<ACT>(g.x);
+                                f.y *= act_slope<ACT>(g.y);
+                            }
+                            acc[2 * e] += f.x;
+                            acc[2 * e + 1] += f.y;
+                            os[e] = pack2<DT>(f.x, f.y);
                         }
-                    }
-                    if (p.dpre)
-                        *reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.dpre) + r * p.ld_dpre + col) =
-                            make_uint4(pack2<DT>(d[0], d[1]), pack2<DT>(d[2], d[3]), pack2<DT>(d[4], d[5]),
-                                       pack2<DT>(d[6], d[7]));
-                } else {
-                    for (int e = 0; e < 8; ++e) {
-                        d[e] = 0.0f;
-                        if (col + e >= p.cols) continue;
-                        d[e] = load1<DT>(dy, e);
-                        if constexpr (ACT != kActNone) d[e] *= act_slope<ACT>(load1<DT>(pre, e));
-                        if (p.dpre) static_cast<unsigned short*>(p.dpre)[r * p.ld_dpre + col + e] = pack1<DT>(d[e]);
+                        if (p.dpre)
+                            *reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.dpre) + r * p.ld_dpre + col) =
+                                make_uint4(os[0], os[1], os[2], os[3]);
                     }
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += d[e];
+            } else {
+                for (long long r = r0 + rl; r < r1; r += 8)
+                    for (int e = 0; e < 8 && col + e < p.cols; ++e) {
+                        float d = load1<DT>(p.dy, r * p.ld_dy + col + e);
+                        if constexpr (ACT != kActNone) d *= act_slope<ACT>(load1<DT>(p.pre, r * p.ld_pre + col + e));
+                        if (p.dpre) static_cast<unsigned short*>(p.dpre)[r * p.ld_dpre + col + e] = pack1<DT>(d);
+                        acc[e] += d;
+                    }
             }
         });
     }
@@ -127,13 +131,17 @@ struct LossParams {
     float* lse;                 // [rows]
     int rows, parts;
     long long vocab, ignore_index;
+    float* total;               // at most 32 rows (one block): their sum or mean too, else NULL
+    int mean;
 };
 
 // lse = max + ln(sum over parts of s_i exp(m_i - max)); loss = lse - target's
 // logit.  An ignored row's loss is 0; a target that is neither ignored nor a
-// word makes its row's loss NaN.  32 rows a block, 8 slices of the parts.
-__global__ void __launch_bounds__(256) layer_loss_rows_kernel(const LossParams p) {
-    __shared__ float2 part[8][32];
+// word makes its row's loss NaN.  32 rows a block, 32 slices of the parts, each
+// slice four independent loads at a time (the pass is latency: 7.0 us for 8 rows
+// x 128 parts with 8 slices and one load at a time).
+__global__ void __launch_bounds__(1024) layer_loss_rows_kernel(const LossParams p) {
+    __shared__ float2 part[32][33];
     const int l = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + l;
     ptx::grid_dependency_wait();
@@ -145,22 +153,52 @@ __global__ void __launch_bounds__(256) layer_loss_rows_kernel(const LossParams p
         s = s * keep + o.y * add;
         m = big;
     };
-    if (row < p.rows)
-        for (int i = slice; i < p.parts; i += 8) join(p.stats[(size_t)i * p.rows + row]);
+    if (row < p.rows) {
+        for (int i = slice; i < p.parts; i += 128) {
+            float2 o[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                o[u] = i + 32 * u < p.parts ? p.stats[(size_t)(i + 32 * u) * p.rows + row] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) join(o[u]);
+        }
+    }
     part[slice][l] = make_float2(m, s);
     __syncthreads();
-    if (slice != 0 || row >= p.rows) return;
-    m = -INFINITY;
-    s = 0.0f;
+    // warp w joins row w's 32 slices: in pairs, always the same ones
+    const float2 mine = part[l][slice];
+    m = mine.x;
+    s = mine.y;
+    __syncthreads();  // `part` is free again
 #pragma unroll
-    for (int i = 0; i < 8; ++i) join(part[i][l]);
-    const float lse = m + logf(s);
-    const long long t = p.target[row];
-    p.lse[row] = lse;
-    p.row_loss[row] = t == p.ignore_index ? 0.0f
-                      : t < 0 || t >= p.vocab ? __int_as_float(0x7FC00000) : lse - p.target_logit[row];
+    for (int o = 16; o > 0; o >>= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+        join(make_float2(om, os));
+    }
+    const int mine_row = blockIdx.x * 32 + slice;
+    if (l == 0 && mine_row < p.rows) {
+        const float lse = m + logf(s);
+        const long long t = p.target[mine_row];
+        p.lse[mine_row] = lse;
+        const float loss = t == p.ignore_index ? 0.0f
+                           : t < 0 || t >= p.vocab ? __int_as_float(0x7FC00000) : lse - p.target_logit[mine_row];
+        p.row_loss[mine_row] = loss;
+        if (p.total != nullptr) part[0][slice] = make_float2(loss, t != p.ignore_index ? 1.0f : 0.0f);
+    }
+    if (p.total == nullptr) return;
+    __syncthreads();
+    if (slice == 0) {
+        float2 v = l < p.rows ? part[0][l] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        if (l == 0) *p.total = p.mean ? (v.y > 0.0f ? v.x / v.y : 0.0f) : v.x;
+    }
 }
 
+// All threads of a block of 32 warps: `join` over every thread's v, in a fixed order.
 template <typename T, typename F>
 __device__ __forceinline__ T block_join(T v, T* scratch, F join) {
 #pragma unroll
@@ -168,28 +206,33 @@ __device__ __forceinline__ T block_join(T v, T* scratch, F join) {
     __syncthreads();
     if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = scratch[0];
-    for (int i = 1; i < (int)(blockDim.x >> 5); ++i) v = join(v, scratch[i]);
+    v = scratch[threadIdx.x & 31];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
 
 // loss = sum of the rows' losses, over the rows that count when mean.  One
-// block; each thread sums its rows in order, in fp64 (rows / 1024 additions).
+// block; each thread sums every 1024th row with Kahan's compensation, then
+// pairwise (fp64, which this GPU runs at a small fraction of fp32's rate, took 14.5
+// us here; this takes 3).
 __global__ void __launch_bounds__(1024) layer_loss_sum_kernel(const float* row_loss, const long long* target, float* loss,
                                                              int rows, long long ignore_index, int mean) {
-    __shared__ double dsum[32];
-    __shared__ int isum[32];
+    __shared__ float fscratch[32];
+    __shared__ int iscratch[32];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    double s = 0.0;
+    float s = 0.0f, lost = 0.0f;
     int n = 0;
     for (int r = threadIdx.x; r < rows; r += 1024) {
-        s += (double)row_loss[r];
+        const float y = __fsub_rn(row_loss[r], lost), t = __fadd_rn(s, y);
+        lost = __fsub_rn(__fsub_rn(t, s), y);
+        s = t;
         n += target[r] != ignore_index;
     }
-    s = block_join(s, dsum, [](double a, double b) { return a + b; });
-    n = block_join(n, isum, [](int a, int b) { return a + b; });
-    if (threadIdx.x == 0) *loss = (float)(mean ? (n > 0 ? s / n : 0.0) : s);
+    s = block_join(s, fscratch, [](float a, float b) { return a + b; });
+    n = block_join(n, iscratch, [](int a, int b) { return a + b; });
+    if (threadIdx.x == 0) *loss = mean ? (n > 0 ? s / (float)n : 0.0f) : s;
 }
 
 // Each row's weight d loss / d row loss: grad[0] / rows that count (mean),

@@ -1,5 +1,6 @@
 // The library's one translation unit: the GEMM and the blocked add, and the
 // layer operators, which share its device facts, tuning config and status word.
+#include <algorithm>
 #include <initializer_list>
 #include <utility>
 

@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import struct
 
 import tensor_core_tiled_02_gb300 as _tc
@@ -25,38 +26,49 @@ import tensor_core_tiled_02_gb300 as _tc
 ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 # d of one piece of the vocabulary (linear_cross_entropy_backward) takes about this much
-LOSS_PIECE_BYTES = 256 << 20
+LOSS_PIECE_BYTES = 512 << 20
+_NO_WORKSPACE = bytes(16)
 
+# torch and what is asked of it on every call, looked up once (importing this module does not import torch)
 _torch = None
 _dtypes = None
+_raw_stream = None
 
 
 def _lazy():
-    global _torch, _dtypes
+    global _torch, _dtypes, _raw_stream
     if _torch is None:
         import torch
 
         _dtypes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+        # the current stream's handle without building a Stream object, where torch offers it
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
         _torch = torch
     return _torch
+
+
+def _side_stream(stream, index):
+    """(handle, torch stream) of a stream the caller names."""
+    if hasattr(stream, "cuda_stream"):
+        return stream.cuda_stream, stream
+    handle = int(stream)
+    return handle, (_torch.cuda.ExternalStream(handle, device=index) if handle else _torch.cuda.default_stream(index))
 
 
 class _Call:
     """The device and stream of one call."""
 
+    __slots__ = ("device", "index", "handle", "stream")
+
     def __init__(self, tensor, stream):
-        torch = _torch
         self.device = tensor.device
+        self.index = tensor.get_device()
         self.stream = None
         if stream is None:
-            self.handle = torch.cuda.current_stream(self.device).cuda_stream
-        elif hasattr(stream, "cuda_stream"):
-            self.handle = stream.cuda_stream
-            self.stream = stream
+            self.handle = _raw_stream(self.index)
         else:
-            self.handle = int(stream)
-            self.stream = torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else (
-                torch.cuda.default_stream(self.device))
+            self.handle, self.stream = _side_stream(stream, self.index)
 
     def empty(self, shape, dtype):
         """Memory that belongs to the call's stream."""
@@ -71,55 +83,72 @@ class _Call:
             return self.empty((rows, cols), dtype)
         return self.empty((rows, (cols + 7) // 8 * 8), dtype)[:, :cols]
 
-    def run(self, name, args, *more):
+    def run(self, name, args):
         fn = getattr(_tc.load_library(), name)
-        if _torch.cuda.current_device() == self.device.index:
-            rc = fn(args, *more)
+        if _torch.cuda.current_device() == self.index:
+            rc = fn(args, self.handle)
         else:
             with _torch.cuda.device(self.device):
-                rc = fn(args, *more)
+                rc = fn(args, self.handle)
         if rc != 0:
             raise _tc.GemmError(rc, name)
 
+    def run_with_workspace(self, name, args, *more):
+        """`args` lacks its last two fields, the workspace and its size."""
+        n = ctypes.c_size_t(0)
+        size = name + "_workspace"
+        rc = getattr(_tc.load_library(), size)(args + _NO_WORKSPACE, *more, ctypes.byref(n))
+        if rc != 0:
+            raise _tc.GemmError(rc, size)
+        nbytes = n.value
+        if nbytes == 0:
+            return self.run(name, args + _NO_WORKSPACE)
+        ws = self.empty((nbytes,), _torch.uint8)
+        self.run(name, args + struct.pack("2q", ws.data_ptr(), nbytes))
 
-def _check(name, t, rows, cols, dtype, device):
-    """A [rows, cols] CUDA matrix of `dtype`; its row stride."""
-    if t.dtype != dtype:
+
+def _check(name, t, rows, cols, dtype, index):
+    """A [rows, cols] matrix of `dtype` on device `index`; its row stride."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    return _stride(name, t)
-
-
-def _stride(name, t):
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, not on CUDA device {index}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+    return ld if rows > 1 else (cols + 7) // 8 * 8
 
 
 def _operand(name, t):
-    """The operand that fixes a call's type and device."""
+    """The operand that fixes a call's type and device: rows, columns, row stride."""
     if t.dim() != 2 or _dtypes.get(t.dtype, 2) == 2:
         raise ValueError(f"{name} must be a 2-D fp16 or bf16 tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _stride(name, t)
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name}'s rows must be contiguous")
+    return rows, cols, ld if rows > 1 else (cols + 7) // 8 * 8
+
+
+def _vector(name, t, n, dtype, index):
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} [{n}] tensor on CUDA device {index}")
+    return t.data_ptr()
 
 
 def _act(act):
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(k for k in ACTS if k)}, got {act!r}")
-    return ACTS[act]
+    return code
 
 
-def _size(name, args, *more):
-    n = ctypes.c_size_t(0)
-    rc = getattr(_tc.load_library(), name)(args, *more, ctypes.byref(n))
-    if rc != 0:
-        raise _tc.GemmError(rc, name)
-    return n.value
+def _pitch(cols):
+    return (cols + 7) // 8 * 8
 
 
 def linear(x, w, bias=None, act=None, residual=None, save_preact=False, out=None, stream=None):
@@ -131,28 +160,21 @@ def linear(x, w, bias=None, act=None, residual=None, save_preact=False, out=None
     """
     torch = _lazy()
     code = _act(act)
-    ldx = _operand("x", x)
-    dt, dev = x.dtype, x.device
-    tokens, k = x.shape
-    if w.dim() != 2:
-        raise ValueError("w must be 2-D")
+    tokens, k, ldx = _operand("x", x)
+    dt, dev = x.dtype, x.get_device()
+    if w.dim() != 2 or w.shape[1] < 1 or k < 1:
+        raise ValueError("w must be 2-D and not empty")
     n = w.shape[1]
     ldw = _check("w", w, k, n, dt, dev)
-    if bias is not None and (bias.dtype != dt or bias.shape != (n,) or bias.device != dev or not bias.is_contiguous()):
-        raise ValueError(f"bias must be a contiguous {dt} [{n}] tensor on {dev}")
+    pbias = _vector("bias", bias, n, dt, dev) if bias is not None else 0
     ldr = _check("residual", residual, tokens, n, dt, dev) if residual is not None else 0
     call = _Call(x, stream)
     y = out if out is not None else call.matrix(tokens, n, dt)
-    ldy = _check("out", y, tokens, n, dt, dev)
+    ldy = _check("out", y, tokens, n, dt, dev) if out is not None else _pitch(n)
     pre = call.matrix(tokens, n, dt) if save_preact else None
-    if tokens and k and n:
-        call.run("linear_forward", struct.pack(
-            "16q", x.data_ptr(), w.data_ptr(), bias.data_ptr() if bias is not None else 0,
-            residual.data_ptr() if residual is not None else 0, y.data_ptr(), pre.data_ptr() if save_preact else 0,
-            ldx, ldw, ldr, ldy, _stride("preact", pre) if save_preact else 0, tokens, k, n, _dtypes[dt], code),
-            call.handle)
-    elif tokens and n:
-        raise ValueError("x and w must have k >= 1")
+    call.run("linear_forward", struct.pack(
+        "16q", x.data_ptr(), w.data_ptr(), pbias, residual.data_ptr() if residual is not None else 0, y.data_ptr(),
+        pre.data_ptr() if save_preact else 0, ldx, ldw, ldr, ldy, _pitch(n), tokens, k, n, _dtypes[dt], code))
     return (y, pre) if save_preact else y
 
 
@@ -164,9 +186,8 @@ def linear_backward(dy, x, w, act=None, preact=None, bias=False, stream=None):
     """
     torch = _lazy()
     code = _act(act)
-    ldx = _operand("x", x)
-    dt, dev = x.dtype, x.device
-    tokens, k = x.shape
+    tokens, k, ldx = _operand("x", x)
+    dt, dev = x.dtype, x.get_device()
     if w.dim() != 2 or w.shape[1] < 1 or k < 1:
         raise ValueError("w must be 2-D and not empty")
     n = w.shape[1]
@@ -179,14 +200,9 @@ def linear_backward(dy, x, w, act=None, preact=None, bias=False, stream=None):
     dx, dw = call.matrix(tokens, k, dt), call.matrix(k, n, dt)
     dbias = call.empty((n,), dt) if bias else None
 
-    def pack(ws, nbytes):
-        return struct.pack("20q", dy.data_ptr(), x.data_ptr(), w.data_ptr(), preact.data_ptr() if code else 0,
-                           dx.data_ptr(), dw.data_ptr(), dbias.data_ptr() if bias else 0, ws, lddy, ldx, ldw, ldp,
-                           _stride("dx", dx), _stride("dw", dw), tokens, k, n, _dtypes[dt], code, nbytes)
-
-    nbytes = _size("linear_backward_workspace", pack(0, 0))
-    ws = call.empty((nbytes,), torch.uint8) if nbytes else None
-    call.run("linear_backward", pack(ws.data_ptr() if nbytes else 0, nbytes), call.handle)
+    call.run_with_workspace("linear_backward", struct.pack(
+        "18q", dy.data_ptr(), x.data_ptr(), w.data_ptr(), preact.data_ptr() if code else 0, dx.data_ptr(), dw.data_ptr(),
+        dbias.data_ptr() if bias else 0, lddy, ldx, ldw, ldp, _pitch(k), _pitch(n), tokens, k, n, _dtypes[dt], code))
     return dx, dw, dbias
 
 
@@ -199,9 +215,8 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu", residual=None, save=False, ou
     """
     _lazy()
     code = _act(act)
-    ldx = _operand("x", x)
-    dt, dev = x.dtype, x.device
-    tokens, dim = x.shape
+    tokens, dim, ldx = _operand("x", x)
+    dt, dev = x.dtype, x.get_device()
     if w_gate.dim() != 2 or w_down.dim() != 2 or not (dim and w_gate.shape[1] and w_down.shape[1]):
         raise ValueError("the weights must be 2-D and not empty")
     ffn, dim_out = w_gate.shape[1], w_down.shape[1]
@@ -210,15 +225,15 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu", residual=None, save=False, ou
     ldr = _check("residual", residual, tokens, dim_out, dt, dev) if residual is not None else 0
     call = _Call(x, stream)
     y = out if out is not None else call.matrix(tokens, dim_out, dt)
-    ldy = _check("out", y, tokens, dim_out, dt, dev)
+    ldy = _check("out", y, tokens, dim_out, dt, dev) if out is not None else _pitch(dim_out)
     hidden = call.matrix(tokens, ffn, dt)
     gate, up = (call.matrix(tokens, ffn, dt), call.matrix(tokens, ffn, dt)) if save else (None, None)
-    ldh = _stride("hidden", hidden)
+    ldh = _pitch(ffn)
     call.run("gated_ffn_forward", struct.pack(
         "24q", x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(),
         residual.data_ptr() if residual is not None else 0, y.data_ptr(), hidden.data_ptr(),
         gate.data_ptr() if save else 0, up.data_ptr() if save else 0, ldx, ldg, ldu, ldd, ldr, ldy, ldh, ldh, ldh,
-        tokens, dim, ffn, dim_out, _dtypes[dt], code), call.handle)
+        tokens, dim, ffn, dim_out, _dtypes[dt], code))
     return (y, gate, up, hidden) if save else y
 
 
@@ -227,9 +242,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, act="silu"
     ``gated_ffn(..., save=True)`` returned.  The residual's gradient is ``dy`` itself."""
     torch = _lazy()
     code = _act(act)
-    ldx = _operand("x", x)
-    dt, dev = x.dtype, x.device
-    tokens, dim = x.shape
+    tokens, dim, ldx = _operand("x", x)
+    dt, dev = x.dtype, x.get_device()
     if w_gate.dim() != 2 or w_down.dim() != 2 or not (dim and w_gate.shape[1] and w_down.shape[1]):
         raise ValueError("the weights must be 2-D and not empty")
     ffn, dim_out = w_gate.shape[1], w_down.shape[1]
@@ -240,15 +254,9 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, gate, up, hidden, act="silu"
     call = _Call(x, stream)
     grads = (call.matrix(tokens, dim, dt), call.matrix(dim, ffn, dt), call.matrix(dim, ffn, dt),
              call.matrix(ffn, dim_out, dt))
-    ptrs = [t.data_ptr() for t in (dy, x, w_gate, w_up, w_down, gate, up, hidden) + grads]
-    rest = lds + [_stride("gradient", g) for g in grads] + [tokens, dim, ffn, dim_out, _dtypes[dt], code]
-
-    def pack(ws, nbytes):
-        return struct.pack("32q", *ptrs, ws, *rest, nbytes)
-
-    nbytes = _size("gated_ffn_backward_workspace", pack(0, 0))
-    ws = call.empty((nbytes,), torch.uint8) if nbytes else None
-    call.run("gated_ffn_backward", pack(ws.data_ptr() if nbytes else 0, nbytes), call.handle)
+    call.run_with_workspace("gated_ffn_backward", struct.pack(
+        "30q", *[t.data_ptr() for t in (dy, x, w_gate, w_up, w_down, gate, up, hidden) + grads], *lds,
+        _pitch(dim), _pitch(ffn), _pitch(ffn), _pitch(dim_out), tokens, dim, ffn, dim_out, _dtypes[dt], code))
     return grads
 
 
@@ -256,14 +264,12 @@ def _loss_operands(h, w, target, reduction):
     torch = _lazy()
     if reduction not in REDUCTIONS:
         raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
-    ldh = _operand("h", h)
-    tokens, dim = h.shape
+    tokens, dim, ldh = _operand("h", h)
     if w.dim() != 2 or w.shape[0] < 1 or dim < 1:
         raise ValueError("w must be [vocabulary, features] and not empty")
-    ldw = _check("w", w, w.shape[0], dim, h.dtype, h.device)
-    if target.dtype != torch.int64 or target.shape != (tokens,) or target.device != h.device or not target.is_contiguous():
-        raise ValueError(f"target must be a contiguous int64 [{tokens}] tensor on {h.device}")
-    return ldh, ldw, tokens, dim, w.shape[0]
+    dev, vocab = h.get_device(), w.shape[0]
+    ldw = _check("w", w, vocab, dim, h.dtype, dev)
+    return ldh, ldw, tokens, dim, vocab, _vector("target", target, tokens, torch.int64, dev)
 
 
 def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean", stream=None):
@@ -275,18 +281,14 @@ def linear_cross_entropy(h, w, target, ignore_index=-100, reduction="mean", stre
     which the backward pass reads.  The logits never reach memory.
     """
     torch = _lazy()
-    ldh, ldw, tokens, dim, vocab = _loss_operands(h, w, target, reduction)
+    ldh, ldw, tokens, dim, vocab, ptarget = _loss_operands(h, w, target, reduction)
     call = _Call(h, stream)
     loss = call.empty((tokens,) if reduction == "none" else (), torch.float32)
     lse = call.empty((tokens,), torch.float32)
 
-    def pack(ws, nbytes):
-        return struct.pack("15q", h.data_ptr(), w.data_ptr(), target.data_ptr(), loss.data_ptr(), lse.data_ptr(), ws,
-                           ldh, ldw, tokens, dim, vocab, _dtypes[h.dtype], ignore_index, REDUCTIONS[reduction], nbytes)
-
-    nbytes = _size("linear_cross_entropy_workspace", pack(0, 0))
-    ws = call.empty((nbytes,), torch.uint8) if nbytes else None
-    call.run("linear_cross_entropy", pack(ws.data_ptr() if nbytes else 0, nbytes), call.handle)
+    call.run_with_workspace("linear_cross_entropy", struct.pack(
+        "13q", h.data_ptr(), w.data_ptr(), ptarget, loss.data_ptr(), lse.data_ptr(), ldh, ldw, tokens, dim, vocab,
+        _dtypes[h.dtype], ignore_index, REDUCTIONS[reduction]))
     return loss, lse
 
 
@@ -300,27 +302,21 @@ def linear_cross_entropy_backward(grad_loss, h, w, target, lse, ignore_index=-10
     h has to be finite in ignored rows too: their weight in dw is 0, not absent.
     """
     torch = _lazy()
-    ldh, ldw, tokens, dim, vocab = _loss_operands(h, w, target, reduction)
-    dev = h.device
+    ldh, ldw, tokens, dim, vocab, ptarget = _loss_operands(h, w, target, reduction)
+    dev = h.get_device()
     each = reduction == "none"
-    if grad_loss.dtype != torch.float32 or grad_loss.device != dev or grad_loss.numel() != (tokens if each else 1) or (
-            not grad_loss.is_contiguous()):
-        raise ValueError(f"grad_loss must be fp32 on {dev}, {'[tokens]' if each else 'one value'}")
-    if lse.dtype != torch.float32 or lse.shape != (tokens,) or lse.device != dev or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 [{tokens}] tensor on {dev}")
+    if grad_loss.dtype is not torch.float32 or grad_loss.get_device() != dev or not grad_loss.is_contiguous() or (
+            grad_loss.numel() != (tokens if each else 1)):
+        raise ValueError(f"grad_loss must be fp32 on CUDA device {dev}, {'[tokens]' if each else 'one value'}")
+    plse = _vector("lse", lse, tokens, torch.float32, dev)
     if piece is None:
         piece = max(256, LOSS_PIECE_BYTES // (2 * max(tokens, 1)) // 256 * 256)
     call = _Call(h, stream)
     dh, dw = call.matrix(tokens, dim, h.dtype), call.matrix(vocab, dim, h.dtype)
 
-    def pack(ws, nbytes):
-        return struct.pack("19q", h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(), grad_loss.data_ptr(),
-                           dh.data_ptr(), dw.data_ptr(), ws, ldh, ldw, _stride("dh", dh), _stride("dw", dw), tokens,
-                           dim, vocab, _dtypes[h.dtype], ignore_index, REDUCTIONS[reduction], nbytes)
-
-    nbytes = _size("linear_cross_entropy_backward_workspace", pack(0, 0), int(piece))
-    ws = call.empty((nbytes,), torch.uint8) if nbytes else None
-    call.run("linear_cross_entropy_backward", pack(ws.data_ptr() if nbytes else 0, nbytes), call.handle)
+    call.run_with_workspace("linear_cross_entropy_backward", struct.pack(
+        "17q", h.data_ptr(), w.data_ptr(), ptarget, plse, grad_loss.data_ptr(), dh.data_ptr(), dw.data_ptr(), ldh, ldw,
+        _pitch(dim), _pitch(dim), tokens, dim, vocab, _dtypes[h.dtype], ignore_index, REDUCTIONS[reduction]), int(piece))
     return dh, dw
 
 
@@ -333,29 +329,34 @@ def clip_grad_norm(grads, max_norm, out=None, eps=1e-6, stream=None):
     """
     torch = _lazy()
     grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"{len(grads)} gradients, but {len(outs)} outputs")
     if not grads:
         raise ValueError("no gradients")
-    dev = grads[0].device
-    codes = []
-    for g, o in zip(grads, outs):
-        code = _dtypes.get(g.dtype)
-        if code is None or not g.is_cuda or g.device != dev or not g.is_contiguous():
-            raise ValueError("gradients must be dense fp16, bf16 or fp32 tensors on one CUDA device")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.device != dev or not o.is_contiguous()):
-            raise ValueError("out must match the gradients")
-        codes.append(code)
+    # hundreds of tensors are common: each question is put to all of them in one sweep
+    tensor = torch.Tensor
     call = _Call(grads[0], stream)
+    kinds, counts = list(map(operator.attrgetter("dtype"), grads)), array.array("q", map(tensor.numel, grads))
+    if out is not None:
+        out = list(out)
+    for name, ts in (("gradients", grads),) if out is None else (("gradients", grads), ("out", out)):
+        if set(map(tensor.get_device, ts)) != {call.index} or call.index < 0 or not all(map(tensor.is_contiguous, ts)):
+            raise ValueError(f"{name} must be dense tensors on one CUDA device")
+    src = array.array("q", map(tensor.data_ptr, grads))
+    dst = src
+    if out is not None:
+        if list(map(operator.attrgetter("dtype"), out)) != kinds or array.array("q", map(tensor.numel, out)) != counts:
+            raise ValueError("out must have the gradients' sizes and types")
+        dst = array.array("q", map(tensor.data_ptr, out))
+    try:
+        codes = array.array("i", map(_dtypes.__getitem__, kinds))
+    except KeyError as e:
+        raise ValueError(f"gradients must be fp16, bf16 or fp32, got {e.args[0]}") from None
     norm = call.empty((), torch.float32)
-    src = array.array("q", [g.data_ptr() for g in grads])
-    dst = src if out is None else array.array("q", [o.data_ptr() for o in outs])
-    count = array.array("q", [g.numel() for g in grads])
-    kinds = array.array("i", codes)
-    nbytes = _size("grad_clip_workspace", len(grads))
-    ws = call.empty((nbytes,), torch.uint8)
-    call.run("grad_clip", struct.pack("7q2dq", src.buffer_info()[0], dst.buffer_info()[0], count.buffer_info()[0],
-                                      kinds.buffer_info()[0], norm.data_ptr(), ws.data_ptr(), len(grads), max_norm, eps,
-                                      nbytes), call.handle)
+    n = ctypes.c_size_t(0)
+    rc = _tc.load_library().grad_clip_workspace(len(grads), ctypes.byref(n))
+    if rc != 0:
+        raise _tc.GemmError(rc, "grad_clip_workspace")
+    ws = call.empty((n.value,), torch.uint8)
+    call.run("grad_clip", struct.pack("7q2dq", src.buffer_info()[0], dst.buffer_info()[0], counts.buffer_info()[0],
+                                      codes.buffer_info()[0], norm.data_ptr(), ws.data_ptr(), len(grads), max_norm, eps,
+                                      n.value))
     return norm
