@@ -8,12 +8,80 @@
 
 namespace tcgemm {
 
+// ---- two fp32 values at a time -----------------------------------------------------------
+// fma.rn.f32x2 and its kin do two in one issue slot: the slope pass is bound by issue
+// (GELU's slope is some 25 operations an element one by one) before HBM.
+
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 parts(F2 a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 both(float c) { return f2(c, c); }
+// Approximations to about 1e-7 of the value; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// act_slope of two values; GELU's by the formula of normal_cdf, its coefficients halved.
+template <int ACT>
+__device__ __forceinline__ F2 act_slope2(F2 x) {
+    if constexpr (ACT == kActGelu) {
+        F2 ax;
+        ax.v = x.v & 0x7FFFFFFF7FFFFFFFull;
+        const float2 den = parts(fma2(both(0.3275911f * 0.70710678118654752f), ax, both(1.0f)));
+        const F2 t = f2(rcp_approx(den.x), rcp_approx(den.y));
+        const float2 y = parts(mul2(mul2(x, x), both(-0.72134752044448170f)));
+        const F2 e = f2(ex2_approx(y.x), ex2_approx(y.y));
+        F2 q = fma2(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
+        q = fma2(t, q, both(0.5f * 1.421413741f));
+        q = fma2(t, q, both(-0.5f * 0.284496736f));
+        q = fma2(t, q, both(0.5f * 0.254829592f));
+        const F2 tail = mul2(q, mul2(t, e));
+        const float2 lo = parts(tail), hi = parts(fma2(tail, both(-1.0f), both(1.0f))), xs = parts(x);
+        const F2 cdf = f2(xs.x < 0.0f ? lo.x : hi.x, xs.y < 0.0f ? lo.y : hi.y);
+        return fma2(mul2(x, both(0.39894228040143268f)), e, cdf);
+    }
+    const float2 xs = parts(x);
+    return f2(act_slope<ACT>(xs.x), act_slope<ACT>(xs.y));
+}
+
 // ---- linear layer: dpre = dy act'(pre), column sums of dpre ------------------------
 //
 // A block takes kSlopeRows rows x 256 columns: 32 groups of 8 columns (16
 // bytes) x 8 rows at a time.  Reads dy and pre once, writes dpre once; the
 // block's column sums (of the unrounded products) go to partial[row block][N].
-constexpr int kSlopeRows = 32;
+constexpr int kSlopeRows = 64;
 constexpr int kSlopeCols = 256;
 
 struct SlopeParams {
@@ -27,21 +95,21 @@ struct SlopeParams {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(256) layer_slope_kernel(const SlopeParams p) {
+__global__ void __launch_bounds__(256, 5) layer_slope_kernel(const SlopeParams p) {
     __shared__ float sums[8][kSlopeCols];
     const int cg = threadIdx.x & 31, rl = threadIdx.x >> 5;
     const int cb = blockIdx.x % p.col_blocks, rb = blockIdx.x / p.col_blocks;
     const int col = cb * kSlopeCols + cg * 8;
     const int r0 = rb * kSlopeRows;
     const int r1 = min(p.rows, r0 + kSlopeRows);
-    float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    F2 acc[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     if (col < p.cols) {
         const bool whole = col + 8 <= p.cols;
         with_act(p.pre ? p.act : kActNone, [&](auto tag) {
             constexpr int ACT = decltype(tag)::value;
-            constexpr int U = 4;  // rows under way per thread: 16-byte loads enough to keep HBM busy
+            constexpr int U = 2;  // rows under way per thread
             if (whole) {
                 for (int rb = r0 + rl; rb < r1; rb += 8 * U) {
                     uint4 w[U], z[U];
@@ -61,15 +129,15 @@ __global__ void __launch_bounds__(256) layer_slope_kernel(const SlopeParams p) {
                         uint32_t os[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float2 f = unpack2<DT>(ws[e]);
+                            const float2 d = unpack2<DT>(ws[e]);
+                            F2 f = f2(d.x, d.y);
                             if constexpr (ACT != kActNone) {
                                 const float2 g = unpack2<DT>(zs[e]);
-                                f.x *= act_slope<ACT>(g.x);
-                                f.y *= act_slope<ACT>(g.y);
+                                f = mul2(f, act_slope2<ACT>(f2(g.x, g.y)));
                             }
-                            acc[2 * e] += f.x;
-                            acc[2 * e + 1] += f.y;
-                            os[e] = pack2<DT>(f.x, f.y);
+                            acc[e] = add2(acc[e], f);
+                            const float2 o = parts(f);
+                            os[e] = pack2<DT>(o.x, o.y);
                         }
                         if (p.dpre)
                             *reinterpret_cast<uint4*>(static_cast<unsigned short*>(p.dpre) + r * p.ld_dpre + col) =
@@ -82,14 +150,18 @@ __global__ void __launch_bounds__(256) layer_slope_kernel(const SlopeParams p) {
                         float d = load1<DT>(p.dy, r * p.ld_dy + col + e);
                         if constexpr (ACT != kActNone) d *= act_slope<ACT>(load1<DT>(p.pre, r * p.ld_pre + col + e));
                         if (p.dpre) static_cast<unsigned short*>(p.dpre)[r * p.ld_dpre + col + e] = pack1<DT>(d);
-                        acc[e] += d;
+                        acc[e >> 1] = add2(acc[e >> 1], e & 1 ? f2(0.0f, d) : f2(d, 0.0f));
                     }
             }
         });
     }
     if (p.partial == nullptr) return;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[rl][cg * 8 + e] = acc[e];
+    for (int e = 0; e < 4; ++e) {
+        const float2 a = parts(acc[e]);
+        sums[rl][cg * 8 + 2 * e] = a.x;
+        sums[rl][cg * 8 + 2 * e + 1] = a.y;
+    }
     __syncthreads();
     const int c = cb * kSlopeCols + threadIdx.x;
     if (c < p.cols) {

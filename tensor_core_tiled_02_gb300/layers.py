@@ -28,6 +28,7 @@ REDUCTIONS = {"none": 0, "mean": 1, "sum": 2}
 # d of one piece of the vocabulary (linear_cross_entropy_backward) takes about this much
 LOSS_PIECE_BYTES = 512 << 20
 _NO_WORKSPACE = bytes(16)
+_DTYPE = operator.attrgetter("dtype")
 
 # torch and what is asked of it on every call, looked up once (importing this module does not import torch)
 _torch = None
@@ -334,22 +335,20 @@ def clip_grad_norm(grads, max_norm, out=None, eps=1e-6, stream=None):
     # hundreds of tensors are common: each question is put to all of them in one sweep
     tensor = torch.Tensor
     call = _Call(grads[0], stream)
-    kinds, counts = list(map(operator.attrgetter("dtype"), grads)), array.array("q", map(tensor.numel, grads))
-    if out is not None:
-        out = list(out)
-    for name, ts in (("gradients", grads),) if out is None else (("gradients", grads), ("out", out)):
+    out = grads if out is None else list(out)
+    kinds, counts = list(map(_DTYPE, grads)), list(map(tensor.numel, grads))
+    for name, ts in (("gradients", grads),) if out is grads else (("gradients", grads), ("out", out)):
         if set(map(tensor.get_device, ts)) != {call.index} or call.index < 0 or not all(map(tensor.is_contiguous, ts)):
             raise ValueError(f"{name} must be dense tensors on one CUDA device")
-    src = array.array("q", map(tensor.data_ptr, grads))
-    dst = src
-    if out is not None:
-        if list(map(operator.attrgetter("dtype"), out)) != kinds or array.array("q", map(tensor.numel, out)) != counts:
-            raise ValueError("out must have the gradients' sizes and types")
-        dst = array.array("q", map(tensor.data_ptr, out))
+    if out is not grads and (list(map(_DTYPE, out)) != kinds or list(map(tensor.numel, out)) != counts):
+        raise ValueError("out must have the gradients' sizes and types")
     try:
-        codes = array.array("i", map(_dtypes.__getitem__, kinds))
+        codes = array.array("i", [_dtypes[k] for k in kinds])
     except KeyError as e:
         raise ValueError(f"gradients must be fp16, bf16 or fp32, got {e.args[0]}") from None
+    src = array.array("q", list(map(tensor.data_ptr, grads)))
+    dst = src if out is grads else array.array("q", list(map(tensor.data_ptr, out)))
+    counts = array.array("q", counts)
     norm = call.empty((), torch.float32)
     n = ctypes.c_size_t(0)
     rc = _tc.load_library().grad_clip_workspace(len(grads), ctypes.byref(n))
