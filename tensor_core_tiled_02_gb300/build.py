@@ -3,7 +3,9 @@
 nvcc compiles the kernels for sm_103a only (``-gencode
 arch=compute_103a,code=sm_103a``) with the CUDA runtime linked statically, so
 the library loads without a GPU and needs no libcuda at link time (the one
-driver entry point it uses is fetched at run time).
+driver entry point it uses is fetched at run time).  g++ compiles the layer
+operators' torch binding (csrc/layer_binding.cpp -> _layers.so) against the
+torch that is installed; it holds no arithmetic.
 """
 from __future__ import annotations
 
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtcgemm.so")
 SOURCES = [os.path.join(CSRC, "tcgemm.cu")]
+BINDING = os.path.join(PKG, "_layers.so")
+BINDING_SOURCE = os.path.join(CSRC, "layer_binding.cpp")
 GENCODE = "arch=compute_103a,code=sm_103a"
 
 # Debug variants of the same sources, each its own library beside the product:
@@ -55,6 +59,28 @@ def build(verbose_ptxas: bool = False, out: str | None = None, extra=(), variant
     return out
 
 
+def build_binding(out: str | None = None) -> str:
+    """The torch binding of the layer operators, for this interpreter and torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    out = out or BINDING
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc_path())))
+    include = [*cpp_extension.include_paths(), os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+                    *[a for d in include for a in ("-isystem", d)], "-I", INCLUDE, "-o", out, BINDING_SOURCE,
+                    "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"], check=True)
+    return out
+
+
+def binding_needs_build() -> bool:
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "layer_ops.h"), os.path.join(INCLUDE, "gemm_f16.h")]
+    return not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
+
+
 def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
@@ -66,4 +92,5 @@ def needs_build() -> bool:
 
 if __name__ == "__main__":
     v = next((a for a in sys.argv[1:] if a in VARIANTS), "")
+    print(build_binding())
     print(build(verbose_ptxas="-v" in sys.argv, variant=v))

@@ -308,11 +308,13 @@ __global__ void __launch_bounds__(1024) layer_loss_sum_kernel(const float* row_l
 }
 
 // Each row's weight d loss / d row loss: grad[0] / rows that count (mean),
-// grad[0] (sum) or grad[row] (none), times a power of two that puts the largest
-// in [2^14, 2^15): p times the weight then keeps fp16's full precision down to
-// p = 2^-28 (unscaled, 1 / tokens times p is subnormal at once).  Ignored
-// rows weigh 0; a target that is no word makes its row's weight NaN.  unscale =
-// the power's inverse, for the products' epilogues.  One block.
+// grad[0] (sum) or grad[row] (none), relative to the largest and times 2^14: p
+// times the weight then keeps fp16's full precision down to p = 2^-28 (unscaled, 1 /
+// tokens times p is subnormal at once), and where all weights are alike a target's
+// entry p - 1 rounds as itself, near -1 to next to nothing (with a power of two alone
+// every target's entry took the same rounding of the weight, up to 0.4 % in bf16).
+// Ignored rows weigh 0; a target that is no word makes its row's weight NaN.
+// unscale = the largest weight over 2^14, for the products' epilogues.  One block.
 __global__ void __launch_bounds__(1024) layer_loss_weights_kernel(const float* grad, const long long* target, float* weight,
                                                                   float* unscale, int rows, long long vocab,
                                                                   long long ignore_index, int reduction) {
@@ -330,17 +332,14 @@ __global__ void __launch_bounds__(1024) layer_loss_weights_kernel(const float* g
     n = block_join(n, iscratch, [](int a, int b) { return a + b; });
     const float each = reduction == 0 ? 0.0f : reduction == 1 ? grad[0] / (float)max(n, 1) : grad[0];
     most = reduction == 0 ? block_join(most, fscratch, [](float a, float b) { return fmaxf(a, b); }) : fabsf(each);
-    // 2^e <= most < 2^(e+1); 0, inf and NaN are left unscaled
-    const int e = (int)((__float_as_uint(most) >> 23) & 255) - 127;
-    const bool scalable = most > 0.0f && e > -127 && e < 128;
-    const int up = scalable ? min(max(14 - e, -100), 100) : 0;
-    const float scale = __uint_as_float((uint32_t)(127 + up) << 23);
+    const bool scalable = most > 0.0f && most < INFINITY;  // else (0, inf, NaN) as it is
     for (int r = threadIdx.x; r < rows; r += 1024) {
         const long long t = target[r];
-        const float w = (reduction == 0 ? grad[r] : each) * scale;
-        weight[r] = t == ignore_index ? 0.0f : t < 0 || t >= vocab ? __int_as_float(0x7FC00000) : w;
+        const float w = reduction == 0 ? grad[r] : each;
+        weight[r] = t == ignore_index ? 0.0f
+                    : t < 0 || t >= vocab ? __int_as_float(0x7FC00000) : scalable ? __fdiv_rn(w, most) * 16384.0f : w;
     }
-    if (threadIdx.x == 0) *unscale = __uint_as_float((uint32_t)(127 - up) << 23);
+    if (threadIdx.x == 0) *unscale = scalable ? most * (1.0f / 16384.0f) : 1.0f;
 }
 
 }  // namespace tcgemm
