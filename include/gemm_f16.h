@@ -267,7 +267,8 @@ const char *gemm_f16_strerror(int code);
  * GEMM_ERR_DEVICE_TIMEOUT.  *site (if not NULL) receives which wait gave up
  * first (1 producer/empty slot, 2 MMA/full slot, 3 MMA/free accumulator,
  * 4 epilogue/ready accumulator, 5 drain, 6 split-K partner ready, 7 split-K
- * partials received, 8 stream-K partial flag), 0 if none.  reset != 0 clears it.
+ * partials received, 8 stream-K partial flag, 12 a tile the epilogue of a
+ * layer operator loads), 0 if none.  reset != 0 clears it.
  */
 int gemm_f16_device_status(int *site, int reset);
 

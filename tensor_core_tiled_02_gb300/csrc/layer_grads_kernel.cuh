@@ -128,6 +128,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    auto stage_ok = [&](int st) {
+        const uint32_t bars = (uint32_t)L::kNumBars * 8u;
+        return holds(bar0, bars, empty_bar(st), 8) && holds(bar0, bars, full_bar(st), 8) &&
+               holds(sA, (uint32_t)(S * L::kABytes), sA + st * L::kABytes, L::kABytes) &&
+               holds(sB, (uint32_t)(S * L::kBBytes), sB + st * L::kBBytes, L::kBBytes);
+    };
+    (void)stage_ok;
     const int pair = blockIdx.x >> 1;
     const int P = gridDim.x >> 1;
 
@@ -145,6 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int m0 = mb * 256 + (int)rank * 128, n0 = nb * PN + (int)rank * kHalf;
                 const int KB = q.k_steps, k_switch = q.k_switch, a_mn = q.a_mn, b_mn = q.b_mn;
                 for (int kb = 0; kb < KB; ++kb) {
+                    if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
+                        ok = false;
+                        break;
+                    }
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) {
                         ok = false;
                         break;
@@ -204,6 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t b_step = q.b_mn ? kSliceStep<true> : kSliceStep<false>;
                 const int KB = q.k_steps;
                 for (int kb = 0; kb < KB; ++kb) {
+                    if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
+                        ok = false;
+                        break;
+                    }
                     if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
                         ok = false;
                         break;
@@ -256,6 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t buf = stg + (n_chunk & 3) * 4096u;
+                if (!TC_CHECK(holds(sC, (uint32_t)(L::kWarps * L::kWarpStaging), buf, 4096u) && acc * PN + PN <= L::kTmemCols,
+                              kSiteSmemBounds))
+                    break;
                 if (lane == 0) ptx::bulk_wait_group_read<3>();
                 __syncwarp();
                 uint32_t v[64];

@@ -194,6 +194,15 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
     ptx::cluster_wait();
     ptx::tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // the parts of the carve-up, for the bounds-check build's tests
+    const uint32_t bars = (uint32_t)L::kNumBars * 8u, staging_all = (uint32_t)(L::kWarps * L::kWarpStaging);
+    (void)bars, (void)staging_all;
+    auto stage_ok = [&](int st) {
+        return holds(bar0, bars, empty_bar(st), 8) && holds(bar0, bars, full_bar(st), 8) &&
+               holds(sA, (uint32_t)(S * L::kABytes), sA + st * L::kABytes, L::kABytes) &&
+               holds(sB, (uint32_t)(S * L::kBBytes), sB + st * L::kBBytes, L::kBBytes);
+    };
+    (void)stage_ok;
 
     // this cluster's tiles: cluster, cluster + clusters, ... (SPLIT: one), and its K steps [kb0, kb1)
     const int cluster = SPLIT ? (int)blockIdx.x / (2 * p.split) : (int)blockIdx.x >> 1;
@@ -221,6 +230,10 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                 // kEpiGate: this CTA's columns are the tile's PN/2 of one weight
                 const int n0 = EPI == kEpiGate ? nb * kHalf : nb * PN + (int)rank * kHalf;
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
+                        ok = false;
+                        break;
+                    }
                     if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) {
                         ok = false;
                         break;
@@ -278,7 +291,15 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
+                if (!TC_CHECK(acc * PN + PN <= L::kTmemCols, kSiteTmemBounds)) {
+                    ok = false;
+                    break;
+                }
                 for (int kb = kb0; kb < kb1; ++kb) {
+                    if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
+                        ok = false;
+                        break;
+                    }
                     if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
                         ok = false;
                         break;
@@ -471,6 +492,12 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                         p.target_logit[row] = tv;
                     }
                 } else {
+                    // (kEpiGate that keeps g and u: three buffers)
+                    if (!TC_CHECK(holds(sC, staging_all, buf0, two_bufs ? 8192u : EPI == kEpiGate && p.keep ? 12288u : 4096u),
+                                  kSiteSmemBounds)) {
+                        failed = true;
+                        break;
+                    }
                     if constexpr (kLoads) {
                         if (loads) {
                             if (!warp_wait(aux_bar(ew, n_chunk & 1), (n_chunk >> 1) & 1, abort_flag, p.wait_limit, kSiteAuxLoad,

@@ -152,6 +152,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 return second;
             };
             auto load_weights = [&](int kb, int st) {
+                if (!TC_CHECK(holds(ring, (uint32_t)(S * p.stage_bytes), ring + (uint32_t)(st * p.stage_bytes),
+                                    (uint32_t)p.stage_bytes),
+                              kSiteSmemBounds))
+                    return;
                 int k;
                 const int second = source(kb, k);
                 const uint32_t fb = full_bar(st);
@@ -228,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         // ---------------- this CTA's partial: TMEM -> shared memory ----------------
         // (the ring is idle: every load was consumed by an MMA, and every MMA is complete)
         const int q = warp & 3;
-        if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0) {
+        if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0 &&
+            TC_CHECK(kTiles * p.nt <= p.tmem_cols, kSiteTmemBounds)) {
             ptx::tc_fence_after();
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
             const uint32_t col = ring + (uint32_t)((q * 32 + lane) * 4);
