@@ -178,7 +178,8 @@ int linear_cross_entropy_backward_workspace(const loss_grad_args *args, long lon
  *   tensors   how many; src, dst, count, dtype are HOST arrays of that length, read
  *             during the call only
  *   src, dst  dense device arrays of count[i] entries of dtype[i] (fp16, bf16 or
- *             fp32), aligned to their type; dst[i] may be src[i] (in place)
+ *             fp32), aligned to their type; dst[i] may be src[i] (in place).
+ *             Different tensors may not overlap (not checked)
  *   norm      one fp32 on the device, or NULL
  * An infinite norm scales by 0 and a NaN norm by NaN, as the formula says.
  */

@@ -236,13 +236,95 @@ def test_deterministic_on_another_stream_and_in_a_graph():
             assert torch.equal(out, first[0])
 
 
-def test_wait_that_runs_out_is_reported():
+# Shapes at which the choice of kernel and split differs on a 152-SM part: tokens, k, n
+KINDS = [(8, 4096, 512),       # few tokens, 16 CTAs a weight tile
+         (3, 2048, 1024), (40, 4096, 14336),
+         (150, 1024, 4096),    # token tiles of one CTA an SM
+         (600, 1024, 1024),    # several token tiles
+         (256, 14336, 4096), (512, 4096, 4096), (500, 5000, 2050),   # pairs sharing a tile along K
+         (1500, 520, 4104), (5000, 264, 1032)]
+
+
+@pytest.mark.parametrize("shape", KINDS, ids=str)
+def test_linear_every_kernel(shape):
+    t, k, n = shape
+    d = Draw(t + n, F16)
+    x, w, b, r = d(t, k), d(k, n, scale=k ** -0.5), d(n)[:n].contiguous(), d(t, n)
+    pre, want = linear_want(x, w, b, "gelu", r)
+    y, p = tc.linear(x, w, bias=b, act="gelu", residual=r, save_preact=True)
+    check(y, want, F16, 1.0, "y")
+    check(p, pre, F16, 1.0, "preact")
+    again = tc.linear(x, w, bias=b, act="gelu", residual=r)
+    assert torch.equal(again, y)
+
+
+# tokens, k, n: dx and dw apart; together with dx the longer; with dw the longer; dw split along its tokens
+GRADS = [(40, 4096, 1024), (300, 8192, 2048), (700, 1024, 2056), (2001, 264, 1031), (4100, 520, 264), (8000, 256, 256),
+         (9000, 64, 520)]
+
+
+@pytest.mark.parametrize("shape", GRADS, ids=str)
+def test_linear_backward_every_kernel(shape):
+    t, k, n = shape
+    d = Draw(t * 3 + n, BF16)
+    x, w, dy = d(t, k), d(k, n, scale=k ** -0.5), d(t, n)
+    dx, dw, db = tc.linear_backward(dy, x, w, bias=True)
+    check(dx, V(dy) @ V(w).T, BF16, 1.0, "dx")
+    check(dw, V(x).T @ V(dy), BF16, 1.0, "dw")
+    check(db[None], V(torch.ones(1, t, device="cuda", dtype=torch.float64)) @ V(dy), BF16, 1.0, "dbias")
+
+
+@pytest.mark.parametrize("shape", [(2000, 264, 520, 136), (4100, 520, 264, 136), (900, 512, 2048, 512)], ids=str)
+def test_gated_ffn_backward_every_kernel(shape):
+    t, k, f, o = shape
+    d = Draw(t, F16)
+    x, wg, wu, wd = d(t, k), d(k, f, scale=k ** -0.5), d(k, f, scale=k ** -0.5), d(f, o, scale=f ** -0.5)
+    dy, g, u, h = d(t, o, scale=0.1), d(t, f, scale=1.5), d(t, f), d(t, f)
+    dx, dwg, dwu, dwd = tc.gated_ffn_backward(dy, x, wg, wu, wd, g, u, h)
+    dh = V(dy) @ V(wd).T
+    dg = (dh * V(u) * V(g).slope("silu")).round(F16)
+    du = (dh * V(g).act("silu")).round(F16)
+    check(dx, dg @ V(wg).T + du @ V(wu).T, F16, 1.2, "dx")
+    check(dwg, V(x).T @ dg, F16, 1.2, "dw_gate")
+    check(dwu, V(x).T @ du, F16, 1.2, "dw_up")
+    check(dwd, V(h).T @ V(dy), F16, 1.0, "dw_down")
+
+
+def test_more_than_2_31_entries():
+    """Outputs past 4 GiB, forward and as a weight gradient: rows at the start, either side of
+    entry 2^31 and at the end."""
+    d = Draw(31, BF16)
+    x, w = d(66000, 64), d(64, 33000, scale=0.125)
+    y = tc.linear(x, w, act="relu")
+    rows = [0, 1, 2**31 // 33000 - 1, 2**31 // 33000, 2**31 // 33000 + 1, 65535, 65999]
+    _, want = linear_want(x[rows], w, None, "relu", None)
+    check(y[rows], want, BF16, 1.0, "y")
+    del y
+    x, dy = d(72, 50000), d(72, 45000)
+    w = torch.empty(50000, 45000, device="cuda", dtype=BF16)  # not read: its gradient's shape
+    w.zero_()
+    _, dw, _ = tc.linear_backward(dy, x, w)
+    rows = [0, 2**31 // 45000 - 1, 2**31 // 45000, 2**31 // 45000 + 1, 49999]
+    check(dw[rows], V(x[:, rows]).T @ V(dy), BF16, 1.0, "dw")
+
+
+@pytest.mark.parametrize("call", ["few", "many", "split", "gated", "backward"])
+def test_wait_that_runs_out_is_reported(call):
     """With no loads issued the MMA warp's bounded wait runs out; the context stays usable."""
     d = Draw(2, F16)
-    x, w = d(300, 256), d(256, 512)
+    w, wd = d(256, 512), d(512, 256)
+    x = {"few": d(3, 256), "many": d(2000, 256), "split": d(512, 256), "gated": d(20, 256), "backward": d(700, 256)}[call]
+    if call == "split":
+        w = d(4096, 4096)
+        x = d(512, 4096)
     try:
         tc.gemm_f16_set_config(inject_stall=1, wait_limit=2_000_000)
-        tc.linear(x, w)
+        if call == "gated":
+            tc.gated_ffn(x, w, w, wd)
+        elif call == "backward":
+            tc.linear_backward(d(700, 512), x, w)
+        else:
+            tc.linear(x, w)
         torch.cuda.synchronize()
         rc, site = tc.gemm_f16_device_status(reset=True)
         assert rc == -11 and site == 2
@@ -250,6 +332,37 @@ def test_wait_that_runs_out_is_reported():
         tc.gemm_f16_set_config()
     _, want = linear_want(x, w, None, None, None)
     check(tc.linear(x, w), want, F16, 1.0, "after")
+
+
+def test_first_calls_from_several_threads():
+    """Six host threads, each on a stream of its own, call into different kernels at once."""
+    import threading
+
+    d = Draw(77, BF16)
+    jobs = []
+    for t, k, n in [(1, 512, 1024), (64, 256, 520), (300, 1024, 264), (512, 4096, 4096), (2000, 264, 776), (150, 136, 2048)]:
+        x, w = d(t, k), d(k, n, scale=k ** -0.5)
+        jobs.append((x, w, V(x) @ V(w)))
+    torch.cuda.synchronize()
+    got, errors = [None] * len(jobs), []
+
+    def work(i):
+        try:
+            side = torch.cuda.Stream()
+            for _ in range(5):
+                got[i] = tc.linear(jobs[i][0], jobs[i][1], stream=side)
+            side.synchronize()
+        except Exception as e:  # noqa: BLE001  (reported below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for y, (_, _, want) in zip(got, jobs):
+        check(y, want, BF16, 1.0, "thread")
 
 
 def test_refusals():
@@ -282,3 +395,6 @@ def test_refusals():
         tc.gated_ffn(x, w, d(64, 136), d(128, 64))
     with pytest.raises(ValueError):
         tc.gated_ffn(x, w, w, d(120, 64))
+    with pytest.raises(tc.GemmError) as e:
+        tc.linear(x[:1].expand(8, 64), w)  # a broadcast row: stride 0
+    assert e.value.code == -2
