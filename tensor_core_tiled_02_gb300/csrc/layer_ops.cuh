@@ -364,7 +364,12 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.act = q.p.act;
     p.bias = q.p.bias;
     p.alpha = q.p.alpha;
-    if (q.ins > 0) {
+    if (EPI == kEpiGateGrad) {
+        p.gate = q.in[0].p;
+        p.ld_gate = q.in[0].ld;
+        p.up = q.in[1].p;
+        p.ld_up = q.in[1].ld;
+    } else if (q.ins > 0) {
         p.addend = q.in[0].p;
         p.ld_addend = q.in[0].ld;
         p.addend_f32 = q.in[0].bytes == 4;
@@ -374,8 +379,9 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.out_f32 = q.out[0].bytes == 4;
     p.keep0 = const_cast<void*>(q.out[1].p);
     p.ld_keep0 = q.out[1].ld;
-    p.keep1 = const_cast<void*>(q.out[2].p);
-    p.ld_keep1 = q.out[2].ld;
+    const Mat& second = q.out[EPI == kEpiGateGrad ? 1 : 2];
+    p.keep1 = const_cast<void*>(second.p);
+    p.ld_keep1 = second.ld;
     p.stats = q.p.stats;
     p.target_logit = q.p.target_logit;
     p.target = q.p.target;
@@ -398,7 +404,7 @@ constexpr long long kFewTokens = 1024;
 template <int LAY, int EPI, int DT>
 int run_product_as(const Product& q, const Ctx& c) {
     const PairPlan g = pair_plan(q, EPI, c);
-    if constexpr (LAY != kTN && EPI != kEpiGateGrad) {
+    if constexpr (LAY != kTN) {
         constexpr int epi = EPI == kEpiStoreF32 ? kEpiStore : EPI;  // the output's type is a parameter there
         if (q.M <= kFewTokens) {
             const SkinnyPlan f = skinny_plan(q, EPI == kEpiGate, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c));

@@ -45,8 +45,10 @@ struct SkinnyParams {
     int addend_f32, out_f32;
     void* out;
     long long ld_out;
-    void *keep0, *keep1;     // x w + bias; kGate: g and u
+    void *keep0, *keep1;     // x w + bias; kEpiGate: g and u; kEpiGateGrad: du in keep1
     long long ld_keep0, ld_keep1;
+    const void *gate, *up;   // kEpiGateGrad: [T, N]
+    long long ld_gate, ld_up;
     float2* stats;           // kEpiLossStats: [ceil(N / 128)][T]
     float* target_logit;
     const long long* target; // kEpiLoss*
@@ -347,6 +349,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                     o[e] = scale == 0.0f ? 0.0f : q * scale;
                 }
                 store4<DT>(p.out, t * p.ld_out + n, left, o);
+            } else if constexpr (EPI == kEpiGateGrad) {
+                float g[4], u[4], du[4];
+                load4<DT>(p.gate, t * p.ld_gate + n, left, g);
+                load4<DT>(p.up, t * p.ld_up + n, left, u);
+                with_act(p.act, [&](auto tag) {
+                    constexpr int ACT = decltype(tag)::value;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[e] = f[0][e] * u[e] * act_slope<ACT>(g[e]);
+                        du[e] = f[0][e] * act_value<ACT>(g[e]);
+                    }
+                });
+                store4<DT>(p.out, t * p.ld_out + n, left, o);
+                store4<DT>(p.keep1, t * p.ld_keep1 + n, left, du);
             } else if constexpr (GATE) {
                 if (p.keep0 != nullptr) {
                     store4<DT>(p.keep0, t * p.ld_keep0 + n, left, f[0]);
