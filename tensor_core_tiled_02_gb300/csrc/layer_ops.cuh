@@ -481,53 +481,49 @@ int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
     return launch_pdl(kern, dim3(2 * pairs), kThreads, L::kSmem, 2, c.stream, tm, p);
 }
 
-// Products with the plain store epilogue, of which list[0] has its own K and the
-// others share theirs: together where that is expected to take less than one after
-// the other.
-int run_grads(GradProduct* list, int n, int dtype, const Ctx& c) {
-    auto alone = [&](const GradProduct& g) {
-        switch (g.layout) {
-            case kNN: return run_product<kNN, kEpiStore>(g.q, dtype, c);
-            case kNT: return run_product<kNT, kEpiStore>(g.q, dtype, c);
-            default: return run_product<kTN, kEpiStore>(g.q, dtype, c);
-        }
-    };
-    bool together = n > 1;
-    if (together) {
-        // The same estimates as above, with at least 6,000 cycles a tile for writing it: a
-        // weight gradient over few tokens is all writing.  (Over 54 backward passes of 8 to
-        // 4096 tokens, widths 512 to 14336, the choice cost 0.4 % on average.)
-        const int pairs = max_pairs_of(*c.dev);
-        long long apart = 0, cycles = 0, longest = 0, tiles = 0;
-        for (int i = 0; i < n; ++i) {
-            const Product& q = list[i].q;
-            const PairPlan g = pair_plan(q, kEpiStore, c);
-            const long long share = ceil_div(g.k_steps, g.split) * 545ll, whole = g.k_steps * 545ll;
-            long long cost = 8500 + (g.split > 1 ? 8500 : 0) +
-                             (g.split > 1 ? 1 : ceil_div(g.tiles, g.pairs)) * (share > 6000 ? share : 6000);
-            const long long bytes = 9500 + product_bytes(q, 1) / 3300;
-            if (cost < bytes) cost = bytes;
-            if (list[i].layout != kTN && q.M <= kFewTokens) {
-                const SkinnyPlan f = skinny_plan(q, false, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c));
-                const long long few = skinny_cycles(f, q, 1);
-                if (few < cost) cost = few;
-            }
-            apart += cost;
-            tiles += g.tiles;
-            const long long tile = whole > 6000 ? whole : 6000;
-            cycles += (long long)g.tiles * tile;
-            if (longest < tile) longest = tile;
-        }
-        const long long spread = (cycles + pairs - 1) / pairs;
-        together = tiles < INT_MAX / 2 && 8500 + (spread > longest ? spread : longest) < apart;
+// Cycles of one product by itself, and of a tile of it among others; the estimates
+// above, with at least 6,000 cycles a tile for writing it: a weight gradient over few
+// tokens is all writing.
+long long alone_cycles(const GradProduct& p, const Ctx& c) {
+    const Product& q = p.q;
+    const PairPlan g = pair_plan(q, kEpiStore, c);
+    const long long tile = ceil_div(g.k_steps, g.split) * 545ll;
+    long long cost = 8500 + (g.split > 1 ? 8500 : 0) + (g.split > 1 ? 1 : ceil_div(g.tiles, g.pairs)) * (tile > 6000 ? tile : 6000);
+    const long long bytes = 9500 + product_bytes(q, 1) / 3300;
+    if (cost < bytes) cost = bytes;
+    if (p.layout != kTN && q.M <= kFewTokens) {
+        const long long few = skinny_cycles(skinny_plan(q, false, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c)), q, 1);
+        if (few < cost) cost = few;
     }
-    if (!together) {
-        for (int i = 0; i < n; ++i) {
-            const int rc = alone(list[i]);
-            if (rc != GEMM_OK) return rc;
-        }
-        return GEMM_OK;
+    return cost;
+}
+
+long long together_cycles(const GradProduct* list, int n, const Ctx& c) {
+    long long cycles = 0, longest = 0, tiles = 0;
+    for (int i = 0; i < n; ++i) {
+        const Product& q = list[i].q;
+        const long long here = (long long)ceil_div(q.M, 256) * ceil_div(q.N, 256);
+        const long long steps = ceil_div(q.K, 64) * (q.a2.p ? 2ll : 1ll) * 545, tile = steps > 6000 ? steps : 6000;
+        tiles += here;
+        cycles += here * tile;
+        if (longest < tile) longest = tile;
     }
+    if (tiles > INT_MAX / 2) return LLONG_MAX / 2;
+    const int pairs = max_pairs_of(*c.dev);
+    const long long spread = (cycles + pairs - 1) / pairs;
+    return 8500 + (spread > longest ? spread : longest);
+}
+
+int run_alone(const GradProduct& g, int dtype, const Ctx& c) {
+    switch (g.layout) {
+        case kNN: return run_product<kNN, kEpiStore>(g.q, dtype, c);
+        case kNT: return run_product<kNT, kEpiStore>(g.q, dtype, c);
+        default: return run_product<kTN, kEpiStore>(g.q, dtype, c);
+    }
+}
+
+int run_together(GradProduct* list, int n, int dtype, const Ctx& c) {
+    if (n == 1) return run_alone(list[0], dtype, c);
     // the group of the larger K goes first
     int longs = 1;
     if (list[0].q.K * (list[0].q.a2.p ? 2 : 1) < list[1].q.K) {
@@ -535,6 +531,24 @@ int run_grads(GradProduct* list, int n, int dtype, const Ctx& c) {
         longs = n - 1;
     }
     return dtype == LAYER_BF16 ? run_grads_as<kBF16>(list, n, longs, c) : run_grads_as<kF16>(list, n, longs, c);
+}
+
+// Products with the plain store epilogue, of which list[0] has its own K and the
+// others share theirs: one after the other, all together, or list[0] alone and the
+// others together, whichever is expected to take least.  (Over 54 backward passes of 8
+// to 4096 tokens, widths 512 to 14336, the choice between the first two cost 0.4 % on
+// average; the third: gated block of 8 tokens, 512 x 2048, 25.6 -> 18.3 us.)
+int run_grads(GradProduct* list, int n, int dtype, const Ctx& c) {
+    if (n <= 1) return n == 1 ? run_alone(list[0], dtype, c) : GEMM_OK;
+    long long apart = 0;
+    for (int i = 0; i < n; ++i) apart += alone_cycles(list[i], c);
+    const long long together = together_cycles(list, n, c);
+    const long long rest = n > 2 ? alone_cycles(list[0], c) + together_cycles(list + 1, n - 1, c) : LLONG_MAX;
+    if (together <= apart && together <= rest) return run_together(list, n, dtype, c);
+    int rc = run_alone(list[0], dtype, c);
+    if (rc == GEMM_OK && rest <= apart) return run_together(list + 1, n - 1, dtype, c);
+    for (int i = 1; i < n && rc == GEMM_OK; ++i) rc = run_alone(list[i], dtype, c);
+    return rc;
 }
 
 // A weight gradient over no tokens is zero.
