@@ -250,6 +250,7 @@ constexpr int kSkinnyTwoSmem = 115712;  // two such CTAs fill an SM's 228 KiB
 // shared memory.
 struct SkinnyPlan {
     int nt, t_tiles, tiles, split, slots, stage_bytes, smem, tmem_cols, waves, k_steps;
+    int push, recv_bytes;
 };
 
 // As pair_cycles.  An SM takes in about 58 bytes a cycle of operands that hit L2; 8,000
@@ -279,7 +280,7 @@ SkinnyPlan skinny_plan(const Product& q, bool gate, int sms, const int* held) {
     // K = N = 4096: 1, 2, 4, 6 and 8 CTAs a tile 19.8, 12.1, 8.6, 8.8 and 9.0 us; 8 tokens,
     // K = 32768, N = 1024: 8, 12 and 16 CTAs a tile 21.2, 17.4 and 15.8 us; the gated product
     // of 4096 x 14336: 2, 3 and 4 CTAs a tile 36.5, 44 and 40.5 us, the last two in two waves).
-    const int fixed = 1024 + 8 * (2 * kSkinnySlots + 1) + 16;
+    const int fixed = 1024 + 8 * (2 * kSkinnySlots + 2) + 16;
     const int in_flight = (kSkinnyTwoSmem - fixed) / g.stage_bytes * weights * kSkinnyTileBytes;
     const bool two = cols <= 128 && in_flight >= (gate ? 65536 : 81920);
     // (After this call's own kernel the weights' first loads run under that kernel's
@@ -292,9 +293,18 @@ SkinnyPlan skinny_plan(const Product& q, bool gate, int sms, const int* held) {
     for (int s = 2; s <= kSkinnySplit && s * 2 <= k_steps && g.tiles * split < want; ++s)
         if (g.tiles <= held[s] * (two ? 2 : 1)) split = s;
     g.split = split;
-    g.slots = ((two ? kSkinnyTwoSmem : kSmemLimit) - fixed) / g.stage_bytes;
+    // Partials are pushed where the buffer they arrive in costs the ring no slot, or the
+    // steps are few (16 tokens: K = 14336, N = 4096 pulled 20.9 us, pushed with five
+    // slots instead of six 21.4; gated block of 512 x 2048 10.3 and 9.9).
+    const int budget = (two ? kSkinnyTwoSmem : kSmemLimit) - fixed;
+    g.recv_bytes = ceil_div(q.M < kPushTokens ? q.M : kPushTokens, split) * split * weights * 512;
+    const int pushed_slots = (budget - g.recv_bytes) / g.stage_bytes;
+    g.push = split > 1 && q.M * weights <= kPushTokens &&
+             (pushed_slots == budget / g.stage_bytes || ceil_div(k_steps, split) <= 16);
+    if (!g.push) g.recv_bytes = 0;
+    g.slots = (budget - g.recv_bytes) / g.stage_bytes;
     if (g.slots > kSkinnySlots) g.slots = kSkinnySlots;
-    g.smem = g.slots * g.stage_bytes + fixed;
+    g.smem = g.slots * g.stage_bytes + g.recv_bytes + fixed;
     const int floor_smem = two ? 78848 : 118784;  // never three CTAs an SM, or two
     if (g.smem < floor_smem) g.smem = floor_smem;
     g.waves = ceil_div((long long)g.tiles * g.split, sms);
@@ -359,6 +369,8 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.weights_early = q.after_own;
     p.slots = g.slots;
     p.stage_bytes = g.stage_bytes;
+    p.push = g.push;
+    p.recv_bytes = g.recv_bytes;
     p.tmem_cols = g.tmem_cols;
     if ((long long)g.tiles * g.split > INT_MAX) return GEMM_ERR_DIM;
     p.act = q.p.act;

@@ -9,11 +9,15 @@
 //
 // Memory-bound: what counts is enough bytes in flight on every SM.  N / 128
 // column tiles alone rarely fill 152 SMs, so a thread-block cluster of up to 16
-// CTAs shares each tile along K.  Each CTA leaves its fp32 partial tile in
-// shared memory; then the CTAs of the cluster each sum a share of the tile's
-// tokens over distributed shared memory, in rank order (the same bits every
-// time), a warp at a time on the 128 columns of one token, and apply the
-// epilogue (layer_pair_kernel.cuh names them).
+// CTAs shares each tile along K.  The fp32 partials then meet over distributed
+// shared memory: each CTA of the cluster sums a share of the tile's tokens, in
+// rank order (the same bits every time), a warp at a time on the 128 columns of
+// one token, and applies the epilogue (layer_pair_kernel.cuh names them).
+//   push  (up to 16 tokens) every thread sends its column's values straight from
+//         Tensor Memory to the CTA that sums the token, which waits for the bytes
+//         on an mbarrier: the way from the last product to the sums takes 0.5 us
+//   pull  each CTA leaves its partial in its idle ring, the cluster meets at a
+//         barrier, then reads: 1.1 us, but no room taken from the ring
 //
 // Roles: warp 0 lane 0 loads, warp 1 lane 0 issues MMAs, warps 2-5 read the
 // accumulator; all six reduce and store.  Every wait is bounded.
@@ -25,6 +29,7 @@ namespace tcgemm {
 
 constexpr int kSkinnySlots = 12;     // most ring slots
 constexpr int kSkinnySplit = 16;     // most CTAs sharing a tile (above 8 a non-portable cluster)
+constexpr int kPushTokens = 16;      // most tokens whose partials are pushed
 constexpr int kSkinnyTileBytes = 128 * 64 * 2;  // one weight tile of one K step
 
 struct SkinnyMaps {
@@ -36,6 +41,7 @@ struct SkinnyParams {
     int t_tiles;             // ceil(T / nt)
     int k_steps, k_switch;   // 64-deep; steps >= k_switch read w[1], x[1] from their start (not kGate)
     int split, slots, stage_bytes, tmem_cols;
+    int push, recv_bytes;    // partials pushed: the buffer they arrive in
     int weights_early;       // the previous kernel is this call's own and does not write the weights
     int act;
     const void* bias;
@@ -68,6 +74,15 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 
+// Four bytes into another CTA's shared memory, counted on an mbarrier there.
+__device__ __forceinline__ void st_async_b32(uint32_t cluster_addr, uint32_t v, uint32_t bar_cluster) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(cluster_addr), "r"(v),
+                 "r"(bar_cluster)
+                 : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // Four neighbouring values of a row, those from `left` on absent (0, not stored).
 template <int DT>
 __device__ __forceinline__ void load4(const void* p, long long at, int left, float (&f)[4]) {
@@ -93,6 +108,49 @@ __device__ __forceinline__ void store4(void* p, long long at, int left, const fl
     }
 }
 
+// Tokens tb, tb + 6, ... below tt_end of this warp: sums the cluster's partials of
+// columns c .. c + 3 into this CTA's own, RANKS x BATCH reads under way at a time.
+template <int RANKS, int BATCH, int TILES>
+__device__ __forceinline__ void pull_sums(uint32_t ring, int nt, int ranks, int tb, int tt_end, int c) {
+    constexpr int kWarps = kThreads / 32;
+#pragma unroll 1
+    for (; tb < tt_end; tb += kWarps * BATCH) {
+#pragma unroll 1
+        for (int i = 0; i < TILES; ++i) {
+            float f[BATCH][4];
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) f[u][0] = f[u][1] = f[u][2] = f[u][3] = 0.0f;
+#pragma unroll 1
+            for (int r0 = 0; r0 < ranks; r0 += RANKS) {
+                uint32_t w[RANKS][BATCH][4];
+#pragma unroll
+                for (int r = 0; r < RANKS; ++r)
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u) {
+                        const int tt = tb + u * kWarps;
+                        w[r][u][0] = w[r][u][1] = w[r][u][2] = w[r][u][3] = 0u;
+                        if (r0 + r < ranks && tt < tt_end)
+                            ptx::ld_cluster_v4(ptx::mapa(ring, r0 + r) + (uint32_t)((i * nt + tt) * 512 + c * 4), w[r][u][0],
+                                               w[r][u][1], w[r][u][2], w[r][u][3]);
+                    }
+#pragma unroll
+                for (int r = 0; r < RANKS; ++r)
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[u][e] += __uint_as_float(w[r][u][e]);
+            }
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int tt = tb + u * kWarps;
+                if (tt < tt_end)
+                    ptx::st_shared_v4(ring + (uint32_t)((i * nt + tt) * 512 + c * 4), __float_as_uint(f[u][0]),
+                                      __float_as_uint(f[u][1]), __float_as_uint(f[u][2]), __float_as_uint(f[u][3]));
+            }
+        }
+    }
+}
+
 template <bool WMN, int EPI, int DT>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
@@ -102,25 +160,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t ring = (raw + 1023u) & ~1023u;
     const int S = p.slots;
-    const uint32_t bar0 = ring + (uint32_t)(S * p.stage_bytes);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bar0 - raw) + 8 * (2 * kSkinnySlots + 1));
+    const uint32_t recv = ring + (uint32_t)(S * p.stage_bytes);
+    const uint32_t bar0 = recv + (uint32_t)p.recv_bytes;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bar0 - raw) + 8 * (2 * kSkinnySlots + 2));
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 #ifdef TCGEMM_CHECK
-    if (bar0 + 8u * (2 * kSkinnySlots + 1) + 8u > raw + ptx::dynamic_smem_size() ||
-        kTiles * p.nt * 512 > S * p.stage_bytes) {
+    if (bar0 + 8u * (2 * kSkinnySlots + 2) + 8u > raw + ptx::dynamic_smem_size() ||
+        (p.push ? p.split * ((p.T + p.split - 1) / p.split) * kTiles * 512 > p.recv_bytes
+                : kTiles * p.nt * 512 > S * p.stage_bytes)) {
         if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
         return;  // every CTA decides alike
     }
 #endif
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kSkinnySlots + s); };
-    const uint32_t done_bar = bar0 + 8u * (2 * kSkinnySlots);
+    const uint32_t done_bar = bar0 + 8u * (2 * kSkinnySlots), recv_bar = done_bar + 8u;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int CS = p.split;
     const int rank = (int)blockIdx.x % CS;
     const int tile = (int)blockIdx.x / CS;
     const int n0 = (tile / p.t_tiles) * 128, t0 = (tile % p.t_tiles) * p.nt;
+    // this CTA's tokens of the tile; pushed partials lie [rank][own token][weight][128 columns]
+    const int tokens = min(p.nt, p.T - t0);
+    const int own0 = tokens * rank / CS, own1 = tokens * (rank + 1) / CS;
+    const int most = (tokens + CS - 1) / CS;
     const int k0 = (int)((long long)p.k_steps * rank / CS), k1 = (int)((long long)p.k_steps * (rank + 1) / CS);
 
     if (threadIdx.x == 0) {
@@ -129,8 +193,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             ptx::mbar_init(empty_bar(s), 1);
         }
         ptx::mbar_init(done_bar, 1);
+        ptx::mbar_init(recv_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
+        if (p.push && own1 > own0) ptx::mbar_arrive_expect_tx(recv_bar, (uint32_t)((own1 - own0) * CS * kTiles * 512));
         ptx::prefetch_tmap(&tm.w[0]);
         ptx::prefetch_tmap(&tm.x[0]);
     }
@@ -140,6 +206,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     ptx::tc_fence_before();
     __syncthreads();
+    if (p.push) {  // every CTA's mbarrier is ready before anyone sends to it
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
     ptx::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -231,23 +301,68 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait_drain(done_bar, 0, p.wait_limit);
         }
     } else {
-        // ---------------- this CTA's partial: TMEM -> shared memory ----------------
-        // (the ring is idle: every load was consumed by an MMA, and every MMA is complete)
+        // ---------------- this CTA's partial out of TMEM ----------------
         const int q = warp & 3;
+        // what the epilogue will read, towards this SM while the weights stream
+        ptx::grid_dependency_wait();
+        if constexpr (EPI == kEpiGateGrad) {
+            const int n = n0 + q * 32;
+            if (n < p.N)
+                for (int t = own0 + lane; t < own1; t += 32) {
+                    prefetch_l1(static_cast<const char*>(p.gate) + ((t0 + t) * p.ld_gate + n) * 2);
+                    prefetch_l1(static_cast<const char*>(p.up) + ((t0 + t) * p.ld_up + n) * 2);
+                }
+            __syncwarp();
+        }
+        if constexpr (EPI == kEpiStore) {
+            const int n = n0 + q * 32;  // 64 bytes of 16-bit values a warp
+            if (lane == 0 && n < p.N) {
+                if (p.bias != nullptr) prefetch_l1(static_cast<const char*>(p.bias) + (long long)n * 2);
+                if (p.addend != nullptr)
+                    for (int t = own0; t < own1; ++t)
+                        prefetch_l1(static_cast<const char*>(p.addend) +
+                                    ((long long)(t0 + t) * p.ld_addend + n) * (p.addend_f32 ? 4 : 2));
+            }
+            __syncwarp();
+        }
         if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0 &&
             TC_CHECK(kTiles * p.nt <= p.tmem_cols, kSiteTmemBounds)) {
             ptx::tc_fence_after();
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
-            const uint32_t col = ring + (uint32_t)((q * 32 + lane) * 4);
+            const uint32_t col = (uint32_t)((q * 32 + lane) * 4);
+            if (p.push) {
 #pragma unroll 1
-            for (int c = 0; c < kTiles * p.nt; c += 16) {
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(trow + c, v);
-                ptx::tmem_ld_wait();
-                // [token][128 columns] fp32
+                for (int i = 0; i < kTiles; ++i) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(trow + i * p.nt, v);
+                    ptx::tmem_ld_wait();
+                    // token t goes to the CTA whose share holds it
+                    int to = 0, first = 0, next = tokens / CS;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(col + (uint32_t)((c + i) * 512)), "r"(v[i]) : "memory");
+                    for (int t = 0; t < kPushTokens; ++t) {
+                        if (t < tokens) {
+                            while (t >= next) {
+                                ++to;
+                                first = next;
+                                next = tokens * (to + 1) / CS;
+                            }
+                            const uint32_t at = recv + (uint32_t)(((rank * most + t - first) * kTiles + i) * 512) + col;
+                            st_async_b32(ptx::mapa(at, to), v[t], ptx::mapa(recv_bar, to));
+                        }
+                    }
+                }
+            } else {
+                // the ring is idle: every load was consumed by an MMA, and every MMA is complete
+#pragma unroll 1
+                for (int c = 0; c < kTiles * p.nt; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(trow + c, v);
+                    ptx::tmem_ld_wait();
+                    // [token][128 columns] fp32
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + col + (uint32_t)((c + i) * 512)), "r"(v[i]) : "memory");
+                }
             }
         }
         ptx::tc_fence_before();
@@ -258,64 +373,50 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, p.tmem_cols);
     }
-    if (CS > 1) {
+    bool here = true;  // the partials of this CTA's tokens are within reach
+    if (p.push) {
+        here = own1 == own0 || warp_wait<true>(recv_bar, 0, abort_flag, p.wait_limit, kSiteReduceData, lane);
+    } else if (CS > 1) {
         __syncwarp();
         ptx::cluster_arrive();
         ptx::cluster_wait();
     }
-    if (*abort_flag == 0) {
+    if (here && *abort_flag == 0) {
         // the previous kernel's reads and writes of what is read and written below are done
         ptx::grid_dependency_wait();
         const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
-        // This CTA's tokens of the tile, a warp on each, a lane four columns.  First the
-        // sums over the cluster, kept in this CTA's own partial (nobody else reads these
-        // tokens of it): several tokens at a time, so that the reads of other CTAs' shared
-        // memory overlap (one at a time, 256 tokens at K = 2048, N = 8192 took 20.8 us, not
-        // 17.9), and apart from the epilogue, whose code four times over costs one token
-        // 0.4 us of instruction fetches.
-        const int tokens = min(p.nt, p.T - t0);
+        // A warp on each of this CTA's tokens, a lane four columns.  Where partials are
+        // pulled, first the sums over the cluster, kept in this CTA's own partial (nobody
+        // else reads these tokens of it): all ranks' values of a batch of tokens at once,
+        // so that the reads of other CTAs' shared memory overlap, and apart from the
+        // epilogue, whose code in every batch would cost instruction fetches.
         const int c = lane * 4, n = n0 + c, left = p.N - n;
-        const int tt_begin = tokens * rank / CS + warp, tt_end = tokens * (rank + 1) / CS;
-        constexpr int kWarps = kThreads / 32, kBatch = 4;
-        if (CS > 1) {
-#pragma unroll 1
-            for (int tb = tt_begin; tb < tt_end; tb += kWarps * kBatch) {
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    float f[kBatch][4];
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) f[u][0] = f[u][1] = f[u][2] = f[u][3] = 0.0f;
-#pragma unroll 2
-                    for (int r = 0; r < CS; ++r) {
-                        const uint32_t from = ptx::mapa(ring, r);
-#pragma unroll
-                        for (int u = 0; u < kBatch; ++u) {
-                            const int tt = tb + u * kWarps;
-                            if (tt < tt_end) {
-                                uint32_t w[4];
-                                ptx::ld_cluster_v4(from + (uint32_t)((i * p.nt + tt) * 512 + c * 4), w[0], w[1], w[2], w[3]);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) f[u][e] += __uint_as_float(w[e]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < kBatch; ++u) {
-                        const int tt = tb + u * kWarps;
-                        if (tt < tt_end)
-                            ptx::st_shared_v4(ring + (uint32_t)((i * p.nt + tt) * 512 + c * 4), __float_as_uint(f[u][0]),
-                                              __float_as_uint(f[u][1]), __float_as_uint(f[u][2]), __float_as_uint(f[u][3]));
-                    }
-                }
-            }
+        const int tt_begin = own0 + warp, tt_end = own1;
+        constexpr int kWarps = kThreads / 32;
+        if (CS > 1 && !p.push) {
+            if (CS <= 4)
+                pull_sums<4, 4, kTiles>(ring, p.nt, CS, tt_begin, tt_end, c);
+            else
+                pull_sums<8, 2, kTiles>(ring, p.nt, CS, tt_begin, tt_end, c);
         }
 #pragma unroll 1
         for (int tt = tt_begin; tt < tt_end; tt += kWarps) {
             const int t = t0 + tt;
             float f[kTiles][4];
 #pragma unroll
-            for (int i = 0; i < kTiles; ++i)
-                ld_shared_f4(ring + (uint32_t)((i * p.nt + tt) * 512 + c * 4), f[i][0], f[i][1], f[i][2], f[i][3]);
+            for (int i = 0; i < kTiles; ++i) {
+                if (p.push) {
+                    f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0.0f;
+#pragma unroll 4
+                    for (int r = 0; r < CS; ++r) {
+                        float a, b, d, e;
+                        ld_shared_f4(recv + (uint32_t)(((r * most + tt - own0) * kTiles + i) * 512 + c * 4), a, b, d, e);
+                        f[i][0] += a, f[i][1] += b, f[i][2] += d, f[i][3] += e;
+                    }
+                } else {
+                    ld_shared_f4(ring + (uint32_t)((i * p.nt + tt) * 512 + c * 4), f[i][0], f[i][1], f[i][2], f[i][3]);
+                }
+            }
             float o[4];
             if constexpr (EPI == kEpiLossStats) {
                 float m = -INFINITY;
@@ -410,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     }
     if (CS > 1) {
-        // no CTA leaves while another still reads its partial
+        // no CTA leaves while another still reads its partial or sends to it
         __syncwarp();
         ptx::cluster_arrive_relaxed();
         ptx::cluster_wait();
