@@ -47,6 +47,18 @@ __device__ __forceinline__ unsigned short pack1(float v) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Approximations to about 1e-7 of the value; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // 1 / (1 + exp(-y)).  exp(-y) overflows to inf for y below -88, where the
 // quotient is 0; __fdividef gives 0 already for a denominator above 2^126.
 __device__ __forceinline__ float sigmoid(float y) { return __fdividef(1.0f, 1.0f + __expf(-y)); }

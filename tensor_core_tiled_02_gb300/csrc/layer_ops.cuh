@@ -219,7 +219,7 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
         rc = encode_mat(&tm.a[i], as[i], dtype, 64, kAMN ? 64 : 128);
         if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], bs[i], dtype, 64, kBMN ? 64 : PN / 2);
     }
-    for (int i = 0; i < q.outs && rc == GEMM_OK && EPI != kEpiLossStats; ++i)
+    for (int i = 0; i < q.outs && rc == GEMM_OK && EPI != kEpiLossStats && EPI != kEpiLossStatsLong; ++i)
         rc = encode_mat(&tm.out[i], q.out[i], dtype, 128 / q.out[i].bytes, 32);
     for (int i = 0; i < q.ins && rc == GEMM_OK; ++i) rc = encode_mat(&tm.in[i], q.in[i], dtype, 128 / q.in[i].bytes, 32);
     if (rc != GEMM_OK) return rc;
@@ -250,7 +250,7 @@ constexpr int kSkinnyTwoSmem = 115712;  // two such CTAs fill an SM's 228 KiB
 // shared memory.
 struct SkinnyPlan {
     int nt, t_tiles, tiles, split, slots, stage_bytes, smem, tmem_cols, waves, k_steps;
-    int push, recv_bytes;
+    int push, recv_bytes, accs;
 };
 
 // As pair_cycles.  An SM takes in about 58 bytes a cycle of operands that hit L2; 8,000
@@ -262,7 +262,8 @@ long long skinny_cycles(const SkinnyPlan& g, const Product& q, int weights) {
     return steps > bytes ? steps : bytes;
 }
 
-SkinnyPlan skinny_plan(const Product& q, bool gate, int sms, const int* held) {
+SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
+    const bool gate = epi == kEpiGate;
     SkinnyPlan g{};
     const int most = gate ? 128 : 256;  // the fp32 partials of a tile have to fit the ring
     g.t_tiles = ceil_div(q.M, most);
@@ -293,6 +294,14 @@ SkinnyPlan skinny_plan(const Product& q, bool gate, int sms, const int* held) {
     for (int s = 2; s <= kSkinnySplit && s * 2 <= k_steps && g.tiles * split < want; ++s)
         if (g.tiles <= held[s] * (two ? 2 : 1)) split = s;
     g.split = split;
+    // the loss's logits in up to eight accumulators, kPromote steps each where there is room
+    g.accs = 1;
+    if (epi == kEpiLossStats) {
+        const int room = (two ? 256 : 512) / g.nt, steps = ceil_div(k_steps, split);
+        g.accs = room < 8 ? room : 8;
+        if (g.accs > ceil_div(steps, kPromote)) g.accs = ceil_div(steps, kPromote);
+        while (g.tmem_cols < g.accs * g.nt) g.tmem_cols *= 2;
+    }
     // Partials are pushed where the buffer they arrive in costs the ring no slot, or the
     // steps are few (16 tokens: K = 14336, N = 4096 pulled 20.9 us, pushed with five
     // slots instead of six 21.4; gated block of 512 x 2048 10.3 and 9.9).
@@ -323,11 +332,13 @@ const int* skinny_clusters(const Ctx& c) {
     if (known[c.ordinal].load(std::memory_order_acquire)) return held[c.ordinal];
     std::lock_guard<std::mutex> lk(g_dev_mu);
     if (known[c.ordinal].load(std::memory_order_relaxed)) return held[c.ordinal];
-    auto kern = layer_skinny_kernel<WMN, EPI, DT>;
+    auto kern = layer_skinny_kernel<WMN, EPI, DT, false>;
     bool can = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
     for (int s = 1; s <= kSkinnySplit; ++s) {
         if (s == kMaxSplit + 1)
-            can = can && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            can = can && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                  cudaFuncSetAttribute(layer_skinny_kernel<WMN, EPI, DT, true>,
+                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         cudaLaunchConfig_t lc = {};
         lc.gridDim = dim3(s * 64, 1, 1);
         lc.blockDim = dim3(kThreads, 1, 1);
@@ -369,7 +380,7 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.weights_early = q.after_own;
     p.slots = g.slots;
     p.stage_bytes = g.stage_bytes;
-    p.push = g.push;
+    p.accs = g.accs;
     p.recv_bytes = g.recv_bytes;
     p.tmem_cols = g.tmem_cols;
     if ((long long)g.tiles * g.split > INT_MAX) return GEMM_ERR_DIM;
@@ -403,11 +414,13 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
     const int smem = g.smem, split = g.split, tiles = g.tiles;
-    auto kern = layer_skinny_kernel<WMN, EPI, DT>;
-    static std::atomic<bool> ready[kMaxDevices];
-    rc = ensure_smem_limit(kern, kSmemLimit, ready[c.ordinal]);
-    if (rc != GEMM_OK) return rc;
-    return launch_pdl(kern, dim3(tiles * split), kThreads, smem, split, c.stream, tm, p);
+    auto start = [&](auto kern, std::atomic<bool>& ready) {
+        const int r = ensure_smem_limit(kern, kSmemLimit, ready);
+        return r != GEMM_OK ? r : launch_pdl(kern, dim3(tiles * split), kThreads, smem, split, c.stream, tm, p);
+    };
+    static std::atomic<bool> ready[2][kMaxDevices];
+    return g.push ? start(layer_skinny_kernel<WMN, EPI, DT, true>, ready[1][c.ordinal])
+                  : start(layer_skinny_kernel<WMN, EPI, DT, false>, ready[0][c.ordinal]);
 }
 
 // The kernel whose expected time is less; beyond kFewTokens always the pairs'.
@@ -419,11 +432,13 @@ int run_product_as(const Product& q, const Ctx& c) {
     if constexpr (LAY != kTN) {
         constexpr int epi = EPI == kEpiStoreF32 ? kEpiStore : EPI;  // the output's type is a parameter there
         if (q.M <= kFewTokens) {
-            const SkinnyPlan f = skinny_plan(q, EPI == kEpiGate, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c));
+            const SkinnyPlan f = skinny_plan(q, EPI, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c));
             constexpr int weights = EPI == kEpiGate ? 2 : 1;
             if (skinny_cycles(f, q, weights) <= pair_cycles(g, q, weights)) return run_product_skinny<LAY == kNN, epi, DT>(q, f, c);
         }
     }
+    if constexpr (EPI == kEpiLossStats)
+        if (g.k_steps > kPromote) return run_product_pair<LAY, kEpiLossStatsLong, DT, false>(q, g, c);
     if constexpr (EPI == kEpiStore)
         if (g.split > 1) return run_product_pair<LAY, EPI, DT, true>(q, g, c);
     return run_product_pair<LAY, EPI, DT, false>(q, g, c);
@@ -504,7 +519,7 @@ long long alone_cycles(const GradProduct& p, const Ctx& c) {
     const long long bytes = 9500 + product_bytes(q, 1) / 3300;
     if (cost < bytes) cost = bytes;
     if (p.layout != kTN && q.M <= kFewTokens) {
-        const long long few = skinny_cycles(skinny_plan(q, false, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c)), q, 1);
+        const long long few = skinny_cycles(skinny_plan(q, kEpiStore, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c)), q, 1);
         if (few < cost) cost = few;
     }
     return cost;

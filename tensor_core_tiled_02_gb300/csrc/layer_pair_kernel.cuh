@@ -17,6 +17,8 @@
 //   kEpiGateGrad    v = dh: dg = dh u act'(g), du = dh act(g), with g and u loaded
 //   kEpiLossStats   v = logits: per row and tile the maximum and the sum of
 //                   exp(v - maximum), and the target's logit; no logit is stored
+//   kEpiLossStatsLong  the same for K above 2048: the tensor core's sums are added up
+//                   in fp32 every 2048 of K
 //   kEpiLossGrad    v = logits again: (exp(v - lse) - [column = target]) times the row's
 //                   weight, in 16 bits, operand of the two products that follow
 //
@@ -55,9 +57,11 @@ enum LayerEpilogue {
     kEpiGateGrad = 3,
     kEpiLossStats = 4,
     kEpiLossGrad = 5,
+    kEpiLossStatsLong = 6,
 };
 
 constexpr int kLayerMaxSplit = 4;
+constexpr int kPromote = 32;           // kEpiLossStatsLong: K steps (of 64) summed on the tensor core at a time
 
 struct LayerMaps {
     CUtensorMap a[2], b[2];
@@ -92,9 +96,9 @@ struct LayerPairLayout {
     static constexpr int kABytes = 128 * 64 * 2;         // this CTA's 128 rows of one K step
     static constexpr int kBBytes = (PN / 2) * 64 * 2;    // this CTA's PN/2 columns
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kWarps = SPLIT ? 8 : 4;         // epilogue warps
+    static constexpr int kWarps = SPLIT || EPI == kEpiLossStatsLong ? 8 : 4;  // epilogue warps
     static constexpr int kThreads = 64 + 32 * kWarps;
-    static constexpr int kWarpStaging = EPI == kEpiLossStats ? 0 : 65536 / kWarps;  // staging per epilogue warp
+    static constexpr int kWarpStaging = EPI == kEpiLossStats || EPI == kEpiLossStatsLong ? 0 : 65536 / kWarps;  // staging per epilogue warp
     // full[8], empty[8], tmem_full[2], tmem_empty[2], drain, aux[warps][2]
     static constexpr int kNumBars = 2 * kMaxStages + 5 + 2 * kWarps;
     static constexpr int kBiasBytes = kWarps * 64 * 2;   // 64 values per epilogue warp
@@ -282,46 +286,126 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
             int tl = 0;
             bool ok = true;
             for (int t = cluster; ok && t < tiles; t += clusters) {
-                const int acc = tl & 1;
-                const uint32_t aph = (tl >> 1) & 1;
-                ++tl;
-                if (!wait_bounded<true>(tempty_bar(acc), aph ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
-                    ok = false;
-                    break;
-                }
-                ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
-                if (!TC_CHECK(acc * PN + PN <= L::kTmemCols, kSiteTmemBounds)) {
-                    ok = false;
-                    break;
-                }
-                for (int kb = kb0; kb < kb1; ++kb) {
-                    if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
-                        ok = false;
-                        break;
-                    }
-                    if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
+                // one accumulator a tile, or (kEpiLossStatsLong) one every kPromote steps
+                for (int ks = kb0, ke; ok && ks < kb1; ks = ke) {
+                    ke = EPI == kEpiLossStatsLong ? min(kb1, ks + kPromote) : kb1;
+                    const int acc = tl & 1;
+                    const uint32_t aph = (tl >> 1) & 1;
+                    ++tl;
+                    if (!wait_bounded<true>(tempty_bar(acc), aph ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint64_t ad0 = operand_desc<kAMN>(sA + stage * L::kABytes);
-                    const uint64_t bd0 = operand_desc<kBMN>(sB + stage * L::kBBytes);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        ptx::mma_f16_ss_pair(d_tmem, ad0 + k * kSliceStep<kAMN>, bd0 + k * kSliceStep<kBMN>, idesc,
-                                             (kb - kb0) | k);
-                    ptx::mma_commit_pair_multicast(empty_bar(stage), both);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1u;
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
+                    if (!TC_CHECK(acc * PN + PN <= L::kTmemCols, kSiteTmemBounds)) {
+                        ok = false;
+                        break;
                     }
+                    for (int kb = ks; kb < ke; ++kb) {
+                        if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
+                            ok = false;
+                            break;
+                        }
+                        if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint64_t ad0 = operand_desc<kAMN>(sA + stage * L::kABytes);
+                        const uint64_t bd0 = operand_desc<kBMN>(sB + stage * L::kBBytes);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_f16_ss_pair(d_tmem, ad0 + k * kSliceStep<kAMN>, bd0 + k * kSliceStep<kBMN>, idesc,
+                                                 (kb - ks) | k);
+                        ptx::mma_commit_pair_multicast(empty_bar(stage), both);
+                        if (++stage == S) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    ptx::mma_commit_pair_multicast(tfull_bar(acc), both);
                 }
-                if (!ok) break;
-                ptx::mma_commit_pair_multicast(tfull_bar(acc), both);
             }
             ptx::mma_commit_pair(drain_bar);
             wait_drain(drain_bar, 0, p.wait_limit);
+        }
+    } else if constexpr (EPI == kEpiLossStatsLong) {
+        // ---------------- statistics (both CTAs): 32 rows x 128 columns a warp ----------------
+        // The running sums of kPromote steps each are added up here in fp32, rounded to
+        // nearest, 128 columns a thread: the tensor core's own accumulation truncates, and its
+        // bias, below 1e-6 of the loss up to K = 2048, reached 8e-6 at K = 8192.  (For K up to
+        // 2048 the other form's four warps cost less: 4096 tokens, K = 1024, 32768 words 160 us
+        // against 172.)
+        const int q = warp & 3, half = (warp - 2) >> 2;
+        const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+        ptx::grid_dependency_wait();
+        ptx::grid_launch_dependents();
+        int tl = 0;
+        bool ok = true;
+        for (int t = cluster; ok && t < tiles; t += clusters) {
+            int mb, nb;
+            layer_tile_coords(t, p, mb, nb);
+            const int row0 = mb * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
+            const int x = nb * PN + half * 128;
+            const bool mine = row0 < p.M && x < p.N;
+            float v[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) v[i] = 0.0f;
+            for (int ks = 0; ks < kb1; ks += kPromote, ++tl) {
+                const int acc = tl & 1;
+                ok = warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (mine) {
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        uint32_t w[32];
+                        ptx::tmem_ld_32x32b_x32(lane_base + (uint32_t)(acc * PN + g * 32), w);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[g * 32 + i] += __uint_as_float(w[i]);
+                    }
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && (t + clusters < tiles || ks + kPromote < kb1))
+                    ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), leader));
+            }
+            if (!ok || !mine) continue;
+            int tcol = -1;  // the target's column, relative to this warp's
+            if (row < p.M) {
+                const long long tg = p.target[row] - x;
+                if (tg >= 0 && tg < 128 && tg < p.N - x) tcol = (int)tg;
+            }
+            if (tcol >= 0) {
+                float picked = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i == tcol) picked = v[i];
+                p.target_logit[row] = picked;
+            }
+            __syncwarp();
+            if (p.N - x < 128) {  // columns from N on are no words
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i >= p.N - x) v[i] = -INFINITY;
+            }
+            float m0 = v[0], m1 = v[1];
+#pragma unroll
+            for (int i = 2; i < 128; i += 2) {
+                m0 = fmaxf(m0, v[i]);
+                m1 = fmaxf(m1, v[i + 1]);
+            }
+            const float m = fmaxf(m0, m1);
+            // the difference before the factor: a maximum near the type's lowest times log2(e)
+            // would overflow.  (While all is -inf the terms are exp(-inf - 0) = 0.)
+            const float mf = m == -INFINITY ? 0.0f : m;
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < 128; ++i) s[i & 3] += ex2_approx((v[i] - mf) * 1.4426950408889634f);
+            if (row < p.M) p.stats[(size_t)(x >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
         }
     } else {
         // ---------------- epilogue (both CTAs): 32 rows a warp, all columns or (SPLIT) half ----------------
@@ -466,15 +550,15 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                     float m = best;
 #pragma unroll
                     for (int i = 0; i < 32; ++i) m = fmaxf(m, __uint_as_float(v[i]));
-                    sum *= best == m ? 1.0f : exp2f((best - m) * 1.4426950408889634f);
+                    sum *= best == m ? 1.0f : ex2_approx((best - m) * 1.4426950408889634f);
                     // the difference before the factor: a maximum near the type's lowest times log2(e)
                     // would overflow.  (While all is -inf the terms are exp(-inf - 0) = 0.)
                     const float mf = m == -INFINITY ? 0.0f : m;
                     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        s0 += exp2f((__uint_as_float(v[i]) - mf) * 1.4426950408889634f);
-                        s1 += exp2f((__uint_as_float(v[i + 1]) - mf) * 1.4426950408889634f);
+                        s0 += ex2_approx((__uint_as_float(v[i]) - mf) * 1.4426950408889634f);
+                        s1 += ex2_approx((__uint_as_float(v[i + 1]) - mf) * 1.4426950408889634f);
                     }
                     sum += s0 + s1;
                     best = m;
@@ -701,7 +785,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                             // a row of weight 0 is 0 whatever its logits hold
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                float e = exp2f((__uint_as_float(v[i]) - lse) * 1.4426950408889634f);
+                                float e = ex2_approx((__uint_as_float(v[i]) - lse) * 1.4426950408889634f);
                                 if (i == rel) e -= 1.0f;
                                 f[i] = scale == 0.0f ? 0.0f : e * scale;
                             }

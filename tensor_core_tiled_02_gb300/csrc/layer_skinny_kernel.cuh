@@ -41,7 +41,8 @@ struct SkinnyParams {
     int t_tiles;             // ceil(T / nt)
     int k_steps, k_switch;   // 64-deep; steps >= k_switch read w[1], x[1] from their start (not kGate)
     int split, slots, stage_bytes, tmem_cols;
-    int push, recv_bytes;    // partials pushed: the buffer they arrive in
+    int accs;                // kEpiLossStats: accumulators the K steps are dealt out to, summed in fp32
+    int recv_bytes;          // PUSH: the buffer partials arrive in
     int weights_early;       // the previous kernel is this call's own and does not write the weights
     int act;
     const void* bias;
@@ -151,7 +152,7 @@ __device__ __forceinline__ void pull_sums(uint32_t ring, int nt, int ranks, int 
     }
 }
 
-template <bool WMN, int EPI, int DT>
+template <bool WMN, int EPI, int DT, bool PUSH>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
     constexpr bool GATE = EPI == kEpiGate;
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 #ifdef TCGEMM_CHECK
     if (bar0 + 8u * (2 * kSkinnySlots + 2) + 8u > raw + ptx::dynamic_smem_size() ||
-        (p.push ? p.split * ((p.T + p.split - 1) / p.split) * kTiles * 512 > p.recv_bytes
+        (PUSH ? p.split * ((p.T + p.split - 1) / p.split) * kTiles * 512 > p.recv_bytes
                 : kTiles * p.nt * 512 > S * p.stage_bytes)) {
         if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
         return;  // every CTA decides alike
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::mbar_init(recv_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
-        if (p.push && own1 > own0) ptx::mbar_arrive_expect_tx(recv_bar, (uint32_t)((own1 - own0) * CS * kTiles * 512));
+        if (PUSH && own1 > own0) ptx::mbar_arrive_expect_tx(recv_bar, (uint32_t)((own1 - own0) * CS * kTiles * 512));
         ptx::prefetch_tmap(&tm.w[0]);
         ptx::prefetch_tmap(&tm.x[0]);
     }
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     ptx::tc_fence_before();
     __syncthreads();
-    if (p.push) {  // every CTA's mbarrier is ready before anyone sends to it
+    if (PUSH) {  // every CTA's mbarrier is ready before anyone sends to it
         ptx::cluster_arrive_relaxed();
         ptx::cluster_wait();
     }
@@ -278,7 +279,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t idesc = layer_idesc(DT, WMN, false, 128, p.nt);
             int stage = 0;
             uint32_t phase = 0;
-            for (int kb = k0; kb < k1; ++kb) {
+            // the loss's logits: consecutive runs of steps into accumulators of their own, as the
+            // tensor core's accumulation truncates (layer_pair_kernel.cuh)
+            const int run = EPI == kEpiLossStats ? (k1 - k0 + p.accs - 1) / p.accs : k1 - k0;
+            uint32_t acc_tmem = tmem;
+            int in_run = 0;
+            for (int kb = k0; kb < k1; ++kb, ++in_run) {
+                if (EPI == kEpiLossStats && in_run == run) {
+                    in_run = 0;
+                    acc_tmem += (uint32_t)p.nt;
+                }
                 if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) break;
                 ptx::tc_fence_after();
                 const uint32_t src = ring + (uint32_t)(stage * p.stage_bytes);
@@ -288,8 +298,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const uint64_t wd = operand_desc<WMN>(src + i * kSkinnyTileBytes);
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        ptx::mma_f16_ss(tmem + (uint32_t)(i * p.nt), wd + k * kSliceStep<WMN>, xd + k * kSliceStep<false>,
-                                        idesc, ((kb - k0) | k) != 0);
+                        ptx::mma_f16_ss(acc_tmem + (uint32_t)(i * p.nt), wd + k * kSliceStep<WMN>,
+                                        xd + k * kSliceStep<false>, idesc, (in_run | k) != 0);
                 }
                 ptx::mma_commit(empty_bar(stage));
                 if (++stage == S) {
@@ -326,16 +336,34 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
         }
         if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0 &&
-            TC_CHECK(kTiles * p.nt <= p.tmem_cols, kSiteTmemBounds)) {
+            TC_CHECK(kTiles * p.nt * (EPI == kEpiLossStats ? p.accs : 1) <= p.tmem_cols, kSiteTmemBounds)) {
             ptx::tc_fence_after();
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
             const uint32_t col = (uint32_t)((q * 32 + lane) * 4);
-            if (p.push) {
+            // accumulators that hold anything (a short K range may leave the last ones empty)
+            const int run = EPI == kEpiLossStats ? (k1 - k0 + p.accs - 1) / p.accs : 1;
+            const int accs = EPI == kEpiLossStats ? (k1 - k0 + run - 1) / run : 1;
+            auto load16 = [&](int c, uint32_t(&v)[16]) {
+                tmem_ld_32x32b_x16(trow + c, v);
+                if constexpr (EPI == kEpiLossStats) {
+#pragma unroll 1
+                    for (int a = 1; a < accs; ++a) {
+                        uint32_t w[16];
+                        tmem_ld_32x32b_x16(trow + a * p.nt + c, w);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) fadd_bits(v[i], w[i]);
+                    }
+                    if (accs > 1) return;
+                }
+                ptx::tmem_ld_wait();
+            };
+            (void)accs;
+            if (PUSH) {
 #pragma unroll 1
                 for (int i = 0; i < kTiles; ++i) {
                     uint32_t v[16];
-                    tmem_ld_32x32b_x16(trow + i * p.nt, v);
-                    ptx::tmem_ld_wait();
+                    load16(i * p.nt, v);
                     // token t goes to the CTA whose share holds it
                     int to = 0, first = 0, next = tokens / CS;
 #pragma unroll
@@ -356,8 +384,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 1
                 for (int c = 0; c < kTiles * p.nt; c += 16) {
                     uint32_t v[16];
-                    tmem_ld_32x32b_x16(trow + c, v);
-                    ptx::tmem_ld_wait();
+                    load16(c, v);
                     // [token][128 columns] fp32
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -374,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::tmem_dealloc(tmem, p.tmem_cols);
     }
     bool here = true;  // the partials of this CTA's tokens are within reach
-    if (p.push) {
+    if (PUSH) {
         here = own1 == own0 || warp_wait<true>(recv_bar, 0, abort_flag, p.wait_limit, kSiteReduceData, lane);
     } else if (CS > 1) {
         __syncwarp();
@@ -393,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int c = lane * 4, n = n0 + c, left = p.N - n;
         const int tt_begin = own0 + warp, tt_end = own1;
         constexpr int kWarps = kThreads / 32;
-        if (CS > 1 && !p.push) {
+        if (CS > 1 && !PUSH) {
             if (CS <= 4)
                 pull_sums<4, 4, kTiles>(ring, p.nt, CS, tt_begin, tt_end, c);
             else
@@ -405,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             float f[kTiles][4];
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
-                if (p.push) {
+                if (PUSH) {
                     f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0.0f;
 #pragma unroll 4
                     for (int r = 0; r < CS; ++r) {
@@ -430,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const float mf = m == -INFINITY ? 0.0f : m;
                 float sum = 0.0f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum += exp2f((f[0][e] - mf) * 1.4426950408889634f);
+                for (int e = 0; e < 4; ++e) sum += ex2_approx((f[0][e] - mf) * 1.4426950408889634f);
 #pragma unroll
                 for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
                 if (lane == 0) p.stats[(size_t)(n0 >> 7) * p.T + t] = make_float2(m, sum);
@@ -446,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const long long rel = p.target[t] - p.col0 - n;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float q = exp2f((f[0][e] - lse) * 1.4426950408889634f) - (rel == e ? 1.0f : 0.0f);
+                    const float q = ex2_approx((f[0][e] - lse) * 1.4426950408889634f) - (rel == e ? 1.0f : 0.0f);
                     o[e] = scale == 0.0f ? 0.0f : q * scale;
                 }
                 store4<DT>(p.out, t * p.ld_out + n, left, o);

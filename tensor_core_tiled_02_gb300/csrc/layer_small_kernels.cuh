@@ -41,18 +41,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
     return r;
 }
 __device__ __forceinline__ F2 both(float c) { return f2(c, c); }
-// Approximations to about 1e-7 of the value; results below 2^-126 are 0.
-__device__ __forceinline__ float ex2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float rcp_approx(float x) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // act_slope of two values; GELU's by the formula of normal_cdf, its coefficients halved.
 template <int ACT>
 __device__ __forceinline__ F2 act_slope2(F2 x) {
