@@ -10,7 +10,10 @@
 //                many as one long tile lasts), then in rounds over all, these pairs first
 //
 // 2001 tokens, 2048 x 8192: dx 64 tiles of 128 steps and dw 256 tiles of 32 on 76
-// pairs take 94 us one after the other, 66 together.
+// pairs take 91 us one after the other, 75 together (1790 TFLOP/s; 73 at the measured
+// peak); dx and the three weight gradients of the gated block, 4096 tokens, 4096 x 14336,
+// 1255 us (1916 TFLOP/s, one launch).  Bound by the tensor pipe, 88 and 96 % of the
+// cycles busy.
 //
 // Tiles, ring, roles and waits are layer_pair_kernel.cuh's, with the operands'
 // major order a property of the problem; the epilogue is y = alpha v.
@@ -36,7 +39,7 @@ struct GradsProblem {
 
 struct GradsParams {
     GradsProblem q[kGradsProblems];
-    int problems, longs;    // problems [0, longs) form the long group
+    int longs;              // problems [0, longs) form the long group
     int tiles[2];           // of the long and the short group
     int rounds, rem, d;     // the long group's full rounds, the tiles of its last, and see above
     int raster_group;
@@ -76,8 +79,8 @@ __device__ __forceinline__ bool grads_tile(const GradsParams& p, int c, int P, i
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     layer_grads_kernel(const __grid_constant__ GradsMaps tm, const __grid_constant__ GradsParams p) {
-    constexpr int PN = 256, kHalf = 128;
-    using L = LayerPairLayout<kEpiStore, PN, false>;
+    constexpr int kHalf = kTileN / 2;
+    using L = LayerPairLayout<kEpiStore, false>;
     constexpr int S = L::kSlots;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int prob, mb, nb;
             for (int i = 0; ok && grads_tile(p, pair, P, i, prob, mb, nb); ++i) {
                 const GradsProblem& q = p.q[prob];
-                const int m0 = mb * 256 + (int)rank * 128, n0 = nb * PN + (int)rank * kHalf;
+                const int m0 = mb * 256 + (int)rank * 128, n0 = nb * kTileN + (int)rank * kHalf;
                 const int KB = q.k_steps, k_switch = q.k_switch, a_mn = q.a_mn, b_mn = q.b_mn;
                 for (int kb = 0; kb < KB; ++kb) {
                     if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
@@ -207,8 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
-                const uint32_t idesc = layer_idesc(DT, q.a_mn != 0, q.b_mn != 0, 256, PN);
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTileN);
+                const uint32_t idesc = layer_idesc(DT, q.a_mn != 0, q.b_mn != 0, 256, kTileN);
                 const uint64_t a_base = q.a_mn ? operand_desc<true>(0) : operand_desc<false>(0);
                 const uint64_t b_base = q.b_mn ? operand_desc<true>(0) : operand_desc<false>(0);
                 const uint32_t a_step = q.a_mn ? kSliceStep<true> : kSliceStep<false>;
@@ -255,11 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; grads_tile(p, pair, P, i, prob, mb, nb); ++i) {
             const GradsProblem& q = p.q[prob];
             const int acc = i & 1;
-            const int row0 = mb * 256 + (int)rank * 128 + q4 * 32, n0 = nb * PN;
-            const int chunks = row0 < q.M ? min(PN / 64, (q.N - n0 + 63) / 64) : 0;
+            const int row0 = mb * 256 + (int)rank * 128 + q4 * 32, n0 = nb * kTileN;
+            const int chunks = row0 < q.M ? min(kTileN / 64, (q.N - n0 + 63) / 64) : 0;
             if (!warp_wait(tfull_bar(acc), (i >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
-            const uint32_t trow = lane_base + (uint32_t)(acc * PN);
+            const uint32_t trow = lane_base + (uint32_t)(acc * kTileN);
             int p2, m2, n2;
             const bool last = !grads_tile(p, pair, P, i + 1, p2, m2, n2);  // no MMA waits for its accumulator
             auto hand_back = [&]() {
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 0; c < chunks; ++c) {
                 const uint32_t buf = stg + (n_chunk & 3) * 4096u;
-                if (!TC_CHECK(holds(sC, (uint32_t)(L::kWarps * L::kWarpStaging), buf, 4096u) && acc * PN + PN <= L::kTmemCols,
+                if (!TC_CHECK(holds(sC, (uint32_t)(L::kWarps * L::kWarpStaging), buf, 4096u) && acc * kTileN + kTileN <= L::kTmemCols,
                               kSiteSmemBounds))
                     break;
                 if (lane == 0) ptx::bulk_wait_group_read<3>();

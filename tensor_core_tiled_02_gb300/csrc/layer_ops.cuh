@@ -202,8 +202,7 @@ PairPlan pair_plan(const Product& q, int epi, const Ctx& c) {
 
 template <int LAY, int EPI, int DT, bool SPLIT>
 int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
-    constexpr int PN = 256;
-    using L = LayerPairLayout<EPI, PN, SPLIT>;
+    using L = LayerPairLayout<EPI, SPLIT>;
     constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
     constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
     LayerMaps tm;
@@ -217,7 +216,7 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
             break;
         }
         rc = encode_mat(&tm.a[i], as[i], dtype, 64, kAMN ? 64 : 128);
-        if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], bs[i], dtype, 64, kBMN ? 64 : PN / 2);
+        if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], bs[i], dtype, 64, kBMN ? 64 : kTileN / 2);
     }
     for (int i = 0; i < q.outs && rc == GEMM_OK && EPI != kEpiLossStats && EPI != kEpiLossStatsLong; ++i)
         rc = encode_mat(&tm.out[i], q.out[i], dtype, 128 / q.out[i].bytes, 32);
@@ -236,7 +235,7 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
     p.split = g.split;
-    auto kern = layer_pair_kernel<LAY, EPI, DT, PN, SPLIT>;
+    auto kern = layer_pair_kernel<LAY, EPI, DT, SPLIT>;
     static std::atomic<bool> ready[kMaxDevices];
     rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
     if (rc != GEMM_OK) return rc;
@@ -278,15 +277,16 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
     // missing L2, so HBM's rate needs four SMs in five busy: one CTA on each, or two of a
     // gated tile's shallow rings.  The split is the least that gives so many CTAs, among
     // those whose clusters all fit at once, at two K steps each at least (one token,
-    // K = N = 4096: 1, 2, 4, 6 and 8 CTAs a tile 19.8, 12.1, 8.6, 8.8 and 9.0 us; 8 tokens,
-    // K = 32768, N = 1024: 8, 12 and 16 CTAs a tile 21.2, 17.4 and 15.8 us; the gated product
-    // of 4096 x 14336: 2, 3 and 4 CTAs a tile 36.5, 44 and 40.5 us, the last two in two waves).
+    // K = N = 4096: 1, 2, 4, 6 and 8 CTAs a tile 20.4, 11.9, 8.5, 8.9 and 8.9 us; 8 tokens,
+    // K = 32768, N = 1024: 8, 12 and 16 CTAs a tile 20.8, 15.9 and 14.9 us; the gated
+    // block of 4096 x 14336: 2, 3 and 4 CTAs a gate and up tile 57, 65 and 61 us in all, the
+    // last two in two waves).
     const int fixed = 1024 + 8 * (2 * kSkinnySlots + 2) + 16;
     const int in_flight = (kSkinnyTwoSmem - fixed) / g.stage_bytes * weights * kSkinnyTileBytes;
     const bool two = cols <= 128 && in_flight >= (gate ? 65536 : 81920);
     // (After this call's own kernel the weights' first loads run under that kernel's
     // end, and twice the CTAs start more of them: worth it where 16 steps each remain.
-    // Gated block for one token, 4096 x 14336: 62.7 -> 58.3 us.)
+    // Gated block for one token, 4096 x 14336: 61.7 -> 57.0 us.)
     const int each = sms * 4 / 5;
     const bool twice = two && (gate || (q.after_own && (long long)k_steps * g.tiles >= 32ll * each));
     const int want = twice ? 2 * each : each;
@@ -302,15 +302,15 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
         if (g.accs > ceil_div(steps, kPromote)) g.accs = ceil_div(steps, kPromote);
         while (g.tmem_cols < g.accs * g.nt) g.tmem_cols *= 2;
     }
-    // Partials are pushed where the buffer they arrive in costs the ring no slot, or the
-    // steps are few (16 tokens: K = 14336, N = 4096 pulled 20.9 us, pushed with five
-    // slots instead of six 21.4; gated block of 512 x 2048 10.3 and 9.9).
+    // Partials of few tokens are pushed within small clusters (pulled and pushed, medians
+    // of seven: one token, K = N = 4096 8.71 and 8.47 us, K = 2048, N = 8192 8.72 and 8.46;
+    // four tokens 8.74 and 8.66, 8.74 and 8.49).  In larger clusters, for more tokens and
+    // for two weights pulling is faster (one token, K = N = 1024, eight CTAs 3.71 and
+    // 3.77; 16 tokens, K = N = 4096 8.88 and 9.04; gated block of 512 x 2048, 8 tokens, 8.51
+    // and 9.30).
     const int budget = (two ? kSkinnyTwoSmem : kSmemLimit) - fixed;
-    g.recv_bytes = ceil_div(q.M < kPushTokens ? q.M : kPushTokens, split) * split * weights * 512;
-    const int pushed_slots = (budget - g.recv_bytes) / g.stage_bytes;
-    g.push = split > 1 && q.M * weights <= kPushTokens &&
-             (pushed_slots == budget / g.stage_bytes || ceil_div(k_steps, split) <= 16);
-    if (!g.push) g.recv_bytes = 0;
+    g.push = epi == kEpiStore && q.M <= kPushTokens && split > 1 && split <= kPushSplit;
+    g.recv_bytes = g.push ? ceil_div(q.M, split) * split * 512 : 0;
     g.slots = (budget - g.recv_bytes) / g.stage_bytes;
     if (g.slots > kSkinnySlots) g.slots = kSkinnySlots;
     g.smem = g.slots * g.stage_bytes + g.recv_bytes + fixed;
@@ -336,9 +336,7 @@ const int* skinny_clusters(const Ctx& c) {
     bool can = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit) == cudaSuccess;
     for (int s = 1; s <= kSkinnySplit; ++s) {
         if (s == kMaxSplit + 1)
-            can = can && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
-                  cudaFuncSetAttribute(layer_skinny_kernel<WMN, EPI, DT, true>,
-                                       cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            can = can && cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
         cudaLaunchConfig_t lc = {};
         lc.gridDim = dim3(s * 64, 1, 1);
         lc.blockDim = dim3(kThreads, 1, 1);
@@ -419,8 +417,9 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
         return r != GEMM_OK ? r : launch_pdl(kern, dim3(tiles * split), kThreads, smem, split, c.stream, tm, p);
     };
     static std::atomic<bool> ready[2][kMaxDevices];
-    return g.push ? start(layer_skinny_kernel<WMN, EPI, DT, true>, ready[1][c.ordinal])
-                  : start(layer_skinny_kernel<WMN, EPI, DT, false>, ready[0][c.ordinal]);
+    if constexpr (EPI == kEpiStore)
+        if (g.push) return start(layer_skinny_kernel<WMN, EPI, DT, true>, ready[1][c.ordinal]);
+    return start(layer_skinny_kernel<WMN, EPI, DT, false>, ready[0][c.ordinal]);
 }
 
 // The kernel whose expected time is less; beyond kFewTokens always the pairs'.
@@ -459,7 +458,7 @@ struct GradProduct {
 template <int DT>
 int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
     constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
-    using L = LayerPairLayout<kEpiStore, 256, false>;
+    using L = LayerPairLayout<kEpiStore, false>;
     GradsMaps tm;
     std::memset(&tm, 0, sizeof(tm));
     GradsParams p;
@@ -485,7 +484,6 @@ int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
         if (rc == GEMM_OK) rc = encode_mat(&tm.out[i], q.out[0], dtype, 64, 32);
     }
     if (rc != GEMM_OK) return rc;
-    p.problems = n;
     p.longs = longs;
     for (int i = 0; i < n; ++i) p.tiles[i < p.longs ? 0 : 1] += p.q[i].tiles_m * p.q[i].tiles_n;
     const int pairs = max_pairs_of(*c.dev);
@@ -564,7 +562,7 @@ int run_together(GradProduct* list, int n, int dtype, const Ctx& c) {
 // others share theirs: one after the other, all together, or list[0] alone and the
 // others together, whichever is expected to take least.  (Over 54 backward passes of 8
 // to 4096 tokens, widths 512 to 14336, the choice between the first two cost 0.4 % on
-// average; the third: gated block of 8 tokens, 512 x 2048, 25.6 -> 18.3 us.)
+// average; the third: gated block of 8 tokens, 512 x 2048, 25.5 together, 15.3 so.)
 int run_grads(GradProduct* list, int n, int dtype, const Ctx& c) {
     if (n <= 1) return n == 1 ? run_alone(list[0], dtype, c) : GEMM_OK;
     long long apart = 0;

@@ -1,4 +1,4 @@
-// The layer operators' matrix product on CTA pairs: D = A B on 256 x PN tiles
+// The layer operators' matrix product on CTA pairs: D = A B on 256 x 256 tiles
 // (tcgen05.mma.cta_group::2, M = 256), fp16 or bf16 operands, each in either
 // major order, fp32 accumulation in Tensor Memory, and the operator's own
 // elementwise work in the epilogue, on the fp32 accumulator.
@@ -11,7 +11,7 @@
 //   epilogue        what it computes of the tile's values v
 //   kEpiStore       y = act(alpha v + bias) + addend; keeps alpha v + bias on request.
 //                   The addend is the residual, or the fp32 sum so far
-//   kEpiGate        the tile's first PN/2 columns come from w_gate, the others
+//   kEpiGate        the tile's first 128 columns come from w_gate, the others
 //                   from w_up (each CTA of the pair loads one of them), so a
 //                   thread holds both g and u of an element: h = act(g) u
 //   kEpiGateGrad    v = dh: dg = dh u act'(g), du = dh act(g), with g and u loaded
@@ -90,11 +90,12 @@ struct LayerParams {
     int inject;
 };
 
-template <int EPI, int PN, bool SPLIT>
+constexpr int kTileN = 256;  // a pair tile's columns
+
+template <int EPI, bool SPLIT>
 struct LayerPairLayout {
-    static_assert(PN == 256 || PN == 128, "tile columns");
     static constexpr int kABytes = 128 * 64 * 2;         // this CTA's 128 rows of one K step
-    static constexpr int kBBytes = (PN / 2) * 64 * 2;    // this CTA's PN/2 columns
+    static constexpr int kBBytes = (kTileN / 2) * 64 * 2;    // this CTA's half of the columns
     static constexpr int kStageBytes = kABytes + kBBytes;
     static constexpr int kWarps = SPLIT || EPI == kEpiLossStatsLong ? 8 : 4;  // epilogue warps
     static constexpr int kThreads = 64 + 32 * kWarps;
@@ -108,8 +109,8 @@ struct LayerPairLayout {
     static constexpr int kSlots = kFit < kMaxStages ? kFit : kMaxStages;
     static_assert(kSlots >= 5, "ring depth");
     static constexpr int kSmem = 1024 + kSlots * kStageBytes + kFixedBytes;
-    static constexpr int kTmemCols = 2 * PN;             // two accumulators
-    static constexpr int kOutN = EPI == kEpiGate ? PN / 2 : PN;      // output columns of a tile
+    static constexpr int kTmemCols = 2 * kTileN;             // two accumulators
+    static constexpr int kOutN = EPI == kEpiGate ? kTileN / 2 : kTileN;      // output columns of a tile
     static constexpr int kChunk = EPI == kEpiStoreF32 || EPI == kEpiLossStats ? 32 : 64;  // columns drained at a time
 };
 
@@ -130,14 +131,14 @@ __device__ __forceinline__ uint32_t swz(uint32_t buf, int lane, int piece) {
     return buf + (uint32_t)(lane * 128) + ((uint32_t)(piece ^ (lane & 7)) << 4);
 }
 
-template <int LAY, int EPI, int DT, int PN, bool SPLIT>
-__global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
+template <int LAY, int EPI, int DT, bool SPLIT>
+__global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
     layer_pair_kernel(const __grid_constant__ LayerMaps tm, const LayerParams p) {
-    using L = LayerPairLayout<EPI, PN, SPLIT>;
+    using L = LayerPairLayout<EPI, SPLIT>;
     constexpr bool kAMN = LAY == kTN, kBMN = LAY != kNT;
     constexpr int S = L::kSlots;
-    constexpr int kHalf = PN / 2;
-    static_assert(!SPLIT || (EPI == kEpiStore && S * L::kStageBytes >= 128 * PN * 4), "partials fit the ring");
+    constexpr int kHalf = kTileN / 2;
+    static_assert(!SPLIT || (EPI == kEpiStore && S * L::kStageBytes >= 128 * kTileN * 4), "partials fit the ring");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t base = (raw + 1023u) & ~1023u;
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                 int mb, nb;
                 layer_tile_coords(t, p, mb, nb);
                 const int m0 = mb * 256 + (int)rank * 128;
-                // kEpiGate: this CTA's columns are the tile's PN/2 of one weight
-                const int n0 = EPI == kEpiGate ? nb * kHalf : nb * PN + (int)rank * kHalf;
+                // kEpiGate: this CTA's columns are the tile's half of one weight
+                const int n0 = EPI == kEpiGate ? nb * kHalf : nb * kTileN + (int)rank * kHalf;
                 for (int kb = kb0; kb < kb1; ++kb) {
                     if (!TC_CHECK(stage_ok(stage), kSiteSmemBounds)) {
                         ok = false;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader only) ----------------
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = layer_idesc(DT, kAMN, kBMN, 256, PN);
+            constexpr uint32_t idesc = layer_idesc(DT, kAMN, kBMN, 256, kTileN);
             int stage = 0;
             uint32_t phase = 0;
             int tl = 0;
@@ -297,8 +298,8 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
                         break;
                     }
                     ptx::tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * PN);
-                    if (!TC_CHECK(acc * PN + PN <= L::kTmemCols, kSiteTmemBounds)) {
+                    const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kTileN);
+                    if (!TC_CHECK(acc * kTileN + kTileN <= L::kTmemCols, kSiteTmemBounds)) {
                         ok = false;
                         break;
                     }
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
             int mb, nb;
             layer_tile_coords(t, p, mb, nb);
             const int row0 = mb * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
-            const int x = nb * PN + half * 128;
+            const int x = nb * kTileN + half * 128;
             const bool mine = row0 < p.M && x < p.N;
             float v[128];
 #pragma unroll
@@ -362,7 +363,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         uint32_t w[32];
-                        ptx::tmem_ld_32x32b_x32(lane_base + (uint32_t)(acc * PN + g * 32), w);
+                        ptx::tmem_ld_32x32b_x32(lane_base + (uint32_t)(acc * kTileN + g * 32), w);
                         ptx::tmem_ld_wait();
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[g * 32 + i] += __uint_as_float(w[i]);
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
             }
             if (!warp_wait(tfull_bar(acc), aph, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
-            const uint32_t trow = lane_base + (uint32_t)(acc * PN);
+            const uint32_t trow = lane_base + (uint32_t)(acc * kTileN);
             auto hand_back = [&]() {
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, PN, SPLIT>::kThreads, 1)
             if constexpr (SPLIT) {
                 // this CTA's partial into its ring (idle: every load was consumed by an MMA, every
                 // MMA is complete): 16-byte groups of four columns, [group][row], read below
-                for (int c = half * (PN / 64); c < (half + 1) * (PN / 64); ++c) {  // 32 columns
+                for (int c = half * (kTileN / 64); c < (half + 1) * (kTileN / 64); ++c) {  // 32 columns
                     uint32_t v[32];
                     ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
                     ptx::tmem_ld_wait();

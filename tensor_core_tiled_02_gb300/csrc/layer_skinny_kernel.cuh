@@ -13,11 +13,15 @@
 // shared memory: each CTA of the cluster sums a share of the tile's tokens, in
 // rank order (the same bits every time), a warp at a time on the 128 columns of
 // one token, and applies the epilogue (layer_pair_kernel.cuh names them).
-//   push  (up to 16 tokens) every thread sends its column's values straight from
-//         Tensor Memory to the CTA that sums the token, which waits for the bytes
-//         on an mbarrier: the way from the last product to the sums takes 0.5 us
+//   push  (a plain product of up to 4 tokens, up to 4 CTAs) every thread sends its
+//         column's values straight from Tensor Memory to the CTA that sums the token,
+//         which waits for the bytes on an mbarrier
 //   pull  each CTA leaves its partial in its idle ring, the cluster meets at a
-//         barrier, then reads: 1.1 us, but no room taken from the ring
+//         barrier, then reads
+//
+// One token, bf16: K = N = 4096 8.5 us (4.0 TB/s of weights), K = 4096, N = 14336 20.7
+// (5.7 TB/s), K = N = 8192 22.7 (5.9 TB/s); gated block of 4096 x 14336, two launches,
+// 57.5 (6.1 TB/s).
 //
 // Roles: warp 0 lane 0 loads, warp 1 lane 0 issues MMAs, warps 2-5 read the
 // accumulator; all six reduce and store.  Every wait is bounded.
@@ -29,7 +33,8 @@ namespace tcgemm {
 
 constexpr int kSkinnySlots = 12;     // most ring slots
 constexpr int kSkinnySplit = 16;     // most CTAs sharing a tile (above 8 a non-portable cluster)
-constexpr int kPushTokens = 16;      // most tokens whose partials are pushed
+constexpr int kPushTokens = 4;       // most tokens whose partials are pushed, and most CTAs
+constexpr int kPushSplit = 4;        // that push them to one another
 constexpr int kSkinnyTileBytes = 128 * 64 * 2;  // one weight tile of one K step
 
 struct SkinnyMaps {
@@ -157,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
     constexpr bool GATE = EPI == kEpiGate;
     constexpr int kTiles = GATE ? 2 : 1;
+    static_assert(!PUSH || EPI == kEpiStore, "pushed partials: one weight, the plain epilogue");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t ring = (raw + 1023u) & ~1023u;
@@ -167,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 #ifdef TCGEMM_CHECK
     if (bar0 + 8u * (2 * kSkinnySlots + 2) + 8u > raw + ptx::dynamic_smem_size() ||
-        (PUSH ? p.split * ((p.T + p.split - 1) / p.split) * kTiles * 512 > p.recv_bytes
+        (PUSH ? p.split * ((p.T + p.split - 1) / p.split) * 512 > p.recv_bytes || p.T > kPushTokens
                 : kTiles * p.nt * 512 > S * p.stage_bytes)) {
         if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
         return;  // every CTA decides alike
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int rank = (int)blockIdx.x % CS;
     const int tile = (int)blockIdx.x / CS;
     const int n0 = (tile / p.t_tiles) * 128, t0 = (tile % p.t_tiles) * p.nt;
-    // this CTA's tokens of the tile; pushed partials lie [rank][own token][weight][128 columns]
+    // this CTA's tokens of the tile; pushed partials lie [rank][own token][128 columns]
     const int tokens = min(p.nt, p.T - t0);
     const int own0 = tokens * rank / CS, own1 = tokens * (rank + 1) / CS;
     const int most = (tokens + CS - 1) / CS;
@@ -197,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         ptx::mbar_init(recv_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
-        if (PUSH && own1 > own0) ptx::mbar_arrive_expect_tx(recv_bar, (uint32_t)((own1 - own0) * CS * kTiles * 512));
+        if (PUSH && own1 > own0) ptx::mbar_arrive_expect_tx(recv_bar, (uint32_t)((own1 - own0) * CS * 512));
         ptx::prefetch_tmap(&tm.w[0]);
         ptx::prefetch_tmap(&tm.x[0]);
     }
@@ -360,23 +366,20 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             (void)accs;
             if (PUSH) {
-#pragma unroll 1
-                for (int i = 0; i < kTiles; ++i) {
-                    uint32_t v[16];
-                    load16(i * p.nt, v);
-                    // token t goes to the CTA whose share holds it
-                    int to = 0, first = 0, next = tokens / CS;
+                uint32_t v[16];
+                load16(0, v);
+                // token t goes to the CTA whose share holds it
+                int to = 0, first = 0, next = tokens / CS;
 #pragma unroll
-                    for (int t = 0; t < kPushTokens; ++t) {
-                        if (t < tokens) {
-                            while (t >= next) {
-                                ++to;
-                                first = next;
-                                next = tokens * (to + 1) / CS;
-                            }
-                            const uint32_t at = recv + (uint32_t)(((rank * most + t - first) * kTiles + i) * 512) + col;
-                            st_async_b32(ptx::mapa(at, to), v[t], ptx::mapa(recv_bar, to));
+                for (int t = 0; t < kPushTokens; ++t) {
+                    if (t < tokens) {
+                        while (t >= next) {
+                            ++to;
+                            first = next;
+                            next = tokens * (to + 1) / CS;
                         }
+                        const uint32_t at = recv + (uint32_t)((rank * most + t - first) * 512) + col;
+                        st_async_b32(ptx::mapa(at, to), v[t], ptx::mapa(recv_bar, to));
                     }
                 }
             } else {
@@ -415,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         // A warp on each of this CTA's tokens, a lane four columns.  Where partials are
         // pulled, first the sums over the cluster, kept in this CTA's own partial (nobody
         // else reads these tokens of it): all ranks' values of a batch of tokens at once,
-        // so that the reads of other CTAs' shared memory overlap, and apart from the
-        // epilogue, whose code in every batch would cost instruction fetches.
+        // so that the reads of other CTAs' shared memory overlap.
         const int c = lane * 4, n = n0 + c, left = p.N - n;
         const int tt_begin = own0 + warp, tt_end = own1;
         constexpr int kWarps = kThreads / 32;
@@ -437,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll 4
                     for (int r = 0; r < CS; ++r) {
                         float a, b, d, e;
-                        ld_shared_f4(recv + (uint32_t)(((r * most + tt - own0) * kTiles + i) * 512 + c * 4), a, b, d, e);
+                        ld_shared_f4(recv + (uint32_t)((r * most + tt - own0) * 512 + c * 4), a, b, d, e);
                         f[i][0] += a, f[i][1] += b, f[i][2] += d, f[i][3] += e;
                     }
                 } else {

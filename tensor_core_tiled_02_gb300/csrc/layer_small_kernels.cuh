@@ -198,8 +198,8 @@ struct LossParams {
 // lse = max + ln(sum over parts of s_i exp(m_i - max)); loss = lse - target's
 // logit.  An ignored row's loss is 0; a target that is neither ignored nor a
 // word makes its row's loss NaN.  32 rows a block, 32 slices of the parts, each
-// slice four independent loads at a time (the pass is latency: 7.0 us for 8 rows
-// x 128 parts with 8 slices and one load at a time).
+// slice four independent loads at a time: the pass is latency (1000 rows x 391
+// parts, 3.2 MB, 10 us from a cold cache).
 __global__ void __launch_bounds__(1024) layer_loss_rows_kernel(const LossParams p) {
     __shared__ float2 part[32][33];
     const int l = threadIdx.x & 31, slice = threadIdx.x >> 5;
