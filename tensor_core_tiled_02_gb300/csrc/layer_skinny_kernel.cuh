@@ -21,7 +21,7 @@
 //
 // One token, bf16: K = N = 4096 8.5 us (4.0 TB/s of weights), K = 4096, N = 14336 20.7
 // (5.7 TB/s), K = N = 8192 22.7 (5.9 TB/s); gated block of 4096 x 14336, two launches,
-// 57.5 (6.1 TB/s).
+// 57.2 (6.2 TB/s).
 //
 // Roles: warp 0 lane 0 loads, warp 1 lane 0 issues MMAs, warps 2-5 read the
 // accumulator; all six reduce and store.  Every wait is bounded.
@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             // Before the wait for the previous kernel, where that kernel is this call's own and
             // does not write the weights: the first of them.  (Elsewhere, asking L2 for them
-            // before the wait measured slower: 8.7 -> 10.2 us for one token at K = N = 4096, the
-            // requests are as scarce as the bytes.)
+            // before the wait measured slower: 8.7 -> 9.0 us for one step of one token at
+            // K = N = 4096, 9.9 for four.)
             const int pre = p.weights_early ? min(S, k1 - k0) : 0;
             for (int i = 0; i < pre; ++i) load_weights(k0 + i, i);
             ptx::grid_dependency_wait();
