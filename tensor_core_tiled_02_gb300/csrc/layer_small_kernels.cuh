@@ -276,7 +276,8 @@ __device__ __forceinline__ T block_join(T v, T* scratch, F join) {
 // loss = sum of the rows' losses, over the rows that count when mean.  One
 // block; each thread sums every 1024th row with Kahan's compensation, then
 // pairwise (fp64, which this GPU runs at a small fraction of fp32's rate, took 14.5
-// us here; this takes 3).
+// us here; this takes 3).  A sum that is infinite has nothing to compensate: its
+// difference to the terms would be NaN and spread to the rows that follow.
 __global__ void __launch_bounds__(1024) layer_loss_sum_kernel(const float* row_loss, const long long* target, float* loss,
                                                              int rows, long long ignore_index, int mean) {
     __shared__ float fscratch[32];
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(1024) layer_loss_sum_kernel(const float* row_l
     int n = 0;
     for (int r = threadIdx.x; r < rows; r += 1024) {
         const float y = __fsub_rn(row_loss[r], lost), t = __fadd_rn(s, y);
-        lost = __fsub_rn(__fsub_rn(t, s), y);
+        lost = isinf(t) ? 0.0f : __fsub_rn(__fsub_rn(t, s), y);
         s = t;
         n += target[r] != ignore_index;
     }
