@@ -286,9 +286,10 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
     const bool two = cols <= 128 && in_flight >= (gate ? 65536 : 81920);
     // (After this call's own kernel the weights' first loads run under that kernel's
     // end, and twice the CTAs start more of them: worth it where 16 steps each remain.
-    // Gated block for one token, 4096 x 14336: 61.7 -> 57.0 us.)
+    // Gated block for one token, 4096 x 14336: 61.7 -> 57.0 us.  Not for the loss's logits:
+    // both passes take the same plan, so that they sum them alike.)
     const int each = sms * 4 / 5;
-    const bool twice = two && (gate || (q.after_own && (long long)k_steps * g.tiles >= 32ll * each));
+    const bool twice = two && (gate || (q.after_own && epi != kEpiLossGrad && (long long)k_steps * g.tiles >= 32ll * each));
     const int want = twice ? 2 * each : each;
     int split = 1;
     for (int s = 2; s <= kSkinnySplit && s * 2 <= k_steps && g.tiles * split < want; ++s)
@@ -296,7 +297,7 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
     g.split = split;
     // the loss's logits in up to eight accumulators, kPromote steps each where there is room
     g.accs = 1;
-    if (epi == kEpiLossStats) {
+    if (epi == kEpiLossStats || epi == kEpiLossGrad) {
         const int room = (two ? 256 : 512) / g.nt, steps = ceil_div(k_steps, split);
         g.accs = room < 8 ? room : 8;
         if (g.accs > ceil_div(steps, kPromote)) g.accs = ceil_div(steps, kPromote);
@@ -438,6 +439,8 @@ int run_product_as(const Product& q, const Ctx& c) {
     }
     if constexpr (EPI == kEpiLossStats)
         if (g.k_steps > kPromote) return run_product_pair<LAY, kEpiLossStatsLong, DT, false>(q, g, c);
+    if constexpr (EPI == kEpiLossGrad)
+        if (g.k_steps > kPromote) return run_product_pair<LAY, kEpiLossGradLong, DT, false>(q, g, c);
     if constexpr (EPI == kEpiStore)
         if (g.split > 1) return run_product_pair<LAY, EPI, DT, true>(q, g, c);
     return run_product_pair<LAY, EPI, DT, false>(q, g, c);

@@ -21,6 +21,9 @@
 //                   in fp32 every 2048 of K
 //   kEpiLossGrad    v = logits again: (exp(v - lse) - [column = target]) times the row's
 //                   weight, in 16 bits, operand of the two products that follow
+//   kEpiLossGradLong   the same with the logits summed as in kEpiLossStatsLong, so that
+//                   they are those the lse was made of, to the bit: where a target's p is
+//                   near 1, p - 1 is smaller than what the two ways of summing differ by
 //
 // Two operand pairs may follow one another along K (dx = dg Wg^T + du Wu^T is
 // one product whose K is both halves): K steps from k_switch on read a[1], b[1].
@@ -59,10 +62,12 @@ enum LayerEpilogue {
     kEpiLossStats = 4,
     kEpiLossGrad = 5,
     kEpiLossStatsLong = 6,
+    kEpiLossGradLong = 7,
 };
 
 constexpr int kLayerMaxSplit = 4;
-constexpr int kPromote = 32;           // kEpiLossStatsLong: K steps (of 64) summed on the tensor core at a time
+__host__ __device__ constexpr bool loss_long(int epi) { return epi == kEpiLossStatsLong || epi == kEpiLossGradLong; }
+constexpr int kPromote = 32;           // loss_long: K steps (of 64) summed on the tensor core at a time
 
 struct LayerMaps {
     CUtensorMap a[2], b[2];
@@ -98,7 +103,7 @@ struct LayerPairLayout {
     static constexpr int kABytes = 128 * 64 * 2;         // this CTA's 128 rows of one K step
     static constexpr int kBBytes = (kTileN / 2) * 64 * 2;    // this CTA's half of the columns
     static constexpr int kStageBytes = kABytes + kBBytes;
-    static constexpr int kWarps = SPLIT || EPI == kEpiLossStatsLong ? 8 : 4;  // epilogue warps
+    static constexpr int kWarps = SPLIT || loss_long(EPI) ? 8 : 4;  // epilogue warps
     static constexpr int kThreads = 64 + 32 * kWarps;
     static constexpr int kWarpStaging = EPI == kEpiLossStats || EPI == kEpiLossStatsLong ? 0 : 65536 / kWarps;  // staging per epilogue warp
     // full[8], empty[8], tmem_full[2], tmem_empty[2], drain, aux[warps][2]
@@ -288,9 +293,9 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             int tl = 0;
             bool ok = true;
             for (int t = cluster; ok && t < tiles; t += clusters) {
-                // one accumulator a tile, or (kEpiLossStatsLong) one every kPromote steps
+                // one accumulator a tile, or (loss_long) one every kPromote steps
                 for (int ks = kb0, ke; ok && ks < kb1; ks = ke) {
-                    ke = EPI == kEpiLossStatsLong ? min(kb1, ks + kPromote) : kb1;
+                    ke = loss_long(EPI) ? min(kb1, ks + kPromote) : kb1;
                     const int acc = tl & 1;
                     const uint32_t aph = (tl >> 1) & 1;
                     ++tl;
@@ -333,18 +338,21 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             ptx::mma_commit_pair(drain_bar);
             wait_drain(drain_bar, 0, p.wait_limit);
         }
-    } else if constexpr (EPI == kEpiLossStatsLong) {
-        // ---------------- statistics (both CTAs): 32 rows x 128 columns a warp ----------------
+    } else if constexpr (loss_long(EPI)) {
+        // ---------------- loss, long K (both CTAs): 32 rows x 128 columns a warp ----------------
         // The running sums of kPromote steps each are added up here in fp32, rounded to
         // nearest, 128 columns a thread: the tensor core's own accumulation truncates, and its
         // bias, below 1e-6 of the loss up to K = 2048, reached 8e-6 at K = 8192.  (For K up to
-        // 2048 the other form's four warps cost less: 4096 tokens, K = 1024, 32768 words 160 us
-        // against 172.)
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        // 2048 the other form's four warps cost less: statistics of 4096 tokens, K = 1024, 32768
+        // words 160 us against 172.)
+        const int ew = warp - 2, q = warp & 3, half = ew >> 2;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
+        const uint32_t stg = sC + (uint32_t)(ew * L::kWarpStaging);
+        (void)stg;
         ptx::grid_dependency_wait();
         ptx::grid_launch_dependents();
         int tl = 0;
+        unsigned n_chunk = 0;  // kEpiLossGradLong: chunks of 64 columns stored; their two buffers alternate
         bool ok = true;
         for (int t = cluster; ok && t < tiles; t += clusters) {
             int mb, nb;
@@ -352,6 +360,16 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             const int row0 = mb * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
             const int x = nb * kTileN + half * 128;
             const bool mine = row0 < p.M && x < p.N;
+            float lse = 0.0f, scale = 0.0f;
+            int tcol = -1;  // the target's column, relative to this warp's
+            if (mine && row < p.M) {
+                const long long tg = p.target[row] - p.col0 - x;
+                if (tg >= 0 && tg < 128 && tg < p.N - x) tcol = (int)tg;
+                if constexpr (EPI == kEpiLossGradLong) {
+                    lse = p.lse[row];
+                    scale = p.row_scale[row];
+                }
+            }
             float v[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) v[i] = 0.0f;
@@ -376,39 +394,67 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                     ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), leader));
             }
             if (!ok || !mine) continue;
-            int tcol = -1;  // the target's column, relative to this warp's
-            if (row < p.M) {
-                const long long tg = p.target[row] - x;
-                if (tg >= 0 && tg < 128 && tg < p.N - x) tcol = (int)tg;
-            }
-            if (tcol >= 0) {
-                float picked = 0.0f;
+            if constexpr (EPI == kEpiLossStatsLong) {
+                if (tcol >= 0) {
+                    float picked = 0.0f;
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i == tcol) picked = v[i];
-                p.target_logit[row] = picked;
-            }
-            __syncwarp();
-            if (p.N - x < 128) {  // columns from N on are no words
+                    for (int i = 0; i < 128; ++i)
+                        if (i == tcol) picked = v[i];
+                    p.target_logit[row] = picked;
+                }
+                __syncwarp();
+                if (p.N - x < 128) {  // columns from N on are no words
 #pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i >= p.N - x) v[i] = -INFINITY;
-            }
-            float m0 = v[0], m1 = v[1];
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= p.N - x) v[i] = -INFINITY;
+                }
+                float m0 = v[0], m1 = v[1];
 #pragma unroll
-            for (int i = 2; i < 128; i += 2) {
-                m0 = fmaxf(m0, v[i]);
-                m1 = fmaxf(m1, v[i + 1]);
-            }
-            const float m = fmaxf(m0, m1);
-            // the difference before the factor: a maximum near the type's lowest times log2(e)
-            // would overflow.  (While all is -inf the terms are exp(-inf - 0) = 0.)
-            const float mf = m == -INFINITY ? 0.0f : m;
-            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 2; i < 128; i += 2) {
+                    m0 = fmaxf(m0, v[i]);
+                    m1 = fmaxf(m1, v[i + 1]);
+                }
+                const float m = fmaxf(m0, m1);
+                // the difference before the factor: a maximum near the type's lowest times log2(e)
+                // would overflow.  (While all is -inf the terms are exp(-inf - 0) = 0.)
+                const float mf = m == -INFINITY ? 0.0f : m;
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int i = 0; i < 128; ++i) s[i & 3] += ex2_approx((v[i] - mf) * 1.4426950408889634f);
-            if (row < p.M) p.stats[(size_t)(x >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+                for (int i = 0; i < 128; ++i) s[i & 3] += ex2_approx((v[i] - mf) * 1.4426950408889634f);
+                if (row < p.M) p.stats[(size_t)(x >> 7) * p.M + row] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    if (x + c * 64 >= p.N) break;
+                    const uint32_t buf = stg + (n_chunk & 1) * 4096u;
+                    if (!TC_CHECK(holds(sC, staging_all, buf, 4096u), kSiteSmemBounds)) break;
+                    if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store two chunks ago has read its buffer
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int col = c * 64 + j * 8 + i;
+                            float e = ex2_approx((v[col] - lse) * 1.4426950408889634f);
+                            if (col == tcol) e -= 1.0f;
+                            f[i] = scale == 0.0f ? 0.0f : e * scale;  // a row of weight 0 is 0 whatever its logits hold
+                        }
+                        ptx::st_shared_v4(swz(buf, lane, j), pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]),
+                                          pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(&tm.out[0], buf, x + c * 64, row0);
+                        ptx::bulk_commit_group();
+                    }
+                    ++n_chunk;
+                }
+            }
         }
+        if (EPI == kEpiLossGradLong && lane == 0) ptx::bulk_wait_group_read<0>();
+        __syncwarp();
     } else {
         // ---------------- epilogue (both CTAs): 32 rows a warp, all columns or (SPLIT) half ----------------
         const int ew = warp - 2;

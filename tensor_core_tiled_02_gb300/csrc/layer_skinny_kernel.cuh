@@ -46,7 +46,7 @@ struct SkinnyParams {
     int t_tiles;             // ceil(T / nt)
     int k_steps, k_switch;   // 64-deep; steps >= k_switch read w[1], x[1] from their start (not kGate)
     int split, slots, stage_bytes, tmem_cols;
-    int accs;                // kEpiLossStats: accumulators the K steps are dealt out to, summed in fp32
+    int accs;                // kEpiLoss*: accumulators the K steps are dealt out to, summed in fp32
     int recv_bytes;          // PUSH: the buffer partials arrive in
     int weights_early;       // the previous kernel is this call's own and does not write the weights
     int act;
@@ -161,6 +161,7 @@ template <bool WMN, int EPI, int DT, bool PUSH>
 __global__ void __launch_bounds__(kThreads, 2)
     layer_skinny_kernel(const __grid_constant__ SkinnyMaps tm, const SkinnyParams p) {
     constexpr bool GATE = EPI == kEpiGate;
+    constexpr bool LOSS = EPI == kEpiLossStats || EPI == kEpiLossGrad;  // logits, summed alike in both passes
     constexpr int kTiles = GATE ? 2 : 1;
     static_assert(!PUSH || EPI == kEpiStore, "pushed partials: one weight, the plain epilogue");
     extern __shared__ uint8_t smem_raw[];
@@ -287,11 +288,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint32_t phase = 0;
             // the loss's logits: consecutive runs of steps into accumulators of their own, as the
             // tensor core's accumulation truncates (layer_pair_kernel.cuh)
-            const int run = EPI == kEpiLossStats ? (k1 - k0 + p.accs - 1) / p.accs : k1 - k0;
+            const int run = LOSS ? (k1 - k0 + p.accs - 1) / p.accs : k1 - k0;
             uint32_t acc_tmem = tmem;
             int in_run = 0;
             for (int kb = k0; kb < k1; ++kb, ++in_run) {
-                if (EPI == kEpiLossStats && in_run == run) {
+                if (LOSS && in_run == run) {
                     in_run = 0;
                     acc_tmem += (uint32_t)p.nt;
                 }
@@ -342,16 +343,16 @@ __global__ void __launch_bounds__(kThreads, 2)
             __syncwarp();
         }
         if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0 &&
-            TC_CHECK(kTiles * p.nt * (EPI == kEpiLossStats ? p.accs : 1) <= p.tmem_cols, kSiteTmemBounds)) {
+            TC_CHECK(kTiles * p.nt * (LOSS ? p.accs : 1) <= p.tmem_cols, kSiteTmemBounds)) {
             ptx::tc_fence_after();
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
             const uint32_t col = (uint32_t)((q * 32 + lane) * 4);
             // accumulators that hold anything (a short K range may leave the last ones empty)
-            const int run = EPI == kEpiLossStats ? (k1 - k0 + p.accs - 1) / p.accs : 1;
-            const int accs = EPI == kEpiLossStats ? (k1 - k0 + run - 1) / run : 1;
+            const int run = LOSS ? (k1 - k0 + p.accs - 1) / p.accs : 1;
+            const int accs = LOSS ? (k1 - k0 + run - 1) / run : 1;
             auto load16 = [&](int c, uint32_t(&v)[16]) {
                 tmem_ld_32x32b_x16(trow + c, v);
-                if constexpr (EPI == kEpiLossStats) {
+                if constexpr (LOSS) {
 #pragma unroll 1
                     for (int a = 1; a < accs; ++a) {
                         uint32_t w[16];

@@ -50,3 +50,52 @@ def test_infinite_loss(tokens, dt):
         t[rows] = IGNORE
         if tokens > 2:
             assert math.isfinite(tc.linear_cross_entropy(h, w, t, ignore_index=IGNORE)[0].item())
+
+def leaning(t, k, v, dt, logit, seed=0):
+    """States along their targets' rows: the target's logit is `logit`, the others' are near 0."""
+    g = torch.Generator(device="cuda").manual_seed(seed + t + k + v)
+    w = (torch.randn(v, k, generator=g, device="cuda") * k ** -0.5).to(dt)
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    rows = w[target].float()
+    h = (rows * (logit / (rows * rows).sum(1, keepdim=True))).to(dt)
+    return h, w, target
+
+
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("piece", [None, 256])
+@pytest.mark.parametrize("shape", [(5, 1024, 300), (5, 8192, 4001), (100, 2056, 300), (100, 8192, 1000), (300, 2048, 1000),
+                                   (300, 8192, 1000), (1100, 4104, 777), (1100, 8192, 600)], ids=str)
+def test_gradient_of_sure_targets(shape, piece, dt):
+    """Targets with 1 - p = 1.5e-4.  p - 1 is a difference of nearly equal values: exp takes the
+    logit minus the log-sum-exp, both held in fp32, so p is off by at most some 2^-22 (1 + |lse|)
+    of itself as long as both passes sum the logits alike, and p - 1 by that over 1 - p of itself.
+    Row by row; d and dh take a rounding each (u / sqrt 3 on average, 2 u allowed).
+    (Logits that differ by 8e-6 between the passes are off by all of 1 - p.)
+
+    With pieces the passes may split the sums over the width differently, so the bound of
+    test_precision_of_wide_logits is added for each of them."""
+    t, k, v = shape
+    logit = math.log(v / 1.5e-4)
+    h, w, target = leaning(t, k, v, dt, logit)
+    scale = 65536.0
+    logits = h.double() @ w.double().T
+    lse = torch.logsumexp(logits, 1)
+    p = torch.exp(logits - lse[:, None])
+    rows = torch.arange(t, device="cuda")
+    # 1 - p without the cancellation
+    rest = p.clone()
+    rest[rows, target] = 0
+    rest = rest.sum(1)
+    d = p.clone()
+    d[rows, target] = -rest
+    want = (d @ w.double()) * (scale / t)
+    _, got_lse = tc.linear_cross_entropy(h, w, target)
+    dh, dw = tc.linear_cross_entropy_backward(torch.tensor(scale, device="cuda"), h, w, target, got_lse, piece=piece)
+    room = 2.0 ** -22 * (1 + lse) / rest + 2 * U[dt]
+    if piece is not None and piece < v:
+        room = room + 2 * 128 * 2.0 ** -25 * logit / rest
+    off = (dh.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert (off <= room).all(), (off.max().item(), room.min().item())
+    want = (d.T @ h.double()) * (scale / t)
+    off = (dw.double() - want).norm() / want.norm()
+    assert off.item() <= room.max().item()
