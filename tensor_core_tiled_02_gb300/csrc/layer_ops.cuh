@@ -250,6 +250,7 @@ constexpr int kSkinnyTwoSmem = 115712;  // two such CTAs fill an SM's 228 KiB
 struct SkinnyPlan {
     int nt, t_tiles, tiles, split, slots, stage_bytes, smem, tmem_cols, waves, k_steps;
     int push, recv_bytes, accs;
+    bool too_long;  // a run of the loss's logits would be longer than allowed
 };
 
 // As pair_cycles.  An SM takes in about 58 bytes a cycle of operands that hit L2; 8,000
@@ -261,7 +262,8 @@ long long skinny_cycles(const SkinnyPlan& g, const Product& q, int weights) {
     return steps > bytes ? steps : bytes;
 }
 
-SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
+// promote: K steps of the loss's logits that may go into one accumulator.
+SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held, int promote) {
     const bool gate = epi == kEpiGate;
     SkinnyPlan g{};
     const int most = gate ? 128 : 256;  // the fp32 partials of a tile have to fit the ring
@@ -295,12 +297,15 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held) {
     for (int s = 2; s <= kSkinnySplit && s * 2 <= k_steps && g.tiles * split < want; ++s)
         if (g.tiles <= held[s] * (two ? 2 : 1)) split = s;
     g.split = split;
-    // the loss's logits in up to eight accumulators, kPromote steps each where there is room
+    // the loss's logits in accumulators of `promote` steps each, if Tensor Memory holds so many
     g.accs = 1;
     if (epi == kEpiLossStats || epi == kEpiLossGrad) {
         const int room = (two ? 256 : 512) / g.nt, steps = ceil_div(k_steps, split);
-        g.accs = room < 8 ? room : 8;
-        if (g.accs > ceil_div(steps, kPromote)) g.accs = ceil_div(steps, kPromote);
+        g.accs = ceil_div(steps, promote);
+        if (g.accs > room) {
+            g.accs = room;
+            g.too_long = true;
+        }
         while (g.tmem_cols < g.accs * g.nt) g.tmem_cols *= 2;
     }
     // Partials of few tokens are pushed within small clusters (pulled and pushed, medians
@@ -432,15 +437,16 @@ int run_product_as(const Product& q, const Ctx& c) {
     if constexpr (LAY != kTN) {
         constexpr int epi = EPI == kEpiStoreF32 ? kEpiStore : EPI;  // the output's type is a parameter there
         if (q.M <= kFewTokens) {
-            const SkinnyPlan f = skinny_plan(q, EPI, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c));
+            const SkinnyPlan f = skinny_plan(q, EPI, c.dev->sms, skinny_clusters<LAY == kNN, epi, DT>(c), kPromote<DT>);
             constexpr int weights = EPI == kEpiGate ? 2 : 1;
-            if (skinny_cycles(f, q, weights) <= pair_cycles(g, q, weights)) return run_product_skinny<LAY == kNN, epi, DT>(q, f, c);
+            if (!f.too_long && skinny_cycles(f, q, weights) <= pair_cycles(g, q, weights))
+                return run_product_skinny<LAY == kNN, epi, DT>(q, f, c);
         }
     }
     if constexpr (EPI == kEpiLossStats)
-        if (g.k_steps > kPromote) return run_product_pair<LAY, kEpiLossStatsLong, DT, false>(q, g, c);
+        if (g.k_steps > kPromote<DT>) return run_product_pair<LAY, kEpiLossStatsLong, DT, false>(q, g, c);
     if constexpr (EPI == kEpiLossGrad)
-        if (g.k_steps > kPromote) return run_product_pair<LAY, kEpiLossGradLong, DT, false>(q, g, c);
+        if (g.k_steps > kPromote<DT>) return run_product_pair<LAY, kEpiLossGradLong, DT, false>(q, g, c);
     if constexpr (EPI == kEpiStore)
         if (g.split > 1) return run_product_pair<LAY, EPI, DT, true>(q, g, c);
     return run_product_pair<LAY, EPI, DT, false>(q, g, c);
@@ -520,7 +526,7 @@ long long alone_cycles(const GradProduct& p, const Ctx& c) {
     const long long bytes = 9500 + product_bytes(q, 1) / 3300;
     if (cost < bytes) cost = bytes;
     if (p.layout != kTN && q.M <= kFewTokens) {
-        const long long few = skinny_cycles(skinny_plan(q, kEpiStore, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c)), q, 1);
+        const long long few = skinny_cycles(skinny_plan(q, kEpiStore, c.dev->sms, skinny_clusters<false, kEpiStore, kF16>(c), 0), q, 1);
         if (few < cost) cost = few;
     }
     return cost;

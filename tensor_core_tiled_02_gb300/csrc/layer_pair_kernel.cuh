@@ -17,8 +17,8 @@
 //   kEpiGateGrad    v = dh: dg = dh u act'(g), du = dh act(g), with g and u loaded
 //   kEpiLossStats   v = logits: per row and tile the maximum and the sum of
 //                   exp(v - maximum), and the target's logit; no logit is stored
-//   kEpiLossStatsLong  the same for K above 2048: the tensor core's sums are added up
-//                   in fp32 every 2048 of K
+//   kEpiLossStatsLong  the same for more than kPromote K steps: the tensor core's sums are
+//                   added up in fp32 every kPromote steps
 //   kEpiLossGrad    v = logits again: (exp(v - lse) - [column = target]) times the row's
 //                   weight, in 16 bits, operand of the two products that follow
 //   kEpiLossGradLong   the same with the logits summed as in kEpiLossStatsLong, so that
@@ -67,7 +67,13 @@ enum LayerEpilogue {
 
 constexpr int kLayerMaxSplit = 4;
 __host__ __device__ constexpr bool loss_long(int epi) { return epi == kEpiLossStatsLong || epi == kEpiLossGradLong; }
-constexpr int kPromote = 32;           // loss_long: K steps (of 64) summed on the tensor core at a time
+// loss_long: K steps (of 64) summed on the tensor core at a time.  It truncates as it adds: a
+// logit whose terms all have one sign is low by 6e-9 of itself a unit of K in fp16 and by half
+// that in bf16, up to 3.6e-6 and 3.4e-6 after these runs (1.2e-5 in fp16 after 2048; terms of
+// random signs lose nothing on average).  Statistics in runs of 2048 took less: 1000 tokens,
+// 2048 x 50021, fp16 133 us against 144; 4096 tokens, 4096 x 65536, bf16 1124 against 1140.
+template <int DT>
+constexpr int kPromote = DT == kF16 ? 8 : 16;
 
 struct LayerMaps {
     CUtensorMap a[2], b[2];
@@ -293,9 +299,9 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             int tl = 0;
             bool ok = true;
             for (int t = cluster; ok && t < tiles; t += clusters) {
-                // one accumulator a tile, or (loss_long) one every kPromote steps
+                // one accumulator a tile, or (loss_long) one every kPromote<DT> steps
                 for (int ks = kb0, ke; ok && ks < kb1; ks = ke) {
-                    ke = loss_long(EPI) ? min(kb1, ks + kPromote) : kb1;
+                    ke = loss_long(EPI) ? min(kb1, ks + kPromote<DT>) : kb1;
                     const int acc = tl & 1;
                     const uint32_t aph = (tl >> 1) & 1;
                     ++tl;
@@ -340,11 +346,8 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
         }
     } else if constexpr (loss_long(EPI)) {
         // ---------------- loss, long K (both CTAs): 32 rows x 128 columns a warp ----------------
-        // The running sums of kPromote steps each are added up here in fp32, rounded to
-        // nearest, 128 columns a thread: the tensor core's own accumulation truncates, and its
-        // bias, below 1e-6 of the loss up to K = 2048, reached 8e-6 at K = 8192.  (For K up to
-        // 2048 the other form's four warps cost less: statistics of 4096 tokens, K = 1024, 32768
-        // words 160 us against 172.)
+        // The sums of kPromote<DT> steps each are added up here in fp32, rounded to nearest, 128
+        // columns a thread.
         const int ew = warp - 2, q = warp & 3, half = ew >> 2;
         const uint32_t lane_base = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 128);
         const uint32_t stg = sC + (uint32_t)(ew * L::kWarpStaging);
@@ -373,7 +376,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             float v[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) v[i] = 0.0f;
-            for (int ks = 0; ks < kb1; ks += kPromote, ++tl) {
+            for (int ks = 0; ks < kb1; ks += kPromote<DT>, ++tl) {
                 const int acc = tl & 1;
                 ok = warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane);
                 if (!ok) break;
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                 }
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && (t + clusters < tiles || ks + kPromote < kb1))
+                if (lane == 0 && (t + clusters < tiles || ks + kPromote<DT> < kb1))
                     ptx::mbar_arrive_cluster(ptx::mapa(tempty_bar(acc), leader));
             }
             if (!ok || !mine) continue;

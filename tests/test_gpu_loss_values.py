@@ -99,3 +99,35 @@ def test_gradient_of_sure_targets(shape, piece, dt):
     want = (d.T @ h.double()) * (scale / t)
     off = (dw.double() - want).norm() / want.norm()
     assert off.item() <= room.max().item()
+
+
+# widths on both sides of the runs in which the logits are summed (512 in fp16, 1024 in bf16), and
+# off their multiples; one CTA, few tokens, pairs with one tile and with several
+LONG = [(300, 520, 3001), (1100, 1024, 9000), (33, 4096, 5000), (200, 4096, 20011), (1, 2048, 1000), (1, 8192, 20011), (5, 2056, 300), (5, 4104, 4001), (100, 2056, 5000), (100, 8192, 20011),
+        (300, 2048, 3001), (300, 2056, 257), (300, 4104, 20011), (300, 8192, 5001), (1100, 2056, 20011), (1100, 8192, 9000)]
+
+
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("shape", LONG, ids=str)
+def test_precision_of_wide_logits(shape, dt):
+    """Targets whose logit's terms all have one sign, the worst for an accumulation that truncates.
+    2^-18 of the largest logit is allowed for it, which the runs keep to (fp16 loses 6e-9 of the
+    sum a unit of K, bf16 half that), and 2^-21 of what it handles for the rest, in fp32.  (Runs of
+    2048 are low by 1.2e-5 and 6e-6, and fail.)"""
+    t, k, v = shape
+    h, w, target = leaning(t, k, v, dt, 14.0)
+    logits = h.double() @ w.double().T
+    lse = torch.logsumexp(logits, 1)
+    loss = lse - logits.gather(1, target[:, None])[:, 0]
+    most = logits.abs().amax(1)
+    room = 2.0 ** -18 * most + 2.0 ** -21 * (1 + lse.abs())
+    got, got_lse = tc.linear_cross_entropy(h, w, target, reduction="none")
+    assert ((got_lse.double() - lse).abs() <= room).all(), ((got_lse.double() - lse).abs() / room).max().item()
+    assert ((got.double() - loss).abs() <= 2 * room).all()
+    total = tc.linear_cross_entropy(h, w, target, reduction="mean")[0].double().item()
+    assert abs(total - loss.mean().item()) <= 2 * room.mean().item()
+    # the bottom of the vocabulary too: a target in the last, ragged tile
+    target = torch.full_like(target, v - 1)
+    loss = lse - logits[:, v - 1]
+    got, _ = tc.linear_cross_entropy(h, w, target, reduction="none")
+    assert ((got.double() - loss).abs() <= 2 * room).all()
