@@ -713,7 +713,10 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                                 with_act(p.act, [&](auto tag) {
                                 constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-                                    for (int i = 0; i < C; ++i) f[i] = act_value<ACT>(f[i]);
+                                    for (int i = 0; i < C; i += 2) {
+                                        const float2 o = parts(act_value2<ACT>(f2(f[i], f[i + 1])));
+                                        f[i] = o.x, f[i + 1] = o.y;
+                                    }
                                 });
                             if (p.addend == 1) {
 #pragma unroll
@@ -785,8 +788,11 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                             with_act(p.act, [&](auto tag) {
                                 constexpr int ACT = decltype(tag)::value;
 #pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    h[i] = act_value<ACT>(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+                                for (int i = 0; i < 32; i += 2) {
+                                    const float2 o = parts(act_value2<ACT>(f2(__uint_as_float(g[i]), __uint_as_float(g[i + 1]))));
+                                    h[i] = o.x * __uint_as_float(u[i]);
+                                    h[i + 1] = o.y * __uint_as_float(u[i + 1]);
+                                }
                             });
 #pragma unroll
                             for (int j = 0; j < 4; ++j)

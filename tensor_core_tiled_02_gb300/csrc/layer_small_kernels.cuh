@@ -8,62 +8,6 @@
 
 namespace tcgemm {
 
-// ---- two fp32 values at a time -----------------------------------------------------------
-// fma.rn.f32x2 and its kin do two in one issue slot: the slope pass is bound by issue
-// (GELU's slope is some 25 operations an element one by one) before HBM.
-
-struct F2 {
-    unsigned long long v;
-};
-__device__ __forceinline__ F2 f2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 parts(F2 a) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 both(float c) { return f2(c, c); }
-// act_slope of two values; GELU's by the formula of normal_cdf, its coefficients halved.
-template <int ACT>
-__device__ __forceinline__ F2 act_slope2(F2 x) {
-    if constexpr (ACT == kActGelu) {
-        F2 ax;
-        ax.v = x.v & 0x7FFFFFFF7FFFFFFFull;
-        const float2 den = parts(fma2(both(0.3275911f * 0.70710678118654752f), ax, both(1.0f)));
-        const F2 t = f2(rcp_approx(den.x), rcp_approx(den.y));
-        const float2 y = parts(mul2(mul2(x, x), both(-0.72134752044448170f)));
-        const F2 e = f2(ex2_approx(y.x), ex2_approx(y.y));
-        F2 q = fma2(t, both(0.5f * 1.061405429f), both(-0.5f * 1.453152027f));
-        q = fma2(t, q, both(0.5f * 1.421413741f));
-        q = fma2(t, q, both(-0.5f * 0.284496736f));
-        q = fma2(t, q, both(0.5f * 0.254829592f));
-        const F2 tail = mul2(q, mul2(t, e));
-        const float2 lo = parts(tail), hi = parts(fma2(tail, both(-1.0f), both(1.0f))), xs = parts(x);
-        const F2 cdf = f2(xs.x < 0.0f ? lo.x : hi.x, xs.y < 0.0f ? lo.y : hi.y);
-        return fma2(mul2(x, both(0.39894228040143268f)), e, cdf);
-    }
-    const float2 xs = parts(x);
-    return f2(act_slope<ACT>(xs.x), act_slope<ACT>(xs.y));
-}
-
 // ---- linear layer: dpre = dy act'(pre), column sums of dpre ------------------------
 //
 // A block takes kSlopeRows rows x 256 columns: 32 groups of 8 columns (16
