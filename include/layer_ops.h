@@ -150,7 +150,9 @@ int linear_cross_entropy_workspace(const loss_args *args, size_t *bytes);
  * grad_loss[0] / targets that count (mean), and 0 for an ignored row.
  *
  * The logits are computed again, a piece of the vocabulary at a time: d of one
- * piece is held in 16 bits in the workspace.  Any workspace from the _workspace
+ * piece is held in 16 bits in the workspace, relative to the largest |weight|; for
+ * dh in fp16 with reduction none relative to each row's own, in a second copy.
+ * Any workspace from the _workspace
  * entry's size for piece = 256 on will do; *piece (a multiple of 256) asks for
  * the size of that piece, or all of vocab when smaller.  More than one piece
  * also takes tokens x dim fp32 for dh's running sum.

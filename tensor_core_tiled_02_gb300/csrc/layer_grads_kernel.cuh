@@ -35,6 +35,8 @@ struct GradsProblem {
     int M, N, tiles_m, tiles_n;
     int k_steps, k_switch;  // steps >= k_switch read the second pair
     int a_mn, b_mn;         // operand stored [K, M] (or [K, N]) rather than [M, K] ([N, K])
+    int alpha_rows;         // one alpha a row
+    const float* alpha;     // device scalar or [M], NULL for 1
 };
 
 struct GradsParams {
@@ -43,7 +45,6 @@ struct GradsParams {
     int tiles[2];           // of the long and the short group
     int rounds, rem, d;     // the long group's full rounds, the tiles of its last, and see above
     int raster_group;
-    const float* alpha;     // device scalar, or NULL for 1
     long long wait_limit;
     int inject;
 };
@@ -252,7 +253,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem_base + ((uint32_t)(q4 * 32) << 16);
         ptx::grid_dependency_wait();
         ptx::grid_launch_dependents();
-        const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
         unsigned n_chunk = 0;
         int prob, mb, nb;
         for (int i = 0; grads_tile(p, pair, P, i, prob, mb, nb); ++i) {
@@ -260,6 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int acc = i & 1;
             const int row0 = mb * 256 + (int)rank * 128 + q4 * 32, n0 = nb * kTileN;
             const int chunks = row0 < q.M ? min(kTileN / 64, (q.N - n0 + 63) / 64) : 0;
+            float alpha = 1.0f;
+            if (q.alpha != nullptr) alpha = !q.alpha_rows ? *q.alpha : row0 + lane < q.M ? q.alpha[row0 + lane] : 0.0f;
             if (!warp_wait(tfull_bar(acc), (i >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
             const uint32_t trow = lane_base + (uint32_t)(acc * kTileN);

@@ -391,6 +391,7 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.act = q.p.act;
     p.bias = q.p.bias;
     p.alpha = q.p.alpha;
+    p.alpha_rows = q.p.alpha_rows;
     if (EPI == kEpiGateGrad) {
         p.gate = q.in[0].p;
         p.ld_gate = q.in[0].ld;
@@ -404,7 +405,7 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.out = const_cast<void*>(q.out[0].p);
     p.ld_out = q.out[0].ld;
     p.out_f32 = q.out[0].bytes == 4;
-    p.keep0 = const_cast<void*>(q.out[1].p);
+    p.keep0 = const_cast<void*>(q.out[1].p);  // (kEpiGateGrad does not read it)
     p.ld_keep0 = q.out[1].ld;
     const Mat& second = q.out[EPI == kEpiGateGrad ? 1 : 2];
     p.keep1 = const_cast<void*>(second.p);
@@ -415,6 +416,7 @@ int run_product_skinny(const Product& q, const SkinnyPlan& g, const Ctx& c) {
     p.col0 = q.p.col0;
     p.lse = q.p.lse;
     p.row_scale = q.p.row_scale;
+    p.row_scale2 = q.p.row_scale2;
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
     const int smem = g.smem, split = g.split, tiles = g.tiles;
@@ -480,6 +482,8 @@ int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
         g.b_mn = list[i].layout != kNT;
         g.M = (int)q.M;
         g.N = (int)q.N;
+        g.alpha = q.p.alpha;
+        g.alpha_rows = q.p.alpha_rows;
         g.tiles_m = ceil_div(q.M, 256);
         g.tiles_n = ceil_div(q.N, 256);
         g.k_switch = ceil_div(q.K, 64);
@@ -505,7 +509,6 @@ int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
         if (p.d > most) p.d = most;
     }
     p.raster_group = 8;
-    p.alpha = list[0].q.p.alpha;
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
     auto kern = layer_grads_kernel<DT>;
@@ -658,18 +661,28 @@ LossPlan loss_plan(const loss_args& a) {
     return g;
 }
 
-// Backward: weights and the unscale factor, d of one piece, dh's running sum.
+// Backward: weights and the unscale factor, d of one piece, dh's running sum.  With
+// by_rows dh's d is scaled row by row (layer_loss_weights_kernel): two more vectors, and a
+// d of its own where dw is wanted too.
 struct LossGradPlan {
     long long piece;
-    size_t unscale_at, d_at, sum_at, bytes;
+    bool by_rows;
+    int copies;
+    size_t unscale_at, row_weight_at, row_unscale_at, d_at, d2_at, sum_at, bytes;
 };
 
 LossGradPlan loss_grad_plan(const loss_grad_args& a, long long piece) {
     LossGradPlan g{};
     g.piece = piece < a.vocab ? piece : a.vocab;
     g.unscale_at = align256((size_t)a.tokens * 4);
-    g.d_at = g.unscale_at + 256;
-    g.sum_at = g.d_at + align256((size_t)a.tokens * pad8(g.piece) * 2);
+    g.by_rows = a.reduction == LAYER_LOSS_NONE && a.dtype == LAYER_F16 && a.dh;
+    g.copies = g.by_rows && a.dw ? 2 : 1;
+    g.row_weight_at = g.unscale_at + 256;
+    g.row_unscale_at = g.row_weight_at + (g.by_rows ? g.unscale_at : 0);
+    g.d_at = g.row_unscale_at + (g.by_rows ? g.unscale_at : 0);
+    const size_t d_bytes = align256((size_t)a.tokens * pad8(g.piece) * 2);
+    g.d2_at = g.d_at + (g.copies - 1) * d_bytes;
+    g.sum_at = g.d2_at + d_bytes;
     g.bytes = g.sum_at + (g.piece < a.vocab && a.dh ? align256((size_t)a.tokens * ((a.dim + 3) & ~3ll) * 4) : 0);
     return g;
 }
@@ -1126,7 +1139,7 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
     if (loss_grad_plan(a, piece).bytes > have) {
         const size_t fixed = loss_grad_plan(a, 256 < a.vocab ? 256 : a.vocab).bytes;
         if (256 >= a.vocab || fixed > have) return GEMM_ERR_WORKSPACE;
-        piece = 256 + (long long)((have - fixed) / ((size_t)T * 2)) / 256 * 256;
+        piece = 256 + (long long)((have - fixed) / ((size_t)T * 2 * loss_grad_plan(a, 256).copies)) / 256 * 256;
         if (piece >= a.vocab) piece = (a.vocab - 1) / 256 * 256;
         while (piece > 256 && loss_grad_plan(a, piece).bytes > have) piece -= 256;
     }
@@ -1140,14 +1153,17 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
     float* weight = reinterpret_cast<float*>(ws);
     float* unscale = reinterpret_cast<float*>(ws + g.unscale_at);
     const int dtype = (int)a.dtype;
-    rc = launch_pdl(layer_loss_weights_kernel, dim3(1), 1024, 0, 1, c.stream, a.grad_loss, a.target, weight, unscale, (int)T,
-                    a.vocab, a.ignore_index, (int)a.reduction);
+    float* row_weight = g.by_rows ? reinterpret_cast<float*>(ws + g.row_weight_at) : nullptr;
+    float* row_unscale = g.by_rows ? reinterpret_cast<float*>(ws + g.row_unscale_at) : nullptr;
+    rc = launch_pdl(layer_loss_weights_kernel, dim3(1), 1024, 0, 1, c.stream, a.grad_loss, a.target, weight, unscale, row_weight,
+                    row_unscale, (int)T, a.vocab, a.ignore_index, (int)a.reduction);
     if (rc != GEMM_OK) return rc;
     const long long ldsum = (a.dim + 3) & ~3ll;
     for (long long v0 = 0; v0 < a.vocab; v0 += piece) {
         const long long n = a.vocab - v0 < piece ? a.vocab - v0 : piece;
         const bool first = v0 == 0, last = v0 + n == a.vocab;
-        const Mat d = mat16(ws + g.d_at, T, n, pad8(g.piece));
+        const Mat d = mat16(ws + g.d_at, T, n, pad8(g.piece));   // dw's, or both's
+        const Mat d2 = mat16(ws + g.d2_at, T, n, pad8(g.piece));  // dh's
         const Mat wp = mat16(static_cast<const char*>(a.w) + (size_t)v0 * a.ldw * 2, n, a.dim, a.ldw);
         Product q;
         q.after_own = true;
@@ -1160,7 +1176,13 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
         q.p.target = a.target;
         q.p.col0 = (int)v0;
         q.p.lse = a.lse;
-        q.p.row_scale = weight;
+        q.p.row_scale = g.by_rows && !a.dw ? row_weight : weight;
+        if (g.copies == 2) {
+            q.out[1] = d2;
+            q.outs = 2;
+            q.p.keep = 1;
+            q.p.row_scale2 = row_weight;
+        }
         if ((rc = run_product<kNT, kEpiLossGrad>(q, dtype, c)) != GEMM_OK) return rc;
         GradProduct list[2];
         int count = 0;
@@ -1170,12 +1192,13 @@ int linear_cross_entropy_backward(const loss_grad_args* args, gemm_stream_t stre
             Product& s = list[0].q;
             list[0].layout = kNN;
             s.after_own = true;
-            s.a = d;
+            s.a = d2;
             s.b = wp;
             s.M = T;
             s.N = a.dim;
             s.K = n;
-            s.p.alpha = unscale;
+            s.p.alpha = g.by_rows ? row_unscale : unscale;
+            s.p.alpha_rows = g.by_rows;
             s.out[0] = last ? dh : sum;
             if (!first) {
                 s.in[0] = sum;

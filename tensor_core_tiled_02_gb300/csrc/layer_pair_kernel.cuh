@@ -89,15 +89,18 @@ struct LayerParams {
     int split;             // SPLIT: pairs sharing a tile along K
     int act;
     int addend;            // kEpiStore*: 0 none, 1 of the output's type, 2 fp32 under a 16-bit output
-    int keep;              // kEpiStore: keep alpha v + bias in out[1]; kEpiGate: keep g and u in out[1], out[2]
+    int keep;              // kEpiStore: keep alpha v + bias in out[1]; kEpiGate: keep g and u in out[1], out[2];
+                           // kEpiLossGrad*: the same with row_scale2 for row_scale in out[1]
     const void* bias;      // N values of the operands' type, or NULL
     const float* alpha;    // device scalar, or NULL for 1
+    int alpha_rows;        // one alpha a row: [M]
     float2* stats;         // kEpiLossStats: [ceil(N / 128)][M] (maximum, sum of exponentials)
     float* target_logit;   // kEpiLossStats: [M], written where the target's column is met
     const long long* target;  // kEpiLoss*: [M]
     int col0;              // kEpiLossGrad: vocabulary index of the tile grid's first column
     const float* lse;      // kEpiLossGrad: [M]
     const float* row_scale;// kEpiLossGrad: [M], 0 for a row that takes no part
+    const float* row_scale2;
     long long wait_limit;
     int inject;
 };
@@ -363,7 +366,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
             const int row0 = mb * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
             const int x = nb * kTileN + half * 128;
             const bool mine = row0 < p.M && x < p.N;
-            float lse = 0.0f, scale = 0.0f;
+            float lse = 0.0f, scale = 0.0f, scale2 = 0.0f;
             int tcol = -1;  // the target's column, relative to this warp's
             if (mine && row < p.M) {
                 const long long tg = p.target[row] - p.col0 - x;
@@ -371,6 +374,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                 if constexpr (EPI == kEpiLossGradLong) {
                     lse = p.lse[row];
                     scale = p.row_scale[row];
+                    if (p.keep) scale2 = p.row_scale2[row];
                 }
             }
             float v[128];
@@ -429,27 +433,37 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     if (x + c * 64 >= p.N) break;
-                    const uint32_t buf = stg + (n_chunk & 1) * 4096u;
-                    if (!TC_CHECK(holds(sC, staging_all, buf, 4096u), kSiteSmemBounds)) break;
-                    if (lane == 0) ptx::bulk_wait_group_read<1>();  // the store two chunks ago has read its buffer
+                    // one of the two buffers in turn, or both
+                    const uint32_t buf = p.keep ? stg : stg + (n_chunk & 1) * 4096u;
+                    if (!TC_CHECK(holds(sC, staging_all, buf, p.keep ? 8192u : 4096u), kSiteSmemBounds)) break;
+                    if (lane == 0) {
+                        if (p.keep) ptx::bulk_wait_group_read<0>();
+                        else ptx::bulk_wait_group_read<1>();  // the store two chunks ago has read its buffer
+                    }
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float f[8];
+                        float e[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int col = c * 64 + j * 8 + i;
-                            float e = ex2_approx((v[col] - lse) * 1.4426950408889634f);
-                            if (col == tcol) e -= 1.0f;
-                            f[i] = scale == 0.0f ? 0.0f : e * scale;  // a row of weight 0 is 0 whatever its logits hold
+                            e[i] = ex2_approx((v[col] - lse) * 1.4426950408889634f);
+                            if (col == tcol) e[i] -= 1.0f;
                         }
-                        ptx::st_shared_v4(swz(buf, lane, j), pack2<DT>(f[0], f[1]), pack2<DT>(f[2], f[3]),
-                                          pack2<DT>(f[4], f[5]), pack2<DT>(f[6], f[7]));
+                        // a row of weight 0 is 0 whatever its logits hold
+                        auto put = [&](uint32_t to, float by) {
+                            auto at = [&](int i) { return by == 0.0f ? 0.0f : e[i] * by; };
+                            ptx::st_shared_v4(swz(to, lane, j), pack2<DT>(at(0), at(1)), pack2<DT>(at(2), at(3)),
+                                              pack2<DT>(at(4), at(5)), pack2<DT>(at(6), at(7)));
+                        };
+                        put(buf, scale);
+                        if (p.keep) put(buf + 4096, scale2);
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         ptx::tma_store_2d(&tm.out[0], buf, x + c * 64, row0);
+                        if (p.keep) ptx::tma_store_2d(&tm.out[1], buf + 4096, x + c * 64, row0);
                         ptx::bulk_commit_group();
                     }
                     ++n_chunk;
@@ -473,13 +487,13 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
         const bool loads = kLoads && (EPI == kEpiGateGrad || p.addend != 0);
         float alpha = 1.0f;
         if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32)
-            if (p.alpha != nullptr) alpha = *p.alpha;
+            if (p.alpha != nullptr && !p.alpha_rows) alpha = *p.alpha;
 
         // A chunk takes one buffer, or two where two matrices move (kEpiGate that keeps g and
         // u: three); while the staging holds two such sets they alternate, and the
         // next chunk's loads run under this one's work.
         constexpr bool kAlwaysTwo = EPI == kEpiGateGrad;
-        const bool two_bufs = kAlwaysTwo || (EPI == kEpiStore && (p.keep || p.addend == 2));
+        const bool two_bufs = kAlwaysTwo || (EPI == kEpiStore && (p.keep || p.addend == 2)) || (EPI == kEpiLossGrad && p.keep);
         const bool one_set = (EPI == kEpiGate && p.keep) || (SPLIT && two_bufs);
         const bool four_sets = !SPLIT && !loads && !two_bufs && !one_set;  // nothing to load: all four in turn
         auto set_of = [&](unsigned n) {
@@ -543,7 +557,7 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                 }
             }
             // per-row values of the loss epilogues
-            float lse = 0.0f, scale = 0.0f, best = -INFINITY, sum = 0.0f;
+            float lse = 0.0f, scale = 0.0f, scale2 = 0.0f, best = -INFINITY, sum = 0.0f;
             int tcol = -1;  // the target's column, relative to the tile grid
             if constexpr (EPI == kEpiLossStats || EPI == kEpiLossGrad) {
                 if (row < p.M) {
@@ -552,9 +566,12 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                     if constexpr (EPI == kEpiLossGrad) {
                         lse = p.lse[row];
                         scale = p.row_scale[row];
+                        if (p.keep) scale2 = p.row_scale2[row];
                     }
                 }
             }
+            if constexpr (EPI == kEpiStore || EPI == kEpiStoreF32)
+                if (p.alpha_rows) alpha = row < p.M ? p.alpha[row] : 0.0f;
             if (!warp_wait(tfull_bar(acc), aph, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
             const uint32_t trow = lane_base + (uint32_t)(acc * kTileN);
@@ -839,26 +856,30 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                             if (c == c1 - 1 && part == 1) hand_back();
                             const int rel = tcol - x - part * 32;
                             float f[32];
-                            // a row of weight 0 is 0 whatever its logits hold
 #pragma unroll
                             for (int i = 0; i < 32; ++i) {
-                                float e = ex2_approx((__uint_as_float(v[i]) - lse) * 1.4426950408889634f);
-                                if (i == rel) e -= 1.0f;
-                                f[i] = scale == 0.0f ? 0.0f : e * scale;
+                                f[i] = ex2_approx((__uint_as_float(v[i]) - lse) * 1.4426950408889634f);
+                                if (i == rel) f[i] -= 1.0f;
                             }
+                            // a row of weight 0 is 0 whatever its logits hold
+                            auto put = [&](uint32_t to, float by) {
+                                auto at = [&](int i) { return by == 0.0f ? 0.0f : f[i] * by; };
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                ptx::st_shared_v4(swz(buf0, lane, part * 4 + j), pack2<DT>(f[8 * j], f[8 * j + 1]),
-                                                  pack2<DT>(f[8 * j + 2], f[8 * j + 3]),
-                                                  pack2<DT>(f[8 * j + 4], f[8 * j + 5]),
-                                                  pack2<DT>(f[8 * j + 6], f[8 * j + 7]));
+                                for (int j = 0; j < 4; ++j)
+                                    ptx::st_shared_v4(swz(to, lane, part * 4 + j), pack2<DT>(at(8 * j), at(8 * j + 1)),
+                                                      pack2<DT>(at(8 * j + 2), at(8 * j + 3)),
+                                                      pack2<DT>(at(8 * j + 4), at(8 * j + 5)),
+                                                      pack2<DT>(at(8 * j + 6), at(8 * j + 7)));
+                            };
+                            put(buf0, scale);
+                            if (p.keep) put(buf1, scale2);
                         }
                     }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
                         ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
-                        if (EPI == kEpiGateGrad || (EPI == kEpiStore && p.keep))
+                        if (EPI == kEpiGateGrad || ((EPI == kEpiStore || EPI == kEpiLossGrad) && p.keep))
                             ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
                         if (EPI == kEpiGate && p.keep) {
                             ptx::tma_store_2d(&tm.out[1], buf0 + 4096, x, row0);

@@ -52,12 +52,13 @@ struct SkinnyParams {
     int act;
     const void* bias;
     const float* alpha;
+    int alpha_rows;          // one alpha a token: [T]
     const void* addend;      // [T, N]: residual, or an fp32 running sum
     long long ld_addend;
     int addend_f32, out_f32;
     void* out;
     long long ld_out;
-    void *keep0, *keep1;     // x w + bias; kEpiGate: g and u; kEpiGateGrad: du in keep1
+    void *keep0, *keep1;     // x w + bias; kEpiGate: g and u; kEpiGateGrad: du in keep1; kEpiLossGrad: with row_scale2
     long long ld_keep0, ld_keep1;
     const void *gate, *up;   // kEpiGateGrad: [T, N]
     long long ld_gate, ld_up;
@@ -65,7 +66,7 @@ struct SkinnyParams {
     float* target_logit;
     const long long* target; // kEpiLoss*
     int col0;
-    const float *lse, *row_scale;
+    const float *lse, *row_scale, *row_scale2;
     long long wait_limit;
     int inject;
 };
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (here && *abort_flag == 0) {
         // the previous kernel's reads and writes of what is read and written below are done
         ptx::grid_dependency_wait();
-        const float alpha = p.alpha != nullptr ? *p.alpha : 1.0f;
+        const float one_alpha = p.alpha != nullptr && !p.alpha_rows ? *p.alpha : 1.0f;
         // A warp on each of this CTA's tokens, a lane four columns.  Where partials are
         // pulled, first the sums over the cluster, kept in this CTA's own partial (nobody
         // else reads these tokens of it): all ranks' values of a batch of tokens at once,
@@ -476,10 +477,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const long long rel = p.target[t] - p.col0 - n;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float q = ex2_approx((f[0][e] - lse) * 1.4426950408889634f) - (rel == e ? 1.0f : 0.0f);
-                    o[e] = scale == 0.0f ? 0.0f : q * scale;
+                    f[0][e] = ex2_approx((f[0][e] - lse) * 1.4426950408889634f) - (rel == e ? 1.0f : 0.0f);
+                    o[e] = scale == 0.0f ? 0.0f : f[0][e] * scale;
                 }
                 store4<DT>(p.out, t * p.ld_out + n, left, o);
+                if (p.keep0 != nullptr) {
+                    const float scale2 = p.row_scale2[t];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = scale2 == 0.0f ? 0.0f : f[0][e] * scale2;
+                    store4<DT>(p.keep0, t * p.ld_keep0 + n, left, o);
+                }
             } else if constexpr (EPI == kEpiGateGrad) {
                 float g[4], u[4], du[4];
                 load4<DT>(p.gate, t * p.ld_gate + n, left, g);
@@ -505,6 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 });
                 store4<DT>(p.out, t * p.ld_out + n, left, o);
             } else {
+                const float alpha = p.alpha_rows ? p.alpha[t] : one_alpha;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     o[e] = f[0][e] * alpha;

@@ -248,10 +248,15 @@ __global__ void __launch_bounds__(1024) layer_loss_sum_kernel(const float* row_l
 // entry p - 1 rounds as itself, near -1 to next to nothing (with a power of two alone
 // every target's entry took the same rounding of the weight, up to 0.4 % in bf16).
 // Ignored rows weigh 0; a target that is no word makes its row's weight NaN.
-// unscale = the largest weight over 2^14, for the products' epilogues.  One block.
+// unscale = the largest weight over 2^14, for the products' epilogues.  That is right for dw,
+// whose entries are sums over the rows.  A row of dh is its own weight's alone, and where the
+// weights differ (none) fp16 has nothing left of a row 2^-24 of the largest: there dh gets
+// a d whose every row is scaled by 2^14 (row_weight: that, or 0 or NaN as above) and
+// unscaled by row_unscale = the row's weight over 2^14.  (bf16 has the exponents.)  One block.
 __global__ void __launch_bounds__(1024) layer_loss_weights_kernel(const float* grad, const long long* target, float* weight,
-                                                                  float* unscale, int rows, long long vocab,
-                                                                  long long ignore_index, int reduction) {
+                                                                  float* unscale, float* row_weight, float* row_unscale,
+                                                                  int rows, long long vocab, long long ignore_index,
+                                                                  int reduction) {
     __shared__ float fscratch[32];
     __shared__ int iscratch[32];
     ptx::grid_dependency_wait();
@@ -272,6 +277,10 @@ __global__ void __launch_bounds__(1024) layer_loss_weights_kernel(const float* g
         const float w = reduction == 0 ? grad[r] : each;
         weight[r] = t == ignore_index ? 0.0f
                     : t < 0 || t >= vocab ? __int_as_float(0x7FC00000) : scalable ? __fdiv_rn(w, most) * 16384.0f : w;
+        if (row_weight != nullptr) {
+            row_weight[r] = t == ignore_index || w == 0.0f ? 0.0f : t < 0 || t >= vocab ? __int_as_float(0x7FC00000) : 16384.0f;
+            row_unscale[r] = t == ignore_index ? 0.0f : w * (1.0f / 16384.0f);
+        }
     }
     if (threadIdx.x == 0) *unscale = scalable ? most * (1.0f / 16384.0f) : 1.0f;
 }

@@ -153,7 +153,10 @@ def linear_cross_entropy_backward(grad_loss, h, w, target, lse, ignore_index=-10
     h has to be finite in ignored rows too: their weight in dw is 0, not absent.
     """
     if piece is None:
-        piece = max(256, LOSS_PIECE_BYTES // (2 * max(h.shape[0], 1)) // 256 * 256)
+        import torch
+
+        copies = 2 if reduction == "none" and h.dtype == torch.float16 else 1
+        piece = max(256, LOSS_PIECE_BYTES // (2 * copies * max(h.shape[0], 1)) // 256 * 256)
     return _call("linear_cross_entropy_backward", stream, h, grad_loss, h, w, target, lse, ignore_index,
                  _reduction(reduction), piece)
 

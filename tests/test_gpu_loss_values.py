@@ -131,3 +131,86 @@ def test_precision_of_wide_logits(shape, dt):
     loss = lse - logits[:, v - 1]
     got, _ = tc.linear_cross_entropy(h, w, target, reduction="none")
     assert ((got.double() - loss).abs() <= 2 * room).all()
+
+
+@pytest.mark.parametrize("piece", [None, 1024])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("tokens", [6, 40, 400, 1500])
+def test_row_weights_of_very_different_size(tokens, dt, piece):
+    """Reduction "none" with row gradients 2^26 apart: dh row by row.  A row takes the rounding
+    of d and of dh, u / sqrt 3 each on average, and where its own entries near fp16's least
+    normal 2^-25 of half an ulp more, below half a u here: 2 u allowed."""
+    k, v = 64, 5000
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    h = torch.randn(tokens, k, generator=g, device="cuda").to(dt)
+    w = (torch.randn(v, k, generator=g, device="cuda") * 0.25).to(dt)
+    target = torch.randint(0, v, (tokens,), generator=g, device="cuda")
+    weight = 2.0 ** torch.randint(-12, 15, (tokens,), generator=g, device="cuda").float()
+    weight[0], weight[1] = 2.0 ** 14, 2.0 ** -12
+    weight[2] *= -1
+    target[3] = IGNORE
+    weight[4] = 0
+    logits = h.double() @ w.double().T
+    p = torch.softmax(logits, 1)
+    word = target.clamp(min=0)
+    p[torch.arange(tokens, device="cuda"), word] -= 1
+    p = p * (weight.double() * (target != IGNORE))[:, None]
+    want, want_w = p @ w.double(), p.T @ h.double()
+    _, lse = tc.linear_cross_entropy(h, w, target, ignore_index=IGNORE, reduction="none")
+    dh, dw = tc.linear_cross_entropy_backward(weight, h, w, target, lse, ignore_index=IGNORE, reduction="none", piece=piece)
+    assert torch.count_nonzero(dh[3]) == 0 and torch.count_nonzero(dh[4]) == 0
+    keep = [i for i in range(tokens) if i not in (3, 4)]
+    off = (dh.double() - want)[keep].norm(dim=1) / want[keep].norm(dim=1)
+    assert (off <= 2 * U[dt]).all(), (off.max().item() / U[dt])
+    # (a few entries of dw pass fp16's largest value and are infinite)
+    fits = want_w.abs() <= torch.finfo(dt).max
+    assert ((dw.double() - want_w)[fits & torch.isfinite(dw)].norm() / want_w[fits].norm()).item() <= 2 * U[dt]
+    beyond = want_w.abs() > torch.finfo(dt).max * (1 - 4 * U[dt])
+    assert not (torch.isinf(dw) & ~beyond).any() and not torch.isnan(dw).any()
+    # a target that is no word makes its row NaN, and no other
+    target[5] = v
+    dh2, _ = tc.linear_cross_entropy_backward(weight, h, w, target, lse, ignore_index=IGNORE, reduction="none", piece=piece)
+    keep = [i for i in range(tokens) if i != 5]
+    assert torch.isnan(dh2[5]).all() and torch.equal(dh2[keep], dh[keep])
+
+
+@pytest.mark.parametrize("reduction", [0, 1], ids=["none", "mean"])
+@pytest.mark.parametrize("dt", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("tokens", [7, 300])
+def test_one_gradient_alone(tokens, dt, reduction):
+    """Through the C ABI: dh or dw left out, in workspaces of their own size, the same bits."""
+    import ctypes
+    import struct
+
+    lib = tc.load_library()
+    k, v, piece = 72, 1500, 512
+    g = torch.Generator(device="cuda").manual_seed(tokens)
+    h = torch.randn(tokens, k, generator=g, device="cuda").to(dt)
+    w = (torch.randn(v, k, generator=g, device="cuda") * 0.25).to(dt)
+    target = torch.randint(0, v, (tokens,), generator=g, device="cuda")
+    grad = 2.0 ** torch.randint(-9, 9, (tokens if reduction == 0 else 1,), generator=g, device="cuda").float()
+    _, lse = tc.linear_cross_entropy(h, w, target)
+
+    def run(want_h, want_w):
+        dh = torch.full((tokens, k), 9.0, device="cuda", dtype=dt)
+        dw = torch.full((v, k), 9.0, device="cuda", dtype=dt)
+        fields = [h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(), grad.data_ptr(),
+                  dh.data_ptr() if want_h else 0, dw.data_ptr() if want_w else 0, k, k, k, k, tokens, k, v,
+                  0 if dt == F16 else 1, IGNORE, reduction, 0, 0]
+        size = ctypes.c_size_t()
+        assert lib.linear_cross_entropy_backward_workspace(struct.pack("19q", *fields), piece, ctypes.byref(size)) == 0
+        ws = torch.empty(size.value, device="cuda", dtype=torch.uint8)
+        fields[-2:] = [ws.data_ptr(), size.value]
+        torch.cuda.synchronize()
+        assert lib.linear_cross_entropy_backward(struct.pack("19q", *fields), None) == 0
+        torch.cuda.synchronize()
+        return dh, dw, size.value
+
+    dh, dw, both = run(True, True)
+    only_h, kept_w, _ = run(True, False)
+    kept_h, only_w, small = run(False, True)
+    assert torch.equal(only_h, dh) and torch.equal(only_w, dw) and small < both
+    assert (kept_w == 9).all() and (kept_h == 9).all()
+    ph, pw = tc.linear_cross_entropy_backward(grad if reduction == 0 else grad[0], h, w, target, lse,
+                                              ignore_index=IGNORE, reduction=("none", "mean")[reduction], piece=piece)
+    assert torch.equal(ph, dh) and torch.equal(pw, dw)
