@@ -33,10 +33,9 @@ uint64_t extent(const Mat& m) { return ((uint64_t)(m.rows - 1) * m.ld + m.cols) 
 int check_mat(const Mat& m) {
     if (empty(m)) return GEMM_OK;
     if (!m.p) return GEMM_ERR_NULL;
-    if (m.ld < m.cols) return GEMM_ERR_DIM;
-    // a tensor map's row stride stays below 2^40 bytes
+    // a tensor map's row stride stays below 2^40 bytes (in elements first: the product may overflow)
+    if (m.ld < m.cols || m.ld >= (1ll << 40) / m.bytes) return GEMM_ERR_DIM;
     if (((uintptr_t)m.p & 15) || (m.ld * m.bytes) % 16 != 0) return GEMM_ERR_ALIGN;
-    if (m.ld * m.bytes >= (1ll << 40)) return GEMM_ERR_DIM;
     return GEMM_OK;
 }
 
