@@ -227,6 +227,19 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t saddr) {
 template <bool MN>
 constexpr uint32_t kSliceStep = MN ? (kUmmaK * 128) >> 4 : (kUmmaK * 2) >> 4;  // descriptor units of 16 bytes
 
+// A TMA store writes whole 16-byte pieces: a row that ends inside one would have zeros
+// behind it, in what may be another matrix's columns.  So tensor maps of 16-bit outputs end
+// at the last whole piece, `n8` = N & ~7 columns, and each lane stores the rest of its row
+// from its 16 bytes `piece` in shared memory.
+__device__ __forceinline__ void store_tail(uint32_t piece, void* out, long long at, int count) {
+    uint32_t w[4];
+    ptx::ld_shared_v4(piece, w[0], w[1], w[2], w[3]);
+    unsigned short* d = static_cast<unsigned short*>(out) + at;
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < count) d[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+}
+
 __device__ __forceinline__ void st_shared_b16(uint32_t addr, unsigned short v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }

@@ -37,6 +37,8 @@ struct GradsProblem {
     int a_mn, b_mn;         // operand stored [K, M] (or [K, N]) rather than [M, K] ([N, K])
     int alpha_rows;         // one alpha a row
     const float* alpha;     // device scalar or [M], NULL for 1
+    void* out;              // the output again, for columns from N & ~7 on (store_tail)
+    long long ld_out;
 };
 
 struct GradsParams {
@@ -292,10 +294,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::st_shared_v4(swz(buf, lane, j), pack2<DT>(at(0), at(1)), pack2<DT>(at(2), at(3)),
                                       pack2<DT>(at(4), at(5)), pack2<DT>(at(6), at(7)));
                 }
+                const int x = n0 + c * 64, n8 = q.N & ~7;
+                if (n8 < q.N && n8 < x + 64 && row0 + lane < q.M)
+                    store_tail(swz(buf, lane, (n8 - x) >> 3), q.out, (row0 + lane) * q.ld_out + n8, q.N - n8);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    ptx::tma_store_2d(&tm.out[prob], buf, n0 + c * 64, row0);
+                    if (x < n8) ptx::tma_store_2d(&tm.out[prob], buf, x, row0);
                     ptx::bulk_commit_group();
                 }
                 ++n_chunk;

@@ -120,6 +120,13 @@ int encode_mat(CUtensorMap* out, const Mat& m, int dtype, uint32_t box_cols, uin
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_TMAP;
 }
 
+// The tensor map of a 16-bit output: its whole 16-byte pieces (store_tail).  Of a matrix
+// without one it is never used.
+int encode_out(CUtensorMap* out, Mat m, int dtype, uint32_t box_rows) {
+    if (m.cols >= 8) m.cols &= ~7ll;
+    return encode_mat(out, m, dtype, 64, box_rows);
+}
+
 template <typename... P, typename... A>
 int launch_pdl(void (*kern)(P...), dim3 grid, int threads, int smem, int cluster, cudaStream_t stream, A&&... args) {
     cudaLaunchConfig_t lc = {};
@@ -218,7 +225,8 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
         if (rc == GEMM_OK) rc = encode_mat(&tm.b[i], bs[i], dtype, 64, kBMN ? 64 : kTileN / 2);
     }
     for (int i = 0; i < q.outs && rc == GEMM_OK && EPI != kEpiLossStats && EPI != kEpiLossStatsLong; ++i)
-        rc = encode_mat(&tm.out[i], q.out[i], dtype, 128 / q.out[i].bytes, 32);
+        rc = EPI == kEpiStore || EPI == kEpiGate ? encode_out(&tm.out[i], q.out[i], dtype, 32)
+                                                 : encode_mat(&tm.out[i], q.out[i], dtype, 128 / q.out[i].bytes, 32);
     for (int i = 0; i < q.ins && rc == GEMM_OK; ++i) rc = encode_mat(&tm.in[i], q.in[i], dtype, 128 / q.in[i].bytes, 32);
     if (rc != GEMM_OK) return rc;
 
@@ -234,6 +242,10 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
     p.split = g.split;
+    for (int i = 0; i < q.outs; ++i) {
+        p.tail_out[i] = const_cast<void*>(q.out[i].p);
+        p.tail_ld[i] = q.out[i].ld;
+    }
     auto kern = layer_pair_kernel<LAY, EPI, DT, SPLIT>;
     static std::atomic<bool> ready[kMaxDevices];
     rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
@@ -493,7 +505,9 @@ int run_grads_as(const GradProduct* list, int n, int longs, const Ctx& c) {
             rc = encode_mat(&tm.a[kGradsProblems], q.a2, dtype, 64, g.a_mn ? 64 : 128);
             if (rc == GEMM_OK) rc = encode_mat(&tm.b[kGradsProblems], q.b2, dtype, 64, g.b_mn ? 64 : 128);
         }
-        if (rc == GEMM_OK) rc = encode_mat(&tm.out[i], q.out[0], dtype, 64, 32);
+        if (rc == GEMM_OK) rc = encode_out(&tm.out[i], q.out[0], dtype, 32);
+        g.out = const_cast<void*>(q.out[0].p);
+        g.ld_out = q.out[0].ld;
     }
     if (rc != GEMM_OK) return rc;
     p.longs = longs;

@@ -101,6 +101,8 @@ struct LayerParams {
     const float* lse;      // kEpiLossGrad: [M]
     const float* row_scale;// kEpiLossGrad: [M], 0 for a row that takes no part
     const float* row_scale2;
+    void* tail_out[3];     // kEpiStore, kEpiGate: the outputs again, for columns from N & ~7 on (store_tail)
+    long long tail_ld[3];
     long long wait_limit;
     int inject;
 };
@@ -875,15 +877,32 @@ __global__ void __launch_bounds__(LayerPairLayout<EPI, SPLIT>::kThreads, 1)
                             if (p.keep) put(buf1, scale2);
                         }
                     }
+                    constexpr bool kTail = EPI == kEpiStore || EPI == kEpiGate;
+                    const int n8 = kTail ? p.N & ~7 : p.N;  // columns the tensor maps hold
+                    if constexpr (kTail) {
+                        if (n8 < p.N && n8 < x + L::kChunk && row < p.M) {
+                            auto tail = [&](uint32_t buf, int o) {
+                                store_tail(swz(buf, lane, (n8 - x) >> 3), p.tail_out[o], row * p.tail_ld[o] + n8, p.N - n8);
+                            };
+                            tail(buf0, 0);
+                            if (EPI == kEpiStore && p.keep) tail(buf1, 1);
+                            if (EPI == kEpiGate && p.keep) {
+                                tail(buf0 + 4096, 1);
+                                tail(buf0 + 8192, 2);
+                            }
+                        }
+                    }
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {
-                        ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
-                        if (EPI == kEpiGateGrad || ((EPI == kEpiStore || EPI == kEpiLossGrad) && p.keep))
-                            ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
-                        if (EPI == kEpiGate && p.keep) {
-                            ptx::tma_store_2d(&tm.out[1], buf0 + 4096, x, row0);
-                            ptx::tma_store_2d(&tm.out[2], buf0 + 8192, x, row0);
+                        if (x < n8) {
+                            ptx::tma_store_2d(&tm.out[0], buf0, x, row0);
+                            if (EPI == kEpiGateGrad || ((EPI == kEpiStore || EPI == kEpiLossGrad) && p.keep))
+                                ptx::tma_store_2d(&tm.out[1], buf1, x, row0);
+                            if (EPI == kEpiGate && p.keep) {
+                                ptx::tma_store_2d(&tm.out[1], buf0 + 4096, x, row0);
+                                ptx::tma_store_2d(&tm.out[2], buf0 + 8192, x, row0);
+                            }
                         }
                         ptx::bulk_commit_group();
                     }
