@@ -17,7 +17,9 @@
  *     (GEMM_ERR_DIM), products of sizes need not.  `tokens` may be 0: outputs
  *     with a row per token are then empty, weight gradients zero.
  *   - Outputs may not overlap inputs or each other (GEMM_ERR_ALIAS), except
- *     where an entry says so.
+ *     where an entry says so.  Matrices that interleave without sharing an
+ *     element are told apart where their row strides are the same (column
+ *     ranges of one buffer); with different strides they are refused.
  *   - Scratch memory comes from the caller as `workspace` (256-byte aligned,
  *     no initial contents needed, free again when the stream has passed the
  *     call).  Its size comes from the *_workspace entry, host-only.

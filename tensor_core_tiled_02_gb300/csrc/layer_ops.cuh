@@ -39,13 +39,15 @@ int check_mat(const Mat& m) {
     return GEMM_OK;
 }
 
+// Bytes [lo, hi), of which a matrix with a row stride takes `width` every `stride`.
 struct Span {
-    uint64_t lo, hi;
+    uint64_t lo, hi, stride, width;
 };
 
 Span span_of(const Mat& m) {
     if (!m.p || empty(m)) return Span{0, 0};
-    return Span{(uint64_t)(uintptr_t)m.p, (uint64_t)(uintptr_t)m.p + extent(m)};
+    return Span{(uint64_t)(uintptr_t)m.p, (uint64_t)(uintptr_t)m.p + extent(m), (uint64_t)m.ld * m.bytes,
+                (uint64_t)m.cols * m.bytes};
 }
 
 Span span_of(const void* p, uint64_t bytes) {
@@ -53,9 +55,15 @@ Span span_of(const void* p, uint64_t bytes) {
     return Span{(uint64_t)(uintptr_t)p, (uint64_t)(uintptr_t)p + bytes};
 }
 
-// Whether any of the `nw` written spans overlaps another of them or a read one.
+// Whether any of the `nw` written spans overlaps another of them or a read one.  Column
+// ranges of the same rows (one stride) may lie side by side.
 bool overlaps(const Span* w, int nw, const Span* r, int nr) {
-    auto meet = [](const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; };
+    auto meet = [](const Span& a, const Span& b) {
+        if (a.lo >= b.hi || b.lo >= a.hi) return false;
+        if (a.stride == 0 || a.stride != b.stride) return true;
+        const uint64_t gap = b.lo >= a.lo ? (b.lo - a.lo) % a.stride : a.stride - (a.lo - b.lo) % a.stride;
+        return gap < a.width || gap + b.width > a.stride;
+    };
     for (int i = 0; i < nw; ++i) {
         for (int j = i + 1; j < nw; ++j)
             if (meet(w[i], w[j])) return true;

@@ -3,7 +3,7 @@ pass: refused on the host, before any CUDA call.  No compute call is made here."
 import pytest
 
 import tensor_core_tiled_02_gb300 as tc
-from test_layer_abi import DIM, GATED, LINEAR, LINEAR_GRAD, LOSS, LOSS_GRAD, P, built  # noqa: F401  (built: a fixture)
+from test_layer_abi import ALIAS, ALIGN, DIM, GATED, LINEAR, LINEAR_GRAD, LOSS, LOSS_GRAD, P, built  # noqa: F401  (built: a fixture)
 
 
 @pytest.fixture(scope="module")
@@ -24,3 +24,20 @@ def test_row_strides_that_overflow(lib, args, entry, names, ld):
              "gated_ffn_forward": dict(residual=P[6], gate=P[7], up=P[8])}.get(entry, {})
     for name in names:
         assert args.call(getattr(lib, entry), None, **there, **{name: ld}) == DIM, name
+
+
+def side(**changes):
+    return LINEAR.call(tc.load_library().linear_forward, None, **changes)
+
+
+@pytest.mark.parametrize("changes", [
+    dict(y=P[0] + 126, ldx=256, ldy=256),                           # one element of x's rows: and no multiple of 16 bytes
+    dict(y=P[0] + 112, ldx=256, ldy=256),                           # x's last eight columns
+    dict(y=P[0] + 272, ldx=256, ldy=256),                           # past the stride, into x's next row
+    dict(y=P[0] + 512 + 272, ldx=256, ldy=256),                     # the same a row on
+    dict(y=P[0] - 512 * 4 + 272, ldx=256, ldy=256),                 # the same before x
+    dict(y=P[0] + 128, ldx=256, ldy=264),                           # another stride
+    dict(y=P[2], residual=P[2] + 512 * 3, ldy=256, ldr=256),        # rows of the residual
+    dict(y=P[2], preact=P[2] + 240, ldy=256, ldp=256)], ids=str)
+def test_overlapping_column_ranges(lib, changes):
+    assert side(**changes) in ((ALIGN,) if changes.get("y") == P[0] + 126 else (ALIAS,))
