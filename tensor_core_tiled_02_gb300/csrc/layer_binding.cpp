@@ -119,6 +119,12 @@ struct Call {
     }
 };
 
+// A tensor the call has written: autograd, which did not see it, must not take a copy it
+// saved for unchanged.  (Inference tensors have no version.)
+void wrote(const at::Tensor& t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 void* ptr(const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 const void* cptr(PyObject* o, const char* name) { return o == Py_None ? nullptr : tensor(o, name).data_ptr(); }
 
@@ -227,6 +233,7 @@ PyObject* py_linear(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
         a.act = integer(v[3]);
         const int rc = abi.linear(&a, c.stream);
         if (rc != 0) return PyLong_FromLong(rc);
+        if (v[6] != Py_None) wrote(y);
         if (save) return wrap_all({y, pre});
         if (v[6] != Py_None) return Py_NewRef(v[6]);
         return wrap(y);
@@ -346,6 +353,7 @@ PyObject* py_gated_ffn(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
         a.act = integer(v[4]);
         const int rc = abi.gated(&a, c.stream);
         if (rc != 0) return PyLong_FromLong(rc);
+        if (v[7] != Py_None) wrote(y);
         if (save) return wrap_all({y, gate, up, hidden});
         if (v[7] != Py_None) return Py_NewRef(v[7]);
         return wrap(y);
@@ -525,6 +533,7 @@ PyObject* py_clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
         a.workspace_bytes = (long long)bytes;
         rc = abi.clip(&a, c.stream);
         if (rc != 0) return PyLong_FromLong(rc);
+        for (Py_ssize_t i = 0; i < n; ++i) wrote(tensor(PyList_GET_ITEM(v[in_place ? 0 : 2], i), "an output"));
         return wrap(norm);
     });
 }
