@@ -12,6 +12,7 @@
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstring>
@@ -166,7 +167,8 @@ double real(PyObject* o) {
     return v;
 }
 
-// No C++ exception leaves a function: refusals become ValueError, torch's own RuntimeError.
+// No C++ exception leaves a function: refusals become ValueError, torch's own what torch makes
+// of them (OutOfMemoryError among them).
 template <typename F>
 PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& f) {
     if (have != want) {
@@ -183,8 +185,8 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& f) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::bad_alloc&) {
         PyErr_NoMemory();
-    } catch (const std::exception& e) {
-        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        torch::translate_exception_to_python(std::current_exception());
     }
     return nullptr;
 }
