@@ -9,6 +9,7 @@
 // their outputs, or the library's status (an int) when it is not 0.
 #include <Python.h>
 
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -170,7 +171,7 @@ double real(PyObject* o) {
 // No C++ exception leaves a function: refusals become ValueError, torch's own what torch makes
 // of them (OutOfMemoryError among them).
 template <typename F>
-PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& f) {
+PyObject* guarded(PyObject* const* v, Py_ssize_t have, Py_ssize_t want, F&& f) {
     if (have != want) {
         PyErr_Format(PyExc_TypeError, "%zd arguments are wanted, got %zd", want, have);
         return nullptr;
@@ -179,6 +180,16 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& f) {
         PyErr_SetString(PyExc_RuntimeError, "the library is not bound");
         return nullptr;
     }
+    // before the call, so that a warning turned into an error leaves everything as it was
+    if (at::GradMode::is_enabled())
+        for (Py_ssize_t i = 0; i < have; ++i)
+            if (THPVariable_Check(v[i]) && THPVariable_Unpack(v[i]).requires_grad()) {
+                if (PyErr_WarnEx(PyExc_UserWarning,
+                                 "a layer operator was given a tensor that requires a gradient: it records no autograd "
+                                 "graph, its gradients are those of its _backward call (torch.no_grad() says so)", 1) < 0)
+                    return nullptr;
+                break;
+            }
     try {
         return f();
     } catch (const Refusal& e) {
@@ -193,7 +204,7 @@ PyObject* guarded(Py_ssize_t have, Py_ssize_t want, F&& f) {
 
 // (x, w, bias, act, residual, save, out) -> y, or (y, preact)
 PyObject* py_linear(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 7, [&]() -> PyObject* {
+    return guarded(v, nargs, 7, [&]() -> PyObject* {
         const at::Tensor& x = Call::checked(tensor(v[0], "x"), "x");
         const at::Tensor& w = tensor(v[1], "w");
         const int64_t tokens = x.size(0), k = x.size(1);
@@ -244,7 +255,7 @@ PyObject* py_linear(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
 
 // (dy, x, w, act, preact, bias) -> (dx, dw, dbias)
 PyObject* py_linear_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 6, [&]() -> PyObject* {
+    return guarded(v, nargs, 6, [&]() -> PyObject* {
         const at::Tensor& x = Call::checked(tensor(v[1], "x"), "x");
         const at::Tensor &dy = tensor(v[0], "dy"), &w = tensor(v[2], "w");
         const int64_t tokens = x.size(0), k = x.size(1);
@@ -304,7 +315,7 @@ Gated gated_sizes(const at::Tensor& x, const at::Tensor& wg, const at::Tensor& w
 
 // (x, w_gate, w_up, w_down, act, residual, save, out) -> y, or (y, gate, up, hidden)
 PyObject* py_gated_ffn(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 8, [&]() -> PyObject* {
+    return guarded(v, nargs, 8, [&]() -> PyObject* {
         const at::Tensor& x = Call::checked(tensor(v[0], "x"), "x");
         const at::Tensor &wg = tensor(v[1], "w_gate"), &wu = tensor(v[2], "w_up"), &wd = tensor(v[3], "w_down");
         const Gated s = gated_sizes(x, wg, wd);
@@ -364,7 +375,7 @@ PyObject* py_gated_ffn(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
 
 // (dy, x, w_gate, w_up, w_down, gate, up, hidden, act) -> (dx, dw_gate, dw_up, dw_down)
 PyObject* py_gated_ffn_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 9, [&]() -> PyObject* {
+    return guarded(v, nargs, 9, [&]() -> PyObject* {
         static const char* const names[8] = {"dy", "x", "w_gate", "w_up", "w_down", "gate", "up", "hidden"};
         const at::Tensor& x = Call::checked(tensor(v[1], "x"), "x");
         const Gated s = gated_sizes(x, tensor(v[2], "w_gate"), tensor(v[4], "w_down"));
@@ -409,7 +420,7 @@ PyObject* py_gated_ffn_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs)
 
 // (h, w, target, ignore_index, reduction) -> (loss, lse)
 PyObject* py_loss(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 5, [&]() -> PyObject* {
+    return guarded(v, nargs, 5, [&]() -> PyObject* {
         const at::Tensor& h = Call::checked(tensor(v[0], "h"), "h");
         const at::Tensor &w = tensor(v[1], "w"), &target = tensor(v[2], "target");
         if (w.dim() != 2 || w.size(0) < 1 || h.size(1) < 1) refuse("w must be [vocabulary, features] and not empty");
@@ -446,7 +457,7 @@ PyObject* py_loss(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
 
 // (grad_loss, h, w, target, lse, ignore_index, reduction, piece) -> (dh, dw)
 PyObject* py_loss_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 8, [&]() -> PyObject* {
+    return guarded(v, nargs, 8, [&]() -> PyObject* {
         const at::Tensor& h = Call::checked(tensor(v[1], "h"), "h");
         const at::Tensor &grad = tensor(v[0], "grad_loss"), &w = tensor(v[2], "w");
         const at::Tensor &target = tensor(v[3], "target"), &lse = tensor(v[4], "lse");
@@ -491,7 +502,7 @@ PyObject* py_loss_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
 
 // (grads, max_norm, out, eps) -> norm; grads and out are lists
 PyObject* py_clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
-    return guarded(nargs, 4, [&]() -> PyObject* {
+    return guarded(v, nargs, 4, [&]() -> PyObject* {
         if (!PyList_Check(v[0]) || PyList_GET_SIZE(v[0]) < 1) refuse("gradients must be a list that is not empty");
         const bool in_place = v[2] == Py_None;
         const Py_ssize_t n = PyList_GET_SIZE(v[0]);

@@ -12,7 +12,8 @@ Calls are asynchronous on ``stream`` (default: torch's current stream of the
 tensors' device).  Outputs and workspaces that a call allocates belong to that
 stream; tensors handed in must be ready on it, and live until it has passed.
 The calls do not record an autograd graph: each forward pass has its
-``_backward``.  ``ValueError`` for tensors a call cannot take, ``GemmError``
+``_backward``, and a tensor that requires a gradient is warned of unless gradients
+are off.  Tensors written in place or through ``out`` change their version.  ``ValueError`` for tensors a call cannot take, ``GemmError``
 for a status of the library.
 """
 from __future__ import annotations

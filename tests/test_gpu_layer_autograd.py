@@ -1,4 +1,6 @@
 """What autograd sees of the layer operators, which it does not run."""
+import warnings
+
 import pytest
 
 import tensor_core_tiled_02_gb300 as tc
@@ -63,3 +65,26 @@ def test_inference_tensors():
         tc.clip_grad_norm([y], 1.0)
     tc.linear(x, w, out=y)
     assert (y == 64).all()
+
+
+def test_operands_that_require_gradients():
+    """The call goes through and says that it records no graph; silent where gradients are off."""
+    x, w = ones(8, 64), ones(64, 64).requires_grad_(True)
+    y = ones(8, 64)
+    h, target = ones(8, 64).requires_grad_(True), torch.zeros(8, dtype=torch.int64, device="cuda")
+    for call in (lambda: tc.linear(x, w, out=y), lambda: tc.gated_ffn(x, w, w, w), lambda: tc.linear_backward(x, x, w),
+                 lambda: tc.linear_cross_entropy(h, x, target)):
+        with pytest.warns(UserWarning, match="records no autograd graph"):
+            out = call()
+        assert not any(t.requires_grad for t in (out if isinstance(out, tuple) else (out,)) if t is not None)
+        with warnings.catch_warnings(), torch.no_grad():
+            warnings.simplefilter("error")
+            call()
+    # turned into an error, it leaves the output alone
+    y.zero_()
+    with warnings.catch_warnings():
+        warnings.simplefilter("error")
+        with pytest.raises(UserWarning):
+            tc.linear(x, w, out=y)
+        tc.linear(x, w.detach())
+    assert torch.count_nonzero(y) == 0
