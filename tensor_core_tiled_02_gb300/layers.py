@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib
+import operator
 import threading
 
 import tensor_core_tiled_02_gb300 as _tc
@@ -61,10 +62,13 @@ def _on(stream, tensor):
     """The torch stream context of a stream the caller names (a stream or a handle)."""
     import torch
 
+    if not isinstance(tensor, torch.Tensor) or not tensor.is_cuda:
+        raise ValueError("every tensor must be a CUDA tensor")
     if not hasattr(stream, "cuda_stream"):
-        if not tensor.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        handle = int(stream)
+        try:
+            handle = operator.index(stream)
+        except TypeError:
+            raise ValueError(f"stream must be a stream or its handle, got {stream!r}") from None
         stream = (torch.cuda.ExternalStream(handle, device=tensor.device) if handle
                   else torch.cuda.default_stream(tensor.device))
     if stream.device != tensor.device:
@@ -85,14 +89,14 @@ def _call(name, stream, tensor, *args):
 
 
 def _act(act):
-    code = ACTS.get(act)
+    code = ACTS.get(act) if act is None or isinstance(act, str) else None
     if code is None:
         raise ValueError(f"act must be one of {sorted(k for k in ACTS if k)}, got {act!r}")
     return code
 
 
 def _reduction(reduction):
-    code = REDUCTIONS.get(reduction)
+    code = REDUCTIONS.get(reduction) if isinstance(reduction, str) else None
     if code is None:
         raise ValueError(f"reduction must be one of {sorted(REDUCTIONS)}, got {reduction!r}")
     return code
@@ -156,6 +160,8 @@ def linear_cross_entropy_backward(grad_loss, h, w, target, lse, ignore_index=-10
     if piece is None:
         import torch
 
+        if not isinstance(h, torch.Tensor) or h.dim() != 2:
+            raise ValueError("h must be a 2-D fp16 or bf16 tensor")
         copies = 2 if reduction == "none" and h.dtype == torch.float16 else 1
         piece = max(256, LOSS_PIECE_BYTES // (2 * copies * max(h.shape[0], 1)) // 256 * 256)
     return _call("linear_cross_entropy_backward", stream, h, grad_loss, h, w, target, lse, ignore_index,
@@ -169,6 +175,8 @@ def clip_grad_norm(grads, max_norm, out=None, eps=1e-6, stream=None):
     place, or into ``out`` (tensors of the same sizes and types).  Returns the norm
     before clipping: one fp32 value on the device, nothing waits for it.
     """
-    grads = list(grads)
-    return _call("clip_grad_norm", stream, grads[0] if grads else None, grads, max_norm,
-                 None if out is None else list(out), eps)
+    try:
+        grads, out = list(grads), None if out is None else list(out)
+    except TypeError:
+        raise ValueError("gradients and out must be lists of tensors") from None
+    return _call("clip_grad_norm", stream, grads[0] if grads else None, grads, max_norm, out, eps)

@@ -41,3 +41,19 @@ def side(**changes):
     dict(y=P[2], preact=P[2] + 240, ldy=256, ldp=256)], ids=str)
 def test_overlapping_column_ranges(lib, changes):
     assert side(**changes) in ((ALIGN,) if changes.get("y") == P[0] + 126 else (ALIAS,))
+
+
+def test_refusals_before_the_binding_sees_the_tensors():
+    """A stream to enter and a piece to choose are looked up on the tensors first: what is not a
+    tensor, has no rows or is no list of any is refused all the same."""
+    torch = pytest.importorskip("torch")
+    x, t = torch.zeros(8, 64, dtype=torch.float16), torch.zeros(8, dtype=torch.int64)
+    for call in (lambda: tc.linear([1.0], x, stream=3), lambda: tc.linear(None, x, stream=0), lambda: tc.linear(x, x, stream="no"),
+                 lambda: tc.clip_grad_norm([], 1.0, stream=3), lambda: tc.clip_grad_norm([None], 1.0, stream=0),
+                 lambda: tc.clip_grad_norm(None, 1.0), lambda: tc.clip_grad_norm([x], 1.0, out=3),
+                 lambda: tc.linear_cross_entropy_backward(x, None, x, t, x),
+                 lambda: tc.linear_cross_entropy_backward(x, torch.zeros((), dtype=torch.float16), x, t, x),
+                 lambda: tc.linear_cross_entropy_backward(x, x, x, t, x, piece=2.5),
+                 lambda: tc.linear(x, x, act=[]), lambda: tc.linear_cross_entropy(x, x, t, reduction=["mean"])):
+        with pytest.raises(ValueError):
+            call()
