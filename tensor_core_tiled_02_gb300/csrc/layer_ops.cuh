@@ -263,6 +263,12 @@ int run_product_pair(const Product& q, const PairPlan& g, const Ctx& c) {
 }
 
 constexpr int kSkinnyTwoSmem = 115712;  // two such CTAs fill an SM's 228 KiB
+// A CTA that pushes partials holds Tensor Memory while it waits for its cluster to start, as
+// the GEMM's clusters do.  Beside one of those that takes all 512 columns (and, with few
+// stages configured, no more than smem_request's half of an SM's shared memory) on another
+// stream, each could hold what the other's peer waits for: so no SM takes both.  (1 KiB a
+// CTA is the system's.  The other forms here give Tensor Memory back before they wait.)
+static_assert(kSkinnyTwoSmem + 1024 + (233472 / 2 + 1) + 1024 > 233472, "a pushing CTA beside a 512-column one");
 
 // How the kernel for few tokens runs a product: tokens a tile, split along K,
 // shared memory.
@@ -341,6 +347,7 @@ SkinnyPlan skinny_plan(const Product& q, int epi, int sms, const int* held, int 
     g.smem = g.slots * g.stage_bytes + g.recv_bytes + fixed;
     const int floor_smem = two ? 78848 : 118784;  // never three CTAs an SM, or two
     if (g.smem < floor_smem) g.smem = floor_smem;
+    if (g.push) g.smem = kSkinnyTwoSmem;  // above
     g.waves = ceil_div((long long)g.tiles * g.split, sms);
     g.k_steps = k_steps;
     return g;
