@@ -8,7 +8,12 @@
  * device pointers owned by the caller, asynchronous on `stream`, host-side
  * argument checks before any CUDA call, callable from several host threads):
  *   - Operands are fp16 or bf16 (one type per call), products are accumulated
- *     in fp32 and each output is rounded once, to nearest even.
+ *     in fp32 and each output is rounded once, to nearest even.  What one
+ *     product of a call hands the next is rounded to that type too: hidden,
+ *     dpre, dgate and dup, and d of the loss.  In fp16 they have its range: a
+ *     hidden above 65504 is infinite, also when nothing is kept, and of dpre,
+ *     dgate and dup nothing is left below 2^-25, so gradients want a loss scale
+ *     there.  (d is scaled by the call itself.)
  *   - A matrix is row-major with a row stride ("ld", in elements) of at least
  *     its width.  TMA wants a row stride that is a multiple of 8 and a base
  *     address that is a multiple of 16 bytes, else GEMM_ERR_ALIGN; widths and
@@ -185,7 +190,9 @@ int linear_cross_entropy_backward_workspace(const loss_grad_args *args, long lon
  *             fp32), aligned to their type; dst[i] may be src[i] (in place).
  *             Different tensors may not overlap (not checked)
  *   norm      one fp32 on the device, or NULL
- * An infinite norm scales by 0 and a NaN norm by NaN, as the formula says.
+ * An infinite norm scales by 0 and a NaN norm by NaN, as the formula says.  Squares
+ * are summed in fp32: a norm above 1e19 comes out infinite, entries below 1e-23 count
+ * as 0.
  */
 typedef struct {
     const void *const *src;

@@ -126,7 +126,8 @@ def gated_ffn(x, w_gate, w_up, w_down, act="silu", residual=None, save=False, ou
 
     x [tokens, dim], w_gate and w_up [dim, ffn], w_down [ffn, dim_out].  ``out`` may be
     the residual itself.  With ``save`` returns (y, gate, up, hidden): x @ w_gate,
-    x @ w_up and act(gate) * up, which ``gated_ffn_backward`` reads.
+    x @ w_up and act(gate) * up, which ``gated_ffn_backward`` reads.  The second product
+    takes hidden rounded to x's type: in fp16 above 65504 it is infinite, kept or not.
     """
     return _call("gated_ffn", stream, x, x, w_gate, w_up, w_down, _act(act), residual, bool(save), out)
 
@@ -155,6 +156,8 @@ def linear_cross_entropy_backward(grad_loss, h, w, target, lse, ignore_index=-10
     ``grad_loss`` is the loss's gradient, fp32 on the device: one value, or [tokens]
     for reduction "none".  The logits are computed again, ``piece`` words of the
     vocabulary at a time (a multiple of 256; by default what fits LOSS_PIECE_BYTES).
+    In fp16 with reduction "none" every row of dh keeps its own precision, however far the
+    rows' gradients lie apart, at twice the memory for a piece.
     h has to be finite in ignored rows too: their weight in dw is 0, not absent.
     """
     if piece is None:
@@ -173,7 +176,8 @@ def clip_grad_norm(grads, max_norm, out=None, eps=1e-6, stream=None):
 
     ``grads``: dense CUDA tensors, fp16, bf16 or fp32, of any shapes, types mixed.  In
     place, or into ``out`` (tensors of the same sizes and types).  Returns the norm
-    before clipping: one fp32 value on the device, nothing waits for it.
+    before clipping: one fp32 value on the device, nothing waits for it.  Squares are
+    summed in fp32: a norm above 1e19 comes out infinite and scales by 0.
     """
     try:
         grads, out = list(grads), None if out is None else list(out)
