@@ -12,7 +12,8 @@ Names follow the C ABI: ``gemm_f16`` (raw pointers), ``gemm_f16_plan``,
 out_dtype)`` of "Quickstart: GPU", section "Pipelining: a matmul kernel".
 The layer operators (``linear``, ``gated_ffn``, ``linear_cross_entropy``, their
 ``_backward`` calls and ``clip_grad_norm``; ``include/layer_ops.h``) are bound
-in ``layers.py``.
+in ``layers.py``; the norm between layers and microscaled operands (``rms_norm``,
+``mx_quantize``, ``mx_linear``; ``include/mx_ops.h``) in ``mx.py``.
 """
 from __future__ import annotations
 
@@ -43,7 +44,9 @@ EXPORTED = ["add_matrices_f32", "gemm_f16", "gemm_f16_acc", "gemm_f16_ws", "gemm
             "gated_ffn_forward", "gated_ffn_backward", "gated_ffn_backward_workspace",
             "linear_cross_entropy", "linear_cross_entropy_workspace",
             "linear_cross_entropy_backward", "linear_cross_entropy_backward_workspace",
-            "grad_clip", "grad_clip_workspace"]
+            "grad_clip", "grad_clip_workspace",
+            "rms_norm_forward", "rms_norm_backward", "rms_norm_backward_workspace", "mx_quantize", "mx_dequantize",
+            "mx_linear"]
 
 
 class GemmPlan(ctypes.Structure):
@@ -111,10 +114,12 @@ def load_library(path: str = LIB_PATH):
             lib.gemm_f16_device_status.restype = ci
             sp = ctypes.POINTER(ctypes.c_size_t)
             for name in ("linear_forward", "linear_backward", "gated_ffn_forward", "gated_ffn_backward",
-                         "linear_cross_entropy", "linear_cross_entropy_backward", "grad_clip"):
+                         "linear_cross_entropy", "linear_cross_entropy_backward", "grad_clip", "rms_norm_forward",
+                         "rms_norm_backward", "mx_quantize", "mx_dequantize", "mx_linear"):
                 getattr(lib, name).argtypes = [vp, vp]
                 getattr(lib, name).restype = ci
-            for name in ("linear_backward_workspace", "gated_ffn_backward_workspace", "linear_cross_entropy_workspace"):
+            for name in ("linear_backward_workspace", "gated_ffn_backward_workspace", "linear_cross_entropy_workspace",
+                         "rms_norm_backward_workspace"):
                 getattr(lib, name).argtypes = [vp, sp]
                 getattr(lib, name).restype = ci
             lib.linear_cross_entropy_backward_workspace.argtypes = [vp, ctypes.c_longlong, sp]
@@ -323,3 +328,5 @@ def matmul(a, b, out_dtype=None, out=None, stream=None, workspace=None):
 from .layers import (  # noqa: E402  (it uses the names above)
     clip_grad_norm, gated_ffn, gated_ffn_backward, linear, linear_backward, linear_cross_entropy,
     linear_cross_entropy_backward)
+from .mx import (  # noqa: E402
+    Mx, mx_dequantize, mx_linear, mx_quantize, rms_norm, rms_norm_backward, rms_norm_mx)

@@ -77,7 +77,7 @@ def build_binding(out: str | None = None) -> str:
 
 
 def binding_needs_build() -> bool:
-    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "layer_ops.h"), os.path.join(INCLUDE, "gemm_f16.h")]
+    deps = [BINDING_SOURCE, os.path.join(INCLUDE, "layer_ops.h"), os.path.join(INCLUDE, "mx_ops.h"), os.path.join(INCLUDE, "gemm_f16.h")]
     return not os.path.exists(BINDING) or any(os.path.getmtime(d) > os.path.getmtime(BINDING) for d in deps)
 
 

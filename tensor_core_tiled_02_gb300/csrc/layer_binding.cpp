@@ -1,6 +1,6 @@
 // The layer operators on torch tensors: argument checks, output memory and the
-// current stream, then one call of the C ABI (include/layer_ops.h).  layers.py
-// holds the signatures and the documentation; this is its native half, because
+// current stream, then one call of the C ABI (include/layer_ops.h, mx_ops.h).  layers.py
+// and mx.py hold the signatures and the documentation; this is their native half, because
 // a call for one token runs 4 to 10 us on the GPU while the same steps in Python
 // took 12 (and 0.5 a tensor for gradient clipping).  Arithmetic happens in
 // libtcgemm.so only.
@@ -21,7 +21,7 @@
 #include <string>
 #include <vector>
 
-#include "layer_ops.h"
+#include "mx_ops.h"
 
 namespace {
 
@@ -39,6 +39,12 @@ struct Abi {
     decltype(&linear_cross_entropy_backward_workspace) loss_grad_ws;
     decltype(&grad_clip) clip;
     decltype(&grad_clip_workspace) clip_ws;
+    decltype(&rms_norm_forward) norm;
+    decltype(&rms_norm_backward) norm_grad;
+    decltype(&rms_norm_backward_workspace) norm_grad_ws;
+    decltype(&mx_quantize) quantize;
+    decltype(&mx_dequantize) dequantize;
+    decltype(&mx_linear) mx_product;
 } abi;
 
 struct Refusal : std::runtime_error {
@@ -93,6 +99,8 @@ struct Call {
     explicit Call(const at::Tensor& t)
         : type(t.scalar_type()), device(t.device()), guard(t.device()),
           stream(c10::cuda::getCurrentCUDAStream(t.device().index()).stream()) {}
+    // outputs of a type of their own
+    Call(const at::Tensor& t, at::ScalarType out) : Call(t) { type = out; }
 
     void matrix(const at::Tensor& t, const char* name, int64_t rows, int64_t cols) const {
         if (t.scalar_type() != type) refuse(std::string(name) + " must be " + type_name(type));
@@ -551,6 +559,257 @@ PyObject* py_clip(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     });
 }
 
+// ---- the norm and microscaled operands ----------------------------------------------
+
+// A microscaled matrix [rows, cols]: data [rows, bytes] and scale, tiles of 512 bytes.
+struct Scaled {
+    at::Tensor data, scale;
+};
+
+int64_t blocks_of(int64_t cols) { return (cols + 31) / 32; }
+int64_t data_bytes(int64_t cols, int64_t format) { return blocks_of(cols) * (format == MX_E4M3 ? 32 : 16); }
+
+Scaled new_scaled(const Call& c, int64_t rows, int64_t cols, int64_t format) {
+    return {c.empty({rows, data_bytes(cols, format)}, at::kByte), c.empty({(rows + 127) / 128, (cols + 127) / 128, 32, 4, 4}, at::kByte)};
+}
+
+// One the caller hands in: sizes that fit, rows without gaps inside.  Returns its row stride.
+int64_t check_scaled(const Call& c, const at::Tensor& data, const at::Tensor& scale, const char* name, int64_t rows, int64_t cols,
+                     int64_t format) {
+    const int64_t width = data_bytes(cols, format);
+    if (data.scalar_type() != at::kByte || data.dim() != 2 || data.size(0) != rows || data.size(1) != width)
+        refuse(std::string(name) + "'s data must be uint8 [" + std::to_string(rows) + ", " + std::to_string(width) + "]");
+    if (data.size(1) > 1 && data.stride(1) != 1) refuse(std::string(name) + "'s rows must be contiguous");
+    if (scale.scalar_type() != at::kByte || !scale.is_contiguous() || scale.numel() != (rows + 127) / 128 * ((cols + 127) / 128) * 512)
+        refuse(std::string(name) + "'s scale must be contiguous uint8 [" + std::to_string((rows + 127) / 128) + ", " +
+               std::to_string((cols + 127) / 128) + ", 32, 4, 4]");
+    c.place(data, name);
+    c.place(scale, name);
+    return rows > 1 ? data.stride(0) : (width + 15) / 16 * 16;
+}
+
+int64_t checked_format(PyObject* o) {
+    const int64_t f = integer(o);
+    if (f != MX_E4M3 && f != MX_E2M1) refuse("format must be \"e4m3\" or \"e2m1\"");
+    return f;
+}
+
+int64_t checked_cols(PyObject* o) {
+    const int64_t n = integer(o);
+    if (n < 0 || n > (1ll << 40)) refuse("cols must be a size");
+    return n;
+}
+
+at::ScalarType type_of(PyObject* o) { return integer(o) == LAYER_BF16 ? at::kBFloat16 : at::kHalf; }
+
+// (x, weight, residual, eps, format or None, save, out, h_out) -> (y, h or None, rstd or None),
+// or with a format (data, scale, h or None, rstd or None)
+PyObject* py_norm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+    return guarded(v, nargs, 8, [&]() -> PyObject* {
+        const at::Tensor& x = Call::checked(tensor(v[0], "x"), "x");
+        const int64_t tokens = x.size(0), dim = x.size(1);
+        if (dim < 1) refuse("x must have columns");
+        const Call c(Call::on_cuda(x, "x"));
+        rms_norm_args a{};
+        a.ldx = stride_of(x, "x");
+        const at::Tensor& weight = tensor(v[1], "weight");
+        c.vector(weight, "weight", dim, c.type);
+        const bool scaled = v[4] != Py_None;
+        at::Tensor y, h, rstd;
+        Scaled m;
+        if (v[2] != Py_None) {
+            const at::Tensor& r = tensor(v[2], "residual");
+            c.matrix(r, "residual", tokens, dim);
+            a.ldr = stride_of(r, "residual");
+            a.residual = r.data_ptr();
+            if (v[7] != Py_None) {
+                h = tensor(v[7], "h_out");
+                c.matrix(h, "h_out", tokens, dim);
+                a.ldh = stride_of(h, "h_out");
+            } else {
+                h = c.matrix(tokens, dim);
+                a.ldh = pitch(dim);
+            }
+        } else if (v[7] != Py_None) {
+            refuse("h_out is x itself where there is no residual");
+        }
+        if (scaled) {
+            a.format = checked_format(v[4]);
+            m = new_scaled(c, tokens, dim, a.format);
+            a.data = m.data.data_ptr();
+            a.scale = m.scale.data_ptr();
+            a.ldd = data_bytes(dim, a.format);
+        } else if (v[6] != Py_None) {
+            y = tensor(v[6], "out");
+            c.matrix(y, "out", tokens, dim);
+            a.ldy = stride_of(y, "out");
+        } else {
+            y = c.matrix(tokens, dim);
+            a.ldy = pitch(dim);
+        }
+        if (v[5] == Py_True) rstd = c.empty({tokens}, at::kFloat);
+        a.x = x.data_ptr();
+        a.weight = weight.data_ptr();
+        a.h = ptr(h);
+        a.y = ptr(y);
+        a.rstd = static_cast<float*>(ptr(rstd));
+        a.tokens = tokens;
+        a.dim = dim;
+        a.dtype = type_code(c.type);
+        a.eps = real(v[3]);
+        const int rc = abi.norm(&a, c.stream);
+        if (rc != 0) return PyLong_FromLong(rc);
+        if (v[6] != Py_None) wrote(y);
+        if (v[7] != Py_None) wrote(h);
+        return scaled ? wrap_all({m.data, m.scale, h, rstd}) : wrap_all({y, h, rstd});
+    });
+}
+
+// (dy, h, weight, rstd, dh, out) -> (dx, dweight)
+PyObject* py_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+    return guarded(v, nargs, 6, [&]() -> PyObject* {
+        const at::Tensor& h = Call::checked(tensor(v[1], "h"), "h");
+        const int64_t tokens = h.size(0), dim = h.size(1);
+        if (dim < 1) refuse("h must have columns");
+        const Call c(h);
+        rms_norm_grad_args a{};
+        a.ldh = stride_of(h, "h");
+        const at::Tensor &dy = tensor(v[0], "dy"), &weight = tensor(v[2], "weight"), &rstd = tensor(v[3], "rstd");
+        c.matrix(dy, "dy", tokens, dim);
+        a.lddy = stride_of(dy, "dy");
+        c.vector(weight, "weight", dim, c.type);
+        c.vector(rstd, "rstd (fp32)", tokens, at::kFloat);
+        if (v[4] != Py_None) {
+            const at::Tensor& dh = tensor(v[4], "dh");
+            c.matrix(dh, "dh", tokens, dim);
+            a.lddh = stride_of(dh, "dh");
+            a.dh = dh.data_ptr();
+        }
+        at::Tensor dx;
+        if (v[5] != Py_None) {
+            dx = tensor(v[5], "out");
+            c.matrix(dx, "out", tokens, dim);
+            a.lddx = stride_of(dx, "out");
+        } else {
+            dx = c.matrix(tokens, dim);
+            a.lddx = pitch(dim);
+        }
+        const at::Tensor dweight = c.empty({dim}, c.type);
+        a.dy = dy.data_ptr();
+        a.h = h.data_ptr();
+        a.weight = weight.data_ptr();
+        a.rstd = static_cast<const float*>(rstd.data_ptr());
+        a.dx = dx.data_ptr();
+        a.dweight = dweight.data_ptr();
+        a.tokens = tokens;
+        a.dim = dim;
+        a.dtype = type_code(c.type);
+        size_t bytes = 0;
+        int rc = abi.norm_grad_ws(&a, &bytes);
+        if (rc != 0) return PyLong_FromLong(rc);
+        const at::Tensor ws = c.workspace(bytes);
+        a.workspace = ptr(ws);
+        a.workspace_bytes = (long long)bytes;
+        rc = abi.norm_grad(&a, c.stream);
+        if (rc != 0) return PyLong_FromLong(rc);
+        if (v[5] != Py_None) wrote(dx);
+        return wrap_all({dx, dweight});
+    });
+}
+
+// (x, format, transpose) -> (data, scale)
+PyObject* py_quantize(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+    return guarded(v, nargs, 3, [&]() -> PyObject* {
+        const at::Tensor& x = Call::on_cuda(Call::checked(tensor(v[0], "x"), "x"), "x");
+        const Call c(x);
+        mx_quantize_args a{};
+        a.rows = x.size(0);
+        a.cols = x.size(1);
+        a.format = checked_format(v[1]);
+        a.transpose = v[2] == Py_True;
+        const int64_t rows = a.transpose ? a.cols : a.rows, cols = a.transpose ? a.rows : a.cols;
+        a.ldx = stride_of(x, "x");
+        const Scaled m = new_scaled(c, rows, cols, a.format);
+        a.x = x.data_ptr();
+        a.data = m.data.data_ptr();
+        a.scale = m.scale.data_ptr();
+        a.ldd = data_bytes(cols, a.format);
+        a.dtype = type_code(c.type);
+        const int rc = abi.quantize(&a, c.stream);
+        if (rc != 0) return PyLong_FromLong(rc);
+        return wrap_all({m.data, m.scale});
+    });
+}
+
+// (data, scale, cols, format, dtype) -> x
+PyObject* py_dequantize(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+    return guarded(v, nargs, 5, [&]() -> PyObject* {
+        const at::Tensor &data = Call::on_cuda(tensor(v[0], "data"), "data"), &scale = tensor(v[1], "scale");
+        const Call c(data, type_of(v[4]));
+        mx_dequantize_args a{};
+        a.rows = data.dim() == 2 ? data.size(0) : 0;
+        a.cols = checked_cols(v[2]);
+        a.format = checked_format(v[3]);
+        a.ldd = check_scaled(c, data, scale, "a", a.rows, a.cols, a.format);
+        const at::Tensor x = c.matrix(a.rows, a.cols);
+        a.data = data.data_ptr();
+        a.scale = scale.data_ptr();
+        a.x = x.data_ptr();
+        a.ldx = pitch(a.cols);
+        a.dtype = type_code(c.type);
+        const int rc = abi.dequantize(&a, c.stream);
+        if (rc != 0) return PyLong_FromLong(rc);
+        return wrap(x);
+    });
+}
+
+// (x data, x scale, w data, w scale, k, format, bias, act, residual, dtype, out) -> y
+PyObject* py_mx_linear(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
+    return guarded(v, nargs, 11, [&]() -> PyObject* {
+        const at::Tensor &x = Call::on_cuda(tensor(v[0], "x"), "x"), &xs = tensor(v[1], "x"), &w = tensor(v[2], "w"), &ws = tensor(v[3], "w");
+        const Call c(x, type_of(v[9]));
+        mx_linear_args a{};
+        a.k = checked_cols(v[4]);
+        a.format = checked_format(v[5]);
+        if (a.k < 1 || w.dim() != 2 || w.size(0) < 1) refuse("x and w must have columns, and w rows");
+        a.tokens = x.dim() == 2 ? x.size(0) : 0;
+        a.n = w.size(0);
+        a.ldx = check_scaled(c, x, xs, "x", a.tokens, a.k, a.format);
+        a.ldw = check_scaled(c, w, ws, "w", a.n, a.k, a.format);
+        if (v[6] != Py_None) c.vector(tensor(v[6], "bias"), "bias", a.n, c.type);
+        if (v[8] != Py_None) {
+            const at::Tensor& r = tensor(v[8], "residual");
+            c.matrix(r, "residual", a.tokens, a.n);
+            a.ldr = stride_of(r, "residual");
+        }
+        at::Tensor y;
+        if (v[10] != Py_None) {
+            y = tensor(v[10], "out");
+            c.matrix(y, "out", a.tokens, a.n);
+            a.ldy = stride_of(y, "out");
+        } else {
+            y = c.matrix(a.tokens, a.n);
+            a.ldy = pitch(a.n);
+        }
+        a.x = x.data_ptr();
+        a.x_scale = xs.data_ptr();
+        a.w = w.data_ptr();
+        a.w_scale = ws.data_ptr();
+        a.bias = cptr(v[6], "bias");
+        a.residual = cptr(v[8], "residual");
+        a.y = y.data_ptr();
+        a.dtype = type_code(c.type);
+        a.act = integer(v[7]);
+        const int rc = abi.mx_product(&a, c.stream);
+        if (rc != 0) return PyLong_FromLong(rc);
+        if (v[10] != Py_None) {
+            wrote(y);
+            return Py_NewRef(v[10]);
+        }
+        return wrap(y);
+    });
+}
+
 // (address, ...) of the entry points, in Abi's order
 PyObject* py_bind(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     constexpr Py_ssize_t kEntries = sizeof(Abi) / sizeof(void*);
@@ -579,6 +838,11 @@ PyMethodDef methods[] = {ENTRY("bind", py_bind),
                          ENTRY("linear_cross_entropy", py_loss),
                          ENTRY("linear_cross_entropy_backward", py_loss_backward),
                          ENTRY("clip_grad_norm", py_clip),
+                         ENTRY("rms_norm", py_norm),
+                         ENTRY("rms_norm_backward", py_norm_backward),
+                         ENTRY("mx_quantize", py_quantize),
+                         ENTRY("mx_dequantize", py_dequantize),
+                         ENTRY("mx_linear", py_mx_linear),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_layers", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -1,0 +1,331 @@
+// Host side of the norm and of the microscaled operands (include/mx_ops.h): argument
+// checks, tensor maps, workspaces and launches.  Part of the library's one translation
+// unit (tcgemm.cu), behind layer_ops.cuh, whose checks and launches it shares.
+#pragma once
+
+#include "mx_ops.h"
+
+#include "mx_linear_kernel.cuh"
+#include "mx_quant_kernel.cuh"
+#include "norm_kernel.cuh"
+
+namespace {
+
+// A microscaled matrix as the caller describes it.
+struct Mx {
+    const void *data, *scale;
+    long long rows, cols, ld;
+    int fmt;
+};
+
+long long mx_blocks(const Mx& m) { return ceil_div(m.cols, kMxBlock); }
+long long mx_width(const Mx& m) { return mx_blocks(m) * mx_block_bytes(m.fmt); }
+Mat mx_data(const Mx& m) { return Mat{m.data, m.rows, mx_width(m), m.ld, 1}; }
+uint64_t mx_scale_bytes(const Mx& m) { return (uint64_t)ceil_div(m.rows, 128) * ceil_div(m.cols, 128) * 512; }
+Span mx_scale_span(const Mx& m) { return span_of(m.scale, mx_scale_bytes(m)); }
+
+int check_mx(const Mx& m) {
+    if (m.rows == 0 || m.cols == 0) return GEMM_OK;
+    if (!m.data || !m.scale) return GEMM_ERR_NULL;
+    if ((uintptr_t)m.scale & 15) return GEMM_ERR_ALIGN;
+    return check_mat(mx_data(m));
+}
+
+int check_format(long long format) { return format == MX_E4M3 || format == MX_E2M1 ? GEMM_OK : GEMM_ERR_CONFIG; }
+
+// dtype and format as compile-time tags.
+template <typename F>
+int with_types(long long dtype, long long format, F&& f) {
+    using std::integral_constant;
+    if (dtype == LAYER_BF16)
+        return format == MX_E2M1 ? f(integral_constant<int, kBF16>{}, integral_constant<int, kE2M1>{})
+                                 : f(integral_constant<int, kBF16>{}, integral_constant<int, kE4M3>{});
+    return format == MX_E2M1 ? f(integral_constant<int, kF16>{}, integral_constant<int, kE2M1>{})
+                             : f(integral_constant<int, kF16>{}, integral_constant<int, kE4M3>{});
+}
+
+// ---- norm ---------------------------------------------------------------------------------
+
+template <int DT, int V, int OUT>
+int run_norm_rows(const NormParams& p, int threads, const Ctx& c) {
+    const int rows = p.group == 32 ? threads / 32 : 1;
+    return launch_pdl(rms_norm_kernel<DT, V, OUT>, dim3(ceil_div(p.tokens, rows)), threads, 0, 1, c.stream, p);
+}
+
+// Threads that share a row, and vectors of eight columns each has.
+template <int DT, int OUT>
+int run_norm(NormParams p, const Ctx& c) {
+    const int vectors = ceil_div(p.dim, 8);
+    if (vectors > 8 * 1024)
+        return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
+    int v = 1;
+    while (v < 8 && (p.tokens > 2 * c.dev->sms ? vectors > 128 * v : vectors > 1024 * v)) v *= 2;
+    p.group = ceil_div(ceil_div(vectors, v), 32) * 32;
+    const int threads = p.group == 32 ? 128 : p.group;
+    switch (v) {
+        case 1: return run_norm_rows<DT, 1, OUT>(p, threads, c);
+        case 2: return run_norm_rows<DT, 2, OUT>(p, threads, c);
+        case 4: return run_norm_rows<DT, 4, OUT>(p, threads, c);
+        default: return run_norm_rows<DT, 8, OUT>(p, threads, c);
+    }
+}
+
+struct NormGradPlan {
+    int threads, v, blocks;
+    bool long_rows;
+    size_t bytes;
+};
+
+constexpr int kNormGradRows = 4;
+
+NormGradPlan norm_grad_plan(const rms_norm_grad_args& a) {
+    NormGradPlan g{};
+    const int vectors = ceil_div(a.dim, 8);
+    g.v = vectors > 512 ? 2 : 1;
+    g.threads = ceil_div(ceil_div(vectors, g.v), 32) * 32;
+    g.long_rows = vectors > 2048;
+    const long long most = ceil_div(a.tokens, kNormGradRows);
+    g.blocks = most < kNormPartials ? (int)most : kNormPartials;
+    g.bytes = a.dweight ? align256((size_t)g.blocks * a.dim * 4) : 0;
+    return g;
+}
+
+template <int DT>
+int run_norm_grad(const NormGradParams& p, const NormGradPlan& g, void* dweight, const Ctx& c) {
+    int rc = GEMM_OK;
+    if (g.long_rows) {
+        // the column sums first: dx may be written over dy
+        if (dweight)
+            rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, 0, 1, c.stream, p);
+        if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
+    } else if (g.v == 1) {
+        rc = launch_pdl(rms_norm_grad_kernel<DT, 1, kNormGradRows>, dim3(g.blocks), g.threads, 0, 1, c.stream, p);
+    } else {
+        rc = launch_pdl(rms_norm_grad_kernel<DT, 2, kNormGradRows>, dim3(g.blocks), g.threads, 0, 1, c.stream, p);
+    }
+    if (rc == GEMM_OK && dweight)
+        rc = launch_pdl(rms_norm_weight_sum_kernel<DT>, dim3(ceil_div(p.dim, 32)), 1024, 0, 1, c.stream, (const float*)p.partial,
+                        dweight, g.blocks, p.dim);
+    return rc;
+}
+
+int check_dtype16(long long dtype) { return check_dtype_act(dtype, LAYER_ACT_NONE); }
+
+}  // namespace
+
+extern "C" {
+
+int rms_norm_forward(const rms_norm_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const rms_norm_args& a = *args;
+    int rc = check_dtype16(a.dtype);
+    if (rc != GEMM_OK) return rc;
+    if ((a.data || a.scale) && (rc = check_format(a.format)) != GEMM_OK) return rc;
+    if (!(a.eps >= 0.0)) return GEMM_ERR_CONFIG;
+    if (!dims_ok({a.dim}, a.tokens)) return GEMM_ERR_DIM;
+    if (a.tokens == 0) return GEMM_OK;
+    const Mat x = mat16(a.x, a.tokens, a.dim, a.ldx), r = mat16(a.residual, a.tokens, a.dim, a.ldr);
+    const Mat h = mat16(a.h, a.tokens, a.dim, a.ldh), y = mat16(a.y, a.tokens, a.dim, a.ldy);
+    const Mx m{a.data, a.scale, a.tokens, a.dim, a.ldd, (int)a.format};
+    if (!a.residual != !a.h || (!a.y && !a.data) || !a.data != !a.scale || !a.weight) return GEMM_ERR_NULL;
+    if ((rc = check_mat(x)) != GEMM_OK) return rc;
+    if (a.residual && (rc = check_all({r, h})) != GEMM_OK) return rc;
+    if (a.y && (rc = check_mat(y)) != GEMM_OK) return rc;
+    if (a.data && (rc = check_mx(m)) != GEMM_OK) return rc;
+    if ((uintptr_t)a.weight & 15 || (uintptr_t)a.rstd & 3) return GEMM_ERR_ALIGN;
+    const bool over_x = a.h == a.x && a.ldh == a.ldx, over_r = a.h == a.residual && a.ldh == a.ldr;
+    const Span none{0, 0};
+    const Span xs = span_of(x), rs = span_of(r), hs = span_of(h), ws = span_of(a.weight, (uint64_t)a.dim * 2);
+    const Span others[] = {span_of(y), a.data ? span_of(mx_data(m)) : none, a.data ? mx_scale_span(m) : none,
+                           span_of(a.rstd, (uint64_t)a.tokens * 4)};
+    const Span all_read[] = {xs, rs, hs, ws};
+    if (overlaps(others, 4, all_read, 4)) return GEMM_ERR_ALIAS;
+    const Span h_read[] = {over_x ? none : xs, over_r ? none : rs, ws};
+    if (overlaps(&hs, 1, h_read, 3)) return GEMM_ERR_ALIAS;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    NormParams p{};
+    p.x = a.x;
+    p.residual = a.residual;
+    p.weight = a.weight;
+    p.h = a.h;
+    p.y = a.y;
+    p.data = static_cast<uint8_t*>(a.data);
+    p.scale = static_cast<uint32_t*>(a.scale);
+    p.rstd = a.rstd;
+    p.ldx = a.ldx;
+    p.ldr = a.ldr;
+    p.ldh = a.ldh;
+    p.ldy = a.ldy;
+    p.ldd = a.ldd;
+    p.tokens = (int)a.tokens;
+    p.dim = (int)a.dim;
+    p.eps = (float)a.eps;
+    if (!a.data) return a.dtype == LAYER_BF16 ? run_norm<kBF16, kNormRow>(p, c) : run_norm<kF16, kNormRow>(p, c);
+    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
+        return run_norm<decltype(dt)::value, decltype(fmt)::value == kE4M3 ? kNormE4M3 : kNormE2M1>(p, c);
+    });
+}
+
+int rms_norm_backward_workspace(const rms_norm_grad_args* args, size_t* bytes) {
+    if (!args || !bytes) return GEMM_ERR_NULL;
+    const int rc = check_dtype16(args->dtype);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({args->dim}, args->tokens)) return GEMM_ERR_DIM;
+    *bytes = norm_grad_plan(*args).bytes;
+    return GEMM_OK;
+}
+
+int rms_norm_backward(const rms_norm_grad_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const rms_norm_grad_args& a = *args;
+    int rc = check_dtype16(a.dtype);
+    if (rc != GEMM_OK) return rc;
+    if (!dims_ok({a.dim}, a.tokens)) return GEMM_ERR_DIM;
+    const Mat dy = mat16(a.dy, a.tokens, a.dim, a.lddy), h = mat16(a.h, a.tokens, a.dim, a.ldh);
+    const Mat dh = mat16(a.dh, a.tokens, a.dim, a.lddh), dx = mat16(a.dx, a.tokens, a.dim, a.lddx);
+    if (!a.weight || (a.tokens > 0 && !a.rstd)) return GEMM_ERR_NULL;
+    if ((rc = check_all({dy, h})) != GEMM_OK) return rc;
+    if (a.dh && (rc = check_mat(dh)) != GEMM_OK) return rc;
+    if (a.dx && (rc = check_mat(dx)) != GEMM_OK) return rc;
+    if (((uintptr_t)a.weight & 15) || ((uintptr_t)a.rstd & 3) || ((uintptr_t)a.dweight & 1)) return GEMM_ERR_ALIGN;
+    const NormGradPlan g = norm_grad_plan(a);
+    if (a.tokens > 0 && (rc = check_workspace(a.workspace, a.workspace_bytes, g.bytes)) != GEMM_OK) return rc;
+    const bool over_dy = a.dx == a.dy && a.lddx == a.lddy, over_dh = a.dx == a.dh && a.lddx == a.lddh;
+    const Span none{0, 0};
+    const Span dys = span_of(dy), hs = span_of(h), dhs = span_of(dh), dxs = span_of(dx);
+    const Span ws = span_of(a.weight, (uint64_t)a.dim * 2), ss = span_of(a.rstd, (uint64_t)a.tokens * 4);
+    const Span others[] = {span_of(a.dweight, (uint64_t)a.dim * 2), span_of(g.bytes ? a.workspace : nullptr, g.bytes)};
+    const Span all_read[] = {dys, hs, dhs, dxs, ws, ss};
+    if (overlaps(others, 2, all_read, 6)) return GEMM_ERR_ALIAS;
+    const Span dx_read[] = {over_dy ? none : dys, hs, over_dh ? none : dhs, ws, ss};
+    if (overlaps(&dxs, 1, dx_read, 5)) return GEMM_ERR_ALIAS;
+    if (!a.dx && !a.dweight) return GEMM_OK;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    if (a.tokens == 0) return a.dweight ? zero_mat(Mat{a.dweight, 1, a.dim, a.dim, 2}, c) : GEMM_OK;
+    NormGradParams p{};
+    p.dy = a.dy;
+    p.h = a.h;
+    p.weight = a.weight;
+    p.dh = a.dh;
+    p.rstd = a.rstd;
+    p.dx = a.dx;
+    p.partial = a.dweight ? static_cast<float*>(a.workspace) : nullptr;
+    p.lddy = a.lddy;
+    p.ldh = a.ldh;
+    p.lddh = a.lddh;
+    p.lddx = a.lddx;
+    p.tokens = (int)a.tokens;
+    p.dim = (int)a.dim;
+    return a.dtype == LAYER_BF16 ? run_norm_grad<kBF16>(p, g, a.dweight, c) : run_norm_grad<kF16>(p, g, a.dweight, c);
+}
+
+int mx_quantize(const mx_quantize_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const mx_quantize_args& a = *args;
+    int rc = check_dtype16(a.dtype);
+    if (rc != GEMM_OK || (rc = check_format(a.format)) != GEMM_OK) return rc;
+    if (a.transpose != 0 && a.transpose != 1) return GEMM_ERR_CONFIG;
+    // either of the two may be the number of tokens
+    if (!dims_ok({}, a.rows) || !dims_ok({}, a.cols)) return GEMM_ERR_DIM;
+    if (a.rows == 0 || a.cols == 0) return GEMM_OK;
+    const Mat x = mat16(a.x, a.rows, a.cols, a.ldx);
+    const Mx m{a.data, a.scale, a.transpose ? a.cols : a.rows, a.transpose ? a.rows : a.cols, a.ldd, (int)a.format};
+    if ((rc = check_mat(x)) != GEMM_OK || (rc = check_mx(m)) != GEMM_OK) return rc;
+    const Span wr[] = {span_of(mx_data(m)), mx_scale_span(m)}, rd[] = {span_of(x)};
+    if (overlaps(wr, 2, rd, 1)) return GEMM_ERR_ALIAS;
+    MxQuantParams p{};
+    p.x = a.x;
+    p.data = static_cast<uint8_t*>(a.data);
+    p.scale = static_cast<uint32_t*>(a.scale);
+    p.ldx = a.ldx;
+    p.ldd = a.ldd;
+    p.rows = (int)a.rows;
+    p.cols = (int)a.cols;
+    p.groups = ceil_div(a.cols, 256);
+    const long long blocks = (long long)p.groups * ceil_div(a.rows, a.transpose ? 128 : 8 * kMxQuantRows);
+    if (blocks > INT_MAX) return GEMM_ERR_DIM;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
+        constexpr int DT = decltype(dt)::value, FMT = decltype(fmt)::value;
+        return a.transpose ? launch_pdl(mx_quantize_columns_kernel<DT, FMT>, dim3((unsigned)blocks), 128, 0, 1, c.stream, p)
+                           : launch_pdl(mx_quantize_kernel<DT, FMT>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p);
+    });
+}
+
+int mx_dequantize(const mx_dequantize_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const mx_dequantize_args& a = *args;
+    int rc = check_dtype16(a.dtype);
+    if (rc != GEMM_OK || (rc = check_format(a.format)) != GEMM_OK) return rc;
+    if (!dims_ok({}, a.rows) || !dims_ok({}, a.cols)) return GEMM_ERR_DIM;
+    if (a.rows == 0 || a.cols == 0) return GEMM_OK;
+    const Mat x = mat16(a.x, a.rows, a.cols, a.ldx);
+    const Mx m{a.data, a.scale, a.rows, a.cols, a.ldd, (int)a.format};
+    if ((rc = check_mx(m)) != GEMM_OK || (rc = check_mat(x)) != GEMM_OK) return rc;
+    const Span wr[] = {span_of(x)}, rd[] = {span_of(mx_data(m)), mx_scale_span(m)};
+    if (overlaps(wr, 1, rd, 2)) return GEMM_ERR_ALIAS;
+    MxValuesParams p{};
+    p.data = static_cast<const uint8_t*>(a.data);
+    p.scale = static_cast<const uint8_t*>(a.scale);
+    p.x = a.x;
+    p.ldd = a.ldd;
+    p.ldx = a.ldx;
+    p.rows = (int)a.rows;
+    p.cols = (int)a.cols;
+    p.groups = ceil_div(a.cols, 256);
+    const long long blocks = (long long)p.groups * ceil_div(a.rows, 8 * kMxQuantRows);
+    if (blocks > INT_MAX) return GEMM_ERR_DIM;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
+        return launch_pdl(mx_dequantize_kernel<decltype(dt)::value, decltype(fmt)::value>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p);
+    });
+}
+
+int mx_linear(const mx_linear_args* args, gemm_stream_t stream) {
+    if (!args) return GEMM_ERR_NULL;
+    const mx_linear_args& a = *args;
+    int rc = check_dtype_act(a.dtype, a.act);
+    if (rc != GEMM_OK || (rc = check_format(a.format)) != GEMM_OK) return rc;
+    if (!dims_ok({a.k, a.n}, a.tokens)) return GEMM_ERR_DIM;
+    if (a.tokens == 0) return GEMM_OK;
+    const Mx x{a.x, a.x_scale, a.tokens, a.k, a.ldx, (int)a.format}, w{a.w, a.w_scale, a.n, a.k, a.ldw, (int)a.format};
+    const Mat y = mat16(a.y, a.tokens, a.n, a.ldy), r = mat16(a.residual, a.tokens, a.n, a.ldr);
+    if ((rc = check_mx(x)) != GEMM_OK || (rc = check_mx(w)) != GEMM_OK || (rc = check_mat(y)) != GEMM_OK) return rc;
+    if (r.p && (rc = check_mat(r)) != GEMM_OK) return rc;
+    if ((uintptr_t)a.bias & 1) return GEMM_ERR_ALIGN;
+    const bool in_place = r.p == y.p && a.ldr == a.ldy;
+    const Span wr[] = {span_of(y)};
+    const Span rd[] = {span_of(mx_data(x)), mx_scale_span(x), span_of(mx_data(w)), mx_scale_span(w),
+                       span_of(a.bias, (uint64_t)a.n * 2), in_place ? Span{0, 0} : span_of(r)};
+    if (overlaps(wr, 1, rd, 6)) return GEMM_ERR_ALIAS;
+    Ctx c;
+    if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
+    MxLinearParams p{};
+    p.x = static_cast<const uint8_t*>(a.x);
+    p.x_scale = static_cast<const uint8_t*>(a.x_scale);
+    p.w = static_cast<const uint8_t*>(a.w);
+    p.w_scale = static_cast<const uint8_t*>(a.w_scale);
+    p.bias = a.bias;
+    p.residual = a.residual;
+    p.y = a.y;
+    p.ldx = a.ldx;
+    p.ldw = a.ldw;
+    p.ldr = a.ldr;
+    p.ldy = a.ldy;
+    p.tokens = (int)a.tokens;
+    p.n = (int)a.n;
+    p.blocks = ceil_div(a.k, kMxBlock);
+    p.act = (int)a.act;
+    const long long blocks = (a.tokens * a.n + 255) / 256;
+    if (blocks > INT_MAX) return GEMM_ERR_DIM;
+    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
+        return launch_pdl(mx_linear_simple_kernel<decltype(dt)::value, decltype(fmt)::value>, dim3((unsigned)blocks), 256, 0, 1,
+                          c.stream, p);
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,349 @@
+// The root-mean-square norm with the residual's addition, its output in 16 bits or
+// in microscaled blocks, and its gradients.
+//
+//   h = x + residual,  r = 1 / sqrt(mean h^2 + eps),  y = h r w
+//   dx = r (dy w) - h r^3 mean(dy w h) + dh,  dw = sum over rows of dy h r
+//
+// Bound by HBM: every matrix is read or written once.  A row's values stay in the
+// registers of the threads that share it, eight neighbouring columns (16 bytes) to
+// a load, between the sum over the row and its use; rows beyond 65536 columns
+// forward and 16384 back are read twice instead.  All sums are fp32 and taken in a
+// fixed order: the same inputs give the same bits.
+#pragma once
+
+#include "mx_common.cuh"
+
+namespace tcgemm {
+
+enum NormOut { kNormRow = 0, kNormE4M3 = 1, kNormE2M1 = 2 };
+
+struct NormParams {
+    const void *x, *residual, *weight;
+    void *h, *y;
+    uint8_t* data;
+    uint32_t* scale;
+    float* rstd;
+    long long ldx, ldr, ldh, ldy, ldd;
+    int tokens, dim;
+    int group;       // threads that share a row: 32 or all of a block's
+    float eps;
+};
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+    return v;
+}
+
+__device__ __forceinline__ float norm_rstd(float squares, int dim, float eps) {
+    return __frsqrt_rn(__fdiv_rn(squares, (float)dim) + eps);
+}
+
+// Eight columns of y: scaled, and stored in each form that is wanted.
+template <int DT, int OUT>
+__device__ __forceinline__ void norm_store(const NormParams& p, int row, int col, uint4 hv, float rstd) {
+    float h[8], w[8], f[8];
+    unpack8<DT>(hv, h);
+    unpack8<DT>(col < p.dim ? load8<DT>(p.weight, col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u), w);
+    // h w is exact in fp32 (two 16-bit significands), so y is rounded once before its last rounding
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = h[i] * w[i] * rstd;
+    if (p.y != nullptr && col < p.dim) store8(p.y, row * p.ldy + col, col, p.dim, pack8<DT>(f));
+    if constexpr (OUT != kNormRow) {
+        constexpr int kFmt = OUT == kNormE4M3 ? kE4M3 : kE2M1;
+        if (col + 8 > p.dim) {  // behind the row's end h and w are 0, but rstd may be infinite
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i >= p.dim) f[i] = 0.0f;
+        }
+        const int k_tiles = (p.dim + 127) >> 7;
+        uint32_t* word = p.scale + (mx_scale_word(row, col >> 7, k_tiles) >> 2);
+        uint8_t* data = p.data + row * p.ldd + (kFmt == kE4M3 ? col : col >> 1);
+        mx_store8<kFmt>(f, data, col < ((p.dim + 31) & ~31), word, (col >> 7) < k_tiles);
+    }
+}
+
+// V vectors of eight columns a thread: thread t of a row's group has columns 8 (t + j group).
+template <int DT, int V, int OUT>
+__global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
+    __shared__ float sums[32];
+    const int lane = threadIdx.x & 31;
+    const bool alone = p.group == 32;  // a warp a row
+    const int t = alone ? lane : (int)threadIdx.x;
+    const int row = alone ? (int)(blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) : (int)blockIdx.x;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    if (row >= p.tokens) return;  // whole warps
+    uint4 h[V], r[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int col = (t + j * p.group) * 8;
+        h[j] = col < p.dim ? load8<DT>(p.x, row * p.ldx + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+        if (p.residual != nullptr)
+            r[j] = col < p.dim ? load8<DT>(p.residual, row * p.ldr + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float squares = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int col = (t + j * p.group) * 8;
+        float a[8];
+        unpack8<DT>(h[j], a);
+        if (p.residual != nullptr) {
+            float b[8];
+            unpack8<DT>(r[j], b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] += b[i];
+            h[j] = pack8<DT>(a);
+            unpack8<DT>(h[j], a);  // as it is stored
+            if (col < p.dim) store8(p.h, row * p.ldh + col, col, p.dim, h[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) squares = fmaf(a[i], a[i], squares);
+    }
+    squares = warp_sum(squares);
+    if (!alone) {
+        if (lane == 0) sums[threadIdx.x >> 5] = squares;
+        __syncthreads();
+        squares = warp_sum(lane < (int)(blockDim.x >> 5) ? sums[lane] : 0.0f);
+    }
+    const float rstd = norm_rstd(squares, p.dim, p.eps);
+    if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < V; ++j) norm_store<DT, OUT>(p, row, (t + j * p.group) * 8, h[j], rstd);
+}
+
+// Rows too long for registers, a block of 1024 threads each: h is written in the first
+// pass and read again in the second (by the thread that wrote it).
+template <int DT, int OUT>
+__global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p) {
+    __shared__ float sums[32];
+    const int lane = threadIdx.x & 31;
+    const int row = (int)blockIdx.x;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    float squares = 0.0f;
+    for (long long c = threadIdx.x * 8; c < p.dim; c += 8192) {
+        const int col = (int)c;
+        float a[8];
+        unpack8<DT>(load8<DT>(p.x, row * p.ldx + col, col, p.dim), a);
+        if (p.residual != nullptr) {
+            float b[8];
+            unpack8<DT>(load8<DT>(p.residual, row * p.ldr + col, col, p.dim), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] += b[i];
+            const uint4 h = pack8<DT>(a);
+            unpack8<DT>(h, a);
+            store8(p.h, row * p.ldh + col, col, p.dim, h);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) squares = fmaf(a[i], a[i], squares);
+    }
+    squares = warp_sum(squares);
+    if (lane == 0) sums[threadIdx.x >> 5] = squares;
+    __syncthreads();
+    squares = warp_sum(sums[lane]);
+    const float rstd = norm_rstd(squares, p.dim, p.eps);
+    if (threadIdx.x == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    __syncwarp();
+    const void* src = p.residual != nullptr ? p.h : p.x;
+    const long long ld = p.residual != nullptr ? p.ldh : p.ldx;
+    // whole warps to the end of the last block's tile
+    for (long long c = (long long)(threadIdx.x - lane) * 8; c < (p.dim + 127ll & ~127ll); c += 8192) {
+        const int col = (int)c + lane * 8;
+        const uint4 h = col < p.dim ? load8<DT>(src, row * ld + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+        norm_store<DT, OUT>(p, row, col, h, rstd);
+    }
+}
+
+// ---- gradients ---------------------------------------------------------------------------
+
+constexpr int kNormPartials = 608;  // most partial sums of dweight: four blocks an SM
+
+struct NormGradParams {
+    const void *dy, *h, *weight, *dh;
+    const float* rstd;
+    void* dx;
+    float* partial;    // [gridDim.x][dim], NULL where dweight is not wanted
+    long long lddy, ldh, lddh, lddx;
+    int tokens, dim;
+};
+
+// A block's threads share the columns, V vectors of eight each, and walk over the rows,
+// R at a time, their share of dweight in registers.
+template <int DT, int V, int R>
+__global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(const NormGradParams p) {
+    __shared__ float sums[2][32][R];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    float dw[V][8];
+    uint4 w[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
+        w[j] = col < p.dim ? load8<DT>(p.weight, col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+    }
+    int set = 0;
+    for (long long base = (long long)blockIdx.x * R; base < p.tokens; base += (long long)gridDim.x * R, set ^= 1) {
+        uint4 g[V][R], h[V][R];
+        float rstd[R], dot[R];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long row = base + u;
+            rstd[u] = row < p.tokens ? p.rstd[row] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
+                const bool here = col < p.dim && row < p.tokens;
+                g[j][u] = here ? load8<DT>(p.dy, row * p.lddy + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+                h[j][u] = here ? load8<DT>(p.h, row * p.ldh + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            dot[u] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float a[8], b[8], c[8];
+                unpack8<DT>(g[j][u], a);
+                unpack8<DT>(h[j][u], b);
+                unpack8<DT>(w[j], c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot[u] = fmaf(a[i] * c[i], b[i], dot[u]);
+                    dw[j][i] = fmaf(a[i] * b[i], rstd[u], dw[j][i]);
+                }
+            }
+            dot[u] = warp_sum(dot[u]);
+        }
+        if (lane == 0)
+#pragma unroll
+            for (int u = 0; u < R; ++u) sums[set][warp][u] = dot[u];
+        __syncthreads();
+        if (p.dx == nullptr) continue;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            const long long row = base + u;
+            const float all = warp_sum(lane < warps ? sums[set][lane][u] : 0.0f);
+            if (row >= p.tokens) continue;
+            const float back = __fdiv_rn(all, (float)p.dim) * rstd[u] * rstd[u] * rstd[u];
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
+                if (col >= p.dim) continue;
+                float a[8], b[8], c[8], d[8];
+                unpack8<DT>(g[j][u], a);
+                unpack8<DT>(h[j][u], b);
+                unpack8<DT>(w[j], c);
+                if (p.dh != nullptr) {
+                    unpack8<DT>(load8<DT>(p.dh, row * p.lddh + col, col, p.dim), d);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] = 0.0f;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] += fmaf(a[i] * c[i], rstd[u], -b[i] * back);
+                store8(p.dx, row * p.lddx + col, col, p.dim, pack8<DT>(d));
+            }
+        }
+    }
+    if (p.partial == nullptr) return;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (col + i < p.dim) p.partial[(size_t)blockIdx.x * p.dim + col + i] = dw[j][i];
+    }
+}
+
+// dx of rows too long for the above, a block of 1024 threads each, in two passes.
+template <int DT>
+__global__ void __launch_bounds__(1024) rms_norm_grad_long_kernel(const NormGradParams p) {
+    __shared__ float sums[32];
+    const int lane = threadIdx.x & 31;
+    const long long row = blockIdx.x;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const float rstd = p.rstd[row];
+    float dot = 0.0f;
+    for (long long c = threadIdx.x * 8; c < p.dim; c += 8192) {
+        const int col = (int)c;
+        float a[8], b[8], w[8];
+        unpack8<DT>(load8<DT>(p.dy, row * p.lddy + col, col, p.dim), a);
+        unpack8<DT>(load8<DT>(p.h, row * p.ldh + col, col, p.dim), b);
+        unpack8<DT>(load8<DT>(p.weight, col, col, p.dim), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dot = fmaf(a[i] * w[i], b[i], dot);
+    }
+    dot = warp_sum(dot);
+    if (lane == 0) sums[threadIdx.x >> 5] = dot;
+    __syncthreads();
+    const float back = __fdiv_rn(warp_sum(sums[lane]), (float)p.dim) * rstd * rstd * rstd;
+    for (long long c = threadIdx.x * 8; c < p.dim; c += 8192) {
+        const int col = (int)c;
+        float a[8], b[8], w[8], d[8];
+        unpack8<DT>(load8<DT>(p.dy, row * p.lddy + col, col, p.dim), a);
+        unpack8<DT>(load8<DT>(p.h, row * p.ldh + col, col, p.dim), b);
+        unpack8<DT>(load8<DT>(p.weight, col, col, p.dim), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[i] = fmaf(a[i] * w[i], rstd, -b[i] * back);
+        if (p.dh != nullptr) {
+            float e[8];
+            unpack8<DT>(load8<DT>(p.dh, row * p.lddh + col, col, p.dim), e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] += e[i];
+        }
+        store8(p.dx, row * p.lddx + col, col, p.dim, pack8<DT>(d));
+    }
+}
+
+// dweight's partial sums for such rows: a thread on eight columns (blockIdx.x), a share of
+// the rows a block (blockIdx.y).
+template <int DT>
+__global__ void __launch_bounds__(256) rms_norm_grad_columns_kernel(const NormGradParams p) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int col = (int)(blockIdx.x * 256 + threadIdx.x) * 8;
+    if (col >= p.dim) return;
+    const long long r0 = (long long)p.tokens * blockIdx.y / gridDim.y, r1 = (long long)p.tokens * (blockIdx.y + 1) / gridDim.y;
+    float dw[8] = {};
+#pragma unroll 4
+    for (long long row = r0; row < r1; ++row) {
+        const float rstd = p.rstd[row];
+        float a[8], b[8];
+        unpack8<DT>(load8<DT>(p.dy, row * p.lddy + col, col, p.dim), a);
+        unpack8<DT>(load8<DT>(p.h, row * p.ldh + col, col, p.dim), b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[i] = fmaf(a[i] * b[i], rstd, dw[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (col + i < p.dim) p.partial[(size_t)blockIdx.y * p.dim + col + i] = dw[i];
+}
+
+// dweight[c] = sum of partial[b][c], rounded once: 32 columns a block, 32 slices of the
+// partials side by side.
+template <int DT>
+__global__ void __launch_bounds__(1024) rms_norm_weight_sum_kernel(const float* partial, void* out, int blocks, int cols) {
+    __shared__ float sums[32][33];
+    const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+    const long long c = blockIdx.x * 32ll + lane;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    float s = 0.0f;
+    if (c < cols) {
+#pragma unroll 4
+        for (int b = slice; b < blocks; b += 32) s += partial[(size_t)b * cols + c];
+    }
+    sums[slice][lane] = s;
+    __syncthreads();
+    s = warp_sum(sums[lane][slice]);
+    const long long mine = blockIdx.x * 32ll + slice;
+    if (lane == 0 && mine < cols) static_cast<unsigned short*>(out)[mine] = pack1<DT>(s);
+}
+
+}  // namespace tcgemm

@@ -34,7 +34,8 @@ LOSS_PIECE_BYTES = 512 << 20
 _ENTRIES = ("linear_forward", "linear_backward", "linear_backward_workspace", "gated_ffn_forward", "gated_ffn_backward",
             "gated_ffn_backward_workspace", "linear_cross_entropy", "linear_cross_entropy_workspace",
             "linear_cross_entropy_backward", "linear_cross_entropy_backward_workspace", "grad_clip",
-            "grad_clip_workspace")
+            "grad_clip_workspace", "rms_norm_forward", "rms_norm_backward", "rms_norm_backward_workspace", "mx_quantize",
+            "mx_dequantize", "mx_linear")
 _lock = threading.Lock()
 _bound = None
 
