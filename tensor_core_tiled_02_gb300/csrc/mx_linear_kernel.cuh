@@ -1,53 +1,620 @@
-// The linear layer on microscaled operands, element by element.
+// The linear layer on microscaled operands: y = act(x w^T + bias) + residual on the
+// tensor core's block-scaled products (tcgen05.mma, kind::mxf4 and kind::mxf8f6f4),
+// which multiply the values of 32 of K by both operands' scales on the way into the
+// fp32 accumulator.
+//
+// Both formats share one layout: a K step is 128 bytes of each row (256 values of
+// e2m1, 128 of e4m3), one row of the 128-byte swizzle, and four products of 32 bytes.
+// The scales of 128 rows by 4 blocks are one 512-byte tile in memory, in shared memory
+// and, copied by tcgen05.cp, four columns of Tensor Memory: lane row % 32, column
+// row / 32, byte block % 4, repeated for each quarter of the lanes.  A product names
+// the byte it starts from in its instruction descriptor.
+//
+// Two kernels: pairs of CTAs on 256 x 256 tiles, and for few tokens 128 weight rows by
+// up to 128 tokens (the weights as the MMA's M), split along K over a cluster.
 #pragma once
 
+#include "layer_skinny_kernel.cuh"
 #include "mx_common.cuh"
 
 namespace tcgemm {
 
-struct MxLinearParams {
-    const uint8_t *x, *x_scale, *w, *w_scale;
-    const void *bias, *residual;
-    void* y;
-    long long ldx, ldw, ldr, ldy;
-    int tokens, n, blocks;
-    int act;
+namespace ptx {
+
+// D (+)= A B with scales from Tensor Memory; FMT as MxFormat.
+template <int FMT>
+__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
+                                          uint32_t b_scale, uint32_t accumulate) {
+    if constexpr (FMT == kE2M1)
+        asm volatile(
+            "{\n"
+            "  .reg .pred p;\n"
+            "  setp.ne.b32 p, %4, 0;\n"
+            "  tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            "  .reg .pred p;\n"
+            "  setp.ne.b32 p, %4, 0;\n"
+            "  tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+            : "memory");
+}
+
+template <int FMT>
+__device__ __forceinline__ void mma_mx_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
+                                               uint32_t b_scale, uint32_t accumulate) {
+    if constexpr (FMT == kE2M1)
+        asm volatile(
+            "{\n"
+            "  .reg .pred p;\n"
+            "  setp.ne.b32 p, %4, 0;\n"
+            "  tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            "  .reg .pred p;\n"
+            "  setp.ne.b32 p, %4, 0;\n"
+            "  tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
+            : "memory");
+}
+
+// One tile of scales, 32 rows of 16 bytes, into four columns of each quarter of the lanes
+// (the pair's form: in both CTAs, each from its own shared memory).
+__device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+}  // namespace ptx
+
+constexpr int kMxStepBytes = 128;  // of each row a K step
+__host__ __device__ constexpr int mx_step_blocks(int fmt) { return kMxStepBytes / mx_block_bytes(fmt); }  // 4 or 8
+__host__ __device__ constexpr int mx_step_tiles(int fmt) { return mx_step_blocks(fmt) / 4; }              // scale tiles of 128 rows
+
+// Instruction descriptor of a block-scaled product: both operands of the format, K-major,
+// scales in powers of two; `a_byte`, `b_byte`: which byte of the scales' words is the first
+// of this product's.
+template <int FMT>
+__host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int a_byte, int b_byte) {
+    const uint32_t type = FMT == kE2M1 ? 1u : 0u;
+    return ((uint32_t)b_byte << 4) | (type << 7) | (type << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 4) << 24) |
+           ((uint32_t)a_byte << 29);
+}
+
+// Shared-memory descriptor of one tile of scales: no swizzle, groups of 8 rows of 16
+// bytes 128 bytes apart.
+__device__ __forceinline__ uint64_t mx_scale_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+struct MxMaps {
+    CUtensorMap x, w, xs, ws;
 };
 
-// A thread an element of y.
-template <int DT, int FMT>
-__global__ void __launch_bounds__(256) mx_linear_simple_kernel(const MxLinearParams p) {
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
-    const long long at = blockIdx.x * 256ll + threadIdx.x;
-    const long long t = at / p.n, c = at % p.n;
-    if (t >= p.tokens) return;
-    const int k_tiles = (p.blocks + 3) >> 2;
-    float sum = 0.0f;
-    for (int b = 0; b < p.blocks; ++b) {
-        const float scale = mx_scale_value(p.x_scale[mx_scale_word(t, b >> 2, k_tiles) + (b & 3)]) *
-                            mx_scale_value(p.w_scale[mx_scale_word(c, b >> 2, k_tiles) + (b & 3)]);
-        constexpr int kBytes = mx_block_bytes(FMT);
-        float part = 0.0f;
+struct MxEpilogue {
+    int act;
+    const void *bias, *residual;
+    void* y;
+    long long ldr, ldy;
+};
+
+// ---- few tokens ----------------------------------------------------------------------------
+
+constexpr int kMxSkinnySlots = 12;
+
+struct MxSkinnyParams {
+    int T, N, nt, t_tiles;
+    int blocks, k_steps;      // of 32 values; of 128 bytes
+    int split, slots, stage_bytes, tmem_cols, scale_col;
+    MxEpilogue e;
+    long long wait_limit;
+    int inject;
+};
+
+// Bias, activation and residual on four neighbouring columns of token t, stored.
+template <int DT>
+__device__ __forceinline__ void mx_finish4(const MxEpilogue& e, long long t, int n, int left, float (&o)[4]) {
+    if (e.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            auto eight = [&](const uint8_t* d, float(&f)[8]) {
-                uint2 q = make_uint2(*reinterpret_cast<const uint32_t*>(d), 0u);
-                if constexpr (FMT == kE4M3) q.y = *reinterpret_cast<const uint32_t*>(d + 4);
-                mx_unpack8<FMT>(q, 1.0f, f);
-            };
-            float a[8], w[8];
-            eight(p.x + t * p.ldx + b * kBytes + i * (kBytes / 4), a);
-            eight(p.w + c * p.ldw + b * kBytes + i * (kBytes / 4), w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) part = fmaf(a[e], w[e], part);
-        }
-        sum = fmaf(part, scale, sum);
+        for (int i = 0; i < 4; ++i)
+            if (i < left) o[i] += load1<DT>(e.bias, n + i);
     }
-    if (p.bias != nullptr) sum += load1<DT>(p.bias, c);
-    if (p.act != kActNone) with_act(p.act, [&](auto tag) { sum = act_value<decltype(tag)::value>(sum); });
-    if (p.residual != nullptr) sum += load1<DT>(p.residual, t * p.ldr + c);
-    static_cast<unsigned short*>(p.y)[t * p.ldy + c] = pack1<DT>(sum);
+    if (e.act != kActNone)
+        with_act(e.act, [&](auto tag) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = act_value<decltype(tag)::value>(o[i]);
+        });
+    if (e.residual != nullptr) {
+        float r[4];
+        load4<DT>(e.residual, t * e.ldr + n, left, r);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += r[i];
+    }
+    store4<DT>(e.y, t * e.ldy + n, left, o);
+}
+
+template <int FMT, int DT>
+__global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_constant__ MxMaps tm, const MxSkinnyParams p) {
+    constexpr int kTiles = mx_step_tiles(FMT);           // scale tiles of a step
+    constexpr int kScaleCols = 8 * kTiles;               // Tensor Memory columns of a step's scales, both operands
+    constexpr uint32_t kScaleBytes = 512 * kTiles;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t ring = (raw + 1023u) & ~1023u;
+    const int S = p.slots;
+    const uint32_t bar0 = ring + (uint32_t)(S * p.stage_bytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem_raw + (bar0 - raw) + 8 * (2 * kMxSkinnySlots + 1));
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+#ifdef TCGEMM_CHECK
+    if (bar0 + 8u * (2 * kMxSkinnySlots + 1) + 8u > raw + ptx::dynamic_smem_size() || p.nt * 512 > S * p.stage_bytes ||
+        p.scale_col + 2 * kScaleCols > p.tmem_cols || p.nt > p.scale_col) {
+        if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
+        return;  // every CTA decides alike
+    }
+#endif
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kMxSkinnySlots + s); };
+    const uint32_t done_bar = bar0 + 8u * (2 * kMxSkinnySlots);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int CS = p.split;
+    const int rank = (int)blockIdx.x % CS;
+    const int tile = (int)blockIdx.x / CS;
+    const int n_tile = tile / p.t_tiles, t_tile = tile % p.t_tiles;
+    const int n0 = n_tile * 128, t0 = t_tile * p.nt;
+    const int tokens = min(p.nt, p.T - t0);
+    const int own0 = tokens * rank / CS, own1 = tokens * (rank + 1) / CS;
+    const int k0 = (int)((long long)p.k_steps * rank / CS), k1 = (int)((long long)p.k_steps * (rank + 1) / CS);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        ptx::mbar_init(done_bar, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm.w);
+        ptx::prefetch_tmap(&tm.x);
+        ptx::prefetch_tmap(&tm.ws);
+        ptx::prefetch_tmap(&tm.xs);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr((const void*)tmem_slot), p.tmem_cols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------- TMA producer ----------------
+        if (lane == 0 && p.inject == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+            ptx::grid_dependency_wait();
+            // after the wait: whoever starts on this may take it that all kernels before this one are complete
+            ptx::grid_launch_dependents();
+            for (int kb = k0; kb < k1; ++kb) {
+                if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) break;
+                const uint32_t dst = ring + (uint32_t)(stage * p.stage_bytes), fb = full_bar(stage);
+                if (!TC_CHECK(holds(ring, (uint32_t)(S * p.stage_bytes), dst, (uint32_t)p.stage_bytes), kSiteSmemBounds)) break;
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)p.stage_bytes);
+                const uint32_t xd = dst + 128 * kMxStepBytes, sd = xd + (uint32_t)(p.nt * kMxStepBytes);
+                ptx::tma_load_2d(dst, &tm.w, fb, kb * kMxStepBytes, n0);
+                ptx::tma_load_2d(sd, &tm.ws, fb, kb * kTiles * 128, n_tile);
+                ptx::tma_load_2d(xd, &tm.x, fb, kb * kMxStepBytes, t0);
+                ptx::tma_load_2d(sd + kScaleBytes, &tm.xs, fb, kb * kTiles * 128, t_tile);
+                issued_mask |= 1u << stage;
+                issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            for (int s = 0; s < S; ++s)
+                if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer ----------------
+        if (lane == 0) {
+            const uint32_t idesc = mx_idesc<FMT>(128, p.nt, 0, 0);
+            int stage = 0, old_stage = 0;
+            uint32_t phase = 0, old_phase = 0;
+            for (int kb = k0; kb < k1; ++kb) {
+                // two sets of scales in Tensor Memory: the products that read this one are complete
+                if (kb - k0 >= 2) {
+                    if (!wait_bounded(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) break;
+                    if (++old_stage == S) {
+                        old_stage = 0;
+                        old_phase ^= 1u;
+                    }
+                }
+                if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) break;
+                ptx::tc_fence_after();
+                const uint32_t src = ring + (uint32_t)(stage * p.stage_bytes);
+                const uint32_t xsrc = src + 128 * kMxStepBytes, ssrc = xsrc + (uint32_t)(p.nt * kMxStepBytes);
+                const uint32_t wcol = tmem + (uint32_t)(p.scale_col + ((kb - k0) & 1) * kScaleCols), xcol = wcol + 4 * kTiles;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    ptx::tmem_cp_scales(wcol + 4 * i, mx_scale_desc(ssrc + 512 * i));
+                    ptx::tmem_cp_scales(xcol + 4 * i, mx_scale_desc(ssrc + kScaleBytes + 512 * i));
+                }
+                const uint64_t wd = operand_desc<false>(src), xd = operand_desc<false>(xsrc);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    constexpr int kPer = FMT == kE2M1 ? 2 : 1;  // blocks of a product
+                    if (kb * mx_step_blocks(FMT) + j * kPer < p.blocks) {
+                        const uint32_t byte = (uint32_t)(j * kPer) & 3u, at = (uint32_t)(j * kPer) >> 2;
+                        ptx::mma_mx_ss<FMT>(tmem, wd + 2 * j, xd + 2 * j, idesc | (byte << 4) | (byte << 29), wcol + 4 * at,
+                                            xcol + 4 * at, ((kb - k0) | j) != 0);
+                    }
+                }
+                ptx::mma_commit(empty_bar(stage));
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            ptx::mma_commit(done_bar);  // also after an abort: no MMA outlives the accumulator
+            wait_drain(done_bar, 0, p.wait_limit);
+        }
+    } else {
+        // ---------------- this CTA's partial out of TMEM ----------------
+        const int q = warp & 3;
+        ptx::grid_dependency_wait();
+        if (warp_wait(done_bar, 0, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane) && *abort_flag == 0) {
+            ptx::tc_fence_after();
+            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16);
+            const uint32_t col = (uint32_t)((q * 32 + lane) * 4);
+            // the ring is idle: every load was consumed by an MMA, and every MMA is complete
+#pragma unroll 1
+            for (int c = 0; c < p.nt; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(trow + c, v);
+                ptx::tmem_ld_wait();
+                // [token][128 columns] fp32
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + col + (uint32_t)((c + i) * 512)), "r"(v[i]) : "memory");
+            }
+        }
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, p.tmem_cols);
+    }
+    if (CS > 1) {
+        __syncwarp();
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    }
+    if (*abort_flag == 0) {
+        // the previous kernel's reads and writes of what is read and written below are done
+        ptx::grid_dependency_wait();
+        // a warp on each of this CTA's tokens, a lane four columns, summed over the cluster first
+        const int c = lane * 4, n = n0 + c, left = p.N - n;
+        constexpr int kWarps = kThreads / 32;
+        if (CS > 1) {
+            if (CS <= 4)
+                pull_sums<4, 4, 1>(ring, p.nt, CS, own0 + warp, own1, c);
+            else
+                pull_sums<8, 2, 1>(ring, p.nt, CS, own0 + warp, own1, c);
+        }
+        if (left > 0) {
+#pragma unroll 1
+            for (int tt = own0 + warp; tt < own1; tt += kWarps) {
+                float o[4];
+                ld_shared_f4(ring + (uint32_t)(tt * 512 + c * 4), o[0], o[1], o[2], o[3]);
+                mx_finish4<DT>(p.e, t0 + tt, n, left, o);
+            }
+        }
+    }
+    if (CS > 1) {
+        // no CTA leaves while another still reads its partial
+        __syncwarp();
+        ptx::cluster_arrive_relaxed();
+        ptx::cluster_wait();
+    }
+}
+
+// ---- CTA pairs -----------------------------------------------------------------------------
+
+template <int FMT>
+struct MxPairLayout {
+    static constexpr int kTiles = mx_step_tiles(FMT);
+    static constexpr int kOperandBytes = 128 * kMxStepBytes;      // this CTA's 128 rows of x, or half of the tile's of w
+    static constexpr int kScaleBytes = 512 * kTiles;              // 128 rows' scales of a step
+    static constexpr int kStageBytes = 2 * kOperandBytes + 3 * kScaleBytes;  // x, w; scales of x's 128 rows and of all 256 of w
+    static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr int kSlots = 6;
+    // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain
+    static constexpr int kNumBars = 2 * kMaxStages + 6;
+    static constexpr int kSmem = 1024 + kSlots * kStride + kNumBars * 8 + 16;
+    static_assert(kSlots <= kMaxStages && kSmem <= 232448, "shared memory");
+    // Tensor Memory: the accumulators overlap in kShared columns, and two steps' scales follow
+    static constexpr int kScaleCols = 12 * kTiles;
+    static constexpr int kSecond = 256 - 64;
+    static constexpr int kScaleCol = kSecond + 256;
+    static_assert(kScaleCol + 2 * kScaleCols <= 512, "Tensor Memory");
+};
+
+struct MxPairParams {
+    int M, N;
+    int tiles_m, tiles_n;
+    int blocks, k_steps;
+    int raster_group;
+    MxEpilogue e;
+    long long wait_limit;
+    int inject;
+};
+
+// 32 neighbouring columns of a row through the epilogue, stored.
+template <int DT>
+__device__ __forceinline__ void mx_finish32(const MxEpilogue& e, long long row, int n, int left, uint32_t (&v)[32]) {
+    if (e.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < left) v[i] = __float_as_uint(__uint_as_float(v[i]) + load1<DT>(e.bias, n + i));
+    }
+    if (e.act != kActNone)
+        with_act(e.act, [&](auto tag) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_value<decltype(tag)::value>(__uint_as_float(v[i])));
+        });
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j * 8 >= left) break;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
+        if (e.residual != nullptr) {
+            float r[8];
+            unpack8<DT>(load8<DT>(e.residual, row * e.ldr + n + 8 * j, 8 * j, left), r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] += r[i];
+        }
+        store8(e.y, row * e.ldy + n + 8 * j, 8 * j, left, pack8<DT>(f));
+    }
+}
+
+template <int FMT, int DT>
+__global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
+    mx_pair_kernel(const __grid_constant__ MxMaps tm, const MxPairParams p) {
+    using L = MxPairLayout<FMT>;
+    constexpr int S = L::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = ptx::smem_addr(smem_raw);
+    const uint32_t ring = (raw + 1023u) & ~1023u;
+    const uint32_t bar0 = ring + S * L::kStride;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (bar0 - raw) + 8 * L::kNumBars);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+#ifdef TCGEMM_CHECK
+    if (bar0 + 8u * L::kNumBars + 8u > raw + ptx::dynamic_smem_size()) {
+        if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
+        return;
+    }
+#endif
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
+    auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
+    const uint32_t shared_bar = bar0 + 8u * (2 * kMaxStages + 4), drain_bar = shared_bar + 8u;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();  // 0 issues the MMAs
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            ptx::mbar_init(full_bar(s), 1);
+            ptx::mbar_init(empty_bar(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            ptx::mbar_init(tfull_bar(a), 1);
+            ptx::mbar_init(tempty_bar(a), 2 * L::kWarps);  // every epilogue warp of both CTAs
+        }
+        ptx::mbar_init(shared_bar, 2 * L::kWarps);
+        ptx::mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tm.x);
+        ptx::prefetch_tmap(&tm.w);
+        ptx::prefetch_tmap(&tm.xs);
+        ptx::prefetch_tmap(&tm.ws);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(ptx::smem_addr((const void*)tmem_slot), 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
+    const int tiles = p.tiles_m * p.tiles_n;
+    auto coords = [&](int t, int& mb, int& nb) {  // groups of m-blocks, every second one backwards along n
+        const int per_group = p.raster_group * p.tiles_n;
+        const int grp = t / per_group, first_m = grp * p.raster_group;
+        const int gm = min(p.tiles_m - first_m, p.raster_group);
+        const int r = t - grp * per_group;
+        mb = first_m + r % gm;
+        nb = r / gm;
+        if (grp & 1) nb = p.tiles_n - 1 - nb;
+    };
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        if (lane == 0 && p.inject == 0) {
+            int stage = 0;
+            uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+            bool ok = true;
+            ptx::grid_dependency_wait();
+            ptx::grid_launch_dependents();
+            for (int t = pair; ok && t < tiles; t += pairs) {
+                int mb, nb;
+                coords(t, mb, nb);
+                for (int kb = 0; kb < p.k_steps; ++kb) {
+                    if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = ring + stage * L::kStride;
+                    if (!TC_CHECK(holds(ring, S * L::kStride, dst, L::kStageBytes), kSiteSmemBounds)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb_local = full_bar(stage);
+                    if (rank == 0) ptx::mbar_arrive_expect_tx(fb_local, 2 * L::kStageBytes);
+                    const uint32_t fb = ptx::mapa(fb_local, 0), sd = dst + 2 * L::kOperandBytes;
+                    const int kx = kb * kMxStepBytes, ks = kb * L::kTiles * 128;
+                    ptx::tma_load_2d_pair(dst, &tm.x, fb, kx, mb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(dst + L::kOperandBytes, &tm.w, fb, kx, nb * 256 + (int)rank * 128);
+                    ptx::tma_load_2d_pair(sd, &tm.xs, fb, ks, mb * 2 + (int)rank);
+                    ptx::tma_load_2d_pair(sd + L::kScaleBytes, &tm.ws, fb, ks, nb * 2);
+                    ptx::tma_load_2d_pair(sd + 2 * L::kScaleBytes, &tm.ws, fb, ks, nb * 2 + 1);
+                    issued_mask |= 1u << stage;
+                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // both CTAs' bytes land before shared memory goes away
+            if (rank == 0)
+                for (int s = 0; s < S; ++s)
+                    if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (leader only) ----------------
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = mx_idesc<FMT>(256, 256, 0, 0);
+            int stage = 0, old_stage = 0, tl = 0;
+            uint32_t phase = 0, old_phase = 0;
+            long long step = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
+                const int acc = tl & 1;
+                // this accumulator's last tile is drained, and of the other's the columns they share
+                if (!wait_bounded<true>(tempty_bar(acc), ((tl >> 1) & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty) ||
+                    !wait_bounded<true>(shared_bar, (tl & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t d_tmem = tmem + (uint32_t)(acc * L::kSecond);
+                for (int kb = 0; kb < p.k_steps; ++kb, ++step) {
+                    // two sets of scales in Tensor Memory: the products that read this one are complete
+                    if (step >= 2) {
+                        if (!wait_bounded(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        if (++old_stage == S) {
+                            old_stage = 0;
+                            old_phase ^= 1u;
+                        }
+                    }
+                    if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t src = ring + stage * L::kStride, ssrc = src + 2 * L::kOperandBytes;
+                    const uint32_t xcol = tmem + L::kScaleCol + (uint32_t)(step & 1) * L::kScaleCols, wcol = xcol + 4 * L::kTiles;
+#pragma unroll
+                    for (int i = 0; i < L::kTiles; ++i) {
+                        // w's 256 rows are eight neighbouring columns a tile of K
+                        ptx::tmem_cp_scales_pair(xcol + 4 * i, mx_scale_desc(ssrc + 512 * i));
+                        ptx::tmem_cp_scales_pair(wcol + 8 * i, mx_scale_desc(ssrc + L::kScaleBytes + 512 * i));
+                        ptx::tmem_cp_scales_pair(wcol + 8 * i + 4, mx_scale_desc(ssrc + 2 * L::kScaleBytes + 512 * i));
+                    }
+                    const uint64_t xd = operand_desc<false>(src), wd = operand_desc<false>(src + L::kOperandBytes);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        constexpr int kPer = FMT == kE2M1 ? 2 : 1;  // blocks of a product
+                        if (kb * mx_step_blocks(FMT) + j * kPer < p.blocks) {
+                            const uint32_t byte = (uint32_t)(j * kPer) & 3u, at = (uint32_t)(j * kPer) >> 2;
+                            ptx::mma_mx_ss_pair<FMT>(d_tmem, xd + 2 * j, wd + 2 * j, idesc | (byte << 4) | (byte << 29), xcol + 4 * at,
+                                                     wcol + 8 * at, (kb | j) != 0);
+                        }
+                    }
+                    ptx::mma_commit_pair_multicast(empty_bar(stage), 3);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                ptx::mma_commit_pair_multicast(tfull_bar(acc), 3);
+            }
+            ptx::mma_commit_pair(drain_bar);
+            wait_drain(drain_bar, 0, p.wait_limit);
+        }
+    } else {
+        // ---------------- epilogue (both CTAs): 32 rows a warp ----------------
+        const int q = warp & 3;
+        ptx::grid_dependency_wait();
+        ptx::grid_launch_dependents();
+        int tl = 0;
+        for (int t = pair; t < tiles; t += pairs, ++tl) {
+            int mb, nb;
+            coords(t, mb, nb);
+            const int acc = tl & 1;
+            if (!warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
+            ptx::tc_fence_after();
+            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond);
+            const int row = mb * 256 + (int)rank * 128 + q * 32 + lane;
+            const int n0 = nb * 256;
+            // the columns the accumulators share first: the first 64 of the second, the last of the first
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const int c = acc ? i : (i + 6) & 7;
+                uint32_t v[32];
+                ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
+                ptx::tmem_ld_wait();
+                if (i == 1 || i == 7) {
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 1 ? shared_bar : tempty_bar(acc), 0));
+                }
+                const int left = p.N - (n0 + c * 32);
+                if (row < p.M && left > 0) mx_finish32<DT>(p.e, row, n0 + c * 32, left, v);
+                __syncwarp();
+            }
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    // neither CTA leaves while the other may still signal into it
+    ptx::cluster_arrive_relaxed();
+    ptx::cluster_wait();
+    if (warp == 1) {
+        __syncwarp();
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, 512);
+    }
 }
 
 }  // namespace tcgemm

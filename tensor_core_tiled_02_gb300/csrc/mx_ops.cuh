@@ -109,6 +109,133 @@ int run_norm_grad(const NormGradParams& p, const NormGradPlan& g, void* dweight,
     return rc;
 }
 
+// ---- linear layer -------------------------------------------------------------------------
+
+// `rows` rows of one K step of a microscaled matrix, 128-byte swizzled.
+int encode_mx_data(CUtensorMap* out, const Mx& m, uint32_t rows) {
+    cuuint64_t dims[2] = {(cuuint64_t)mx_width(m), (cuuint64_t)m.rows};
+    cuuint64_t strides[1] = {(cuuint64_t)m.ld};
+    cuuint32_t box[2] = {kMxStepBytes, rows}, estr[2] = {1, 1};
+    return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(m.data), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? GEMM_OK
+               : GEMM_ERR_TMAP;
+}
+
+// Its scales: a row of tiles a row, in words; a K step is one tile or two.
+int encode_mx_scale(CUtensorMap* out, const Mx& m) {
+    const long long k_tiles = ceil_div(m.cols, 128);
+    cuuint64_t dims[2] = {(cuuint64_t)k_tiles * 128, (cuuint64_t)ceil_div(m.rows, 128)};
+    cuuint64_t strides[1] = {(cuuint64_t)k_tiles * 512};
+    cuuint32_t box[2] = {(cuuint32_t)mx_step_tiles(m.fmt) * 128, 1}, estr[2] = {1, 1};
+    return g_encode(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(m.scale), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? GEMM_OK
+               : GEMM_ERR_TMAP;
+}
+
+struct MxProduct {
+    Mx x, w;
+    MxEpilogue e;
+};
+
+int encode_mx(MxMaps* tm, const MxProduct& q, uint32_t x_rows) {
+    std::memset(tm, 0, sizeof(*tm));
+    int rc = encode_mx_data(&tm->x, q.x, x_rows);
+    if (rc == GEMM_OK) rc = encode_mx_data(&tm->w, q.w, 128);
+    if (rc == GEMM_OK) rc = encode_mx_scale(&tm->xs, q.x);
+    if (rc == GEMM_OK) rc = encode_mx_scale(&tm->ws, q.w);
+    return rc;
+}
+
+struct MxSkinnyPlan {
+    int nt, t_tiles, tiles, split, slots, stage_bytes, smem, scale_col, tmem_cols, k_steps;
+};
+
+MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
+    MxSkinnyPlan g{};
+    const int fmt = q.x.fmt;
+    g.t_tiles = ceil_div(q.x.rows, 128);
+    g.nt = g.t_tiles > 1 ? 128 : ceil_div(q.x.rows, 16) * 16;
+    g.tiles = ceil_div(q.w.rows, 128) * g.t_tiles;
+    g.k_steps = ceil_div(mx_width(q.x), kMxStepBytes);
+    g.stage_bytes = (128 + g.nt) * kMxStepBytes + 1024 * mx_step_tiles(fmt);
+    g.scale_col = (g.nt + 31) / 32 * 32;
+    const int cols = g.scale_col + 16 * mx_step_tiles(fmt);
+    g.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    g.split = 1;
+    for (int s = 2; s <= kMaxSplit && 2 * s <= g.k_steps && g.tiles * g.split < sms * 4 / 5; ++s) g.split = s;
+    const int fixed = 1024 + 8 * (2 * kMxSkinnySlots + 1) + 16;
+    g.slots = (kSkinnyTwoSmem - fixed) / g.stage_bytes;
+    if (g.slots > kMxSkinnySlots) g.slots = kMxSkinnySlots;
+    g.smem = g.slots * g.stage_bytes + fixed;
+    return g;
+}
+
+template <int FMT, int DT>
+int run_mx_skinny(const MxProduct& q, const MxSkinnyPlan& g, const Ctx& c) {
+    MxMaps tm;
+    int rc = encode_mx(&tm, q, g.nt);
+    if (rc != GEMM_OK) return rc;
+    MxSkinnyParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.T = (int)q.x.rows;
+    p.N = (int)q.w.rows;
+    p.nt = g.nt;
+    p.t_tiles = g.t_tiles;
+    p.blocks = (int)mx_blocks(q.x);
+    p.k_steps = g.k_steps;
+    p.split = g.split;
+    p.slots = g.slots;
+    p.stage_bytes = g.stage_bytes;
+    p.tmem_cols = g.tmem_cols;
+    p.scale_col = g.scale_col;
+    p.e = q.e;
+    p.wait_limit = c.wait_limit;
+    p.inject = c.inject;
+    auto kern = mx_skinny_kernel<FMT, DT>;
+    static std::atomic<bool> ready[kMaxDevices];
+    rc = ensure_smem_limit(kern, kSmemLimit, ready[c.ordinal]);
+    if (rc != GEMM_OK) return rc;
+    return launch_pdl(kern, dim3(g.tiles * g.split), kThreads, g.smem, g.split, c.stream, tm, p);
+}
+
+template <int FMT, int DT>
+int run_mx_pair(const MxProduct& q, const Ctx& c) {
+    using L = MxPairLayout<FMT>;
+    MxMaps tm;
+    int rc = encode_mx(&tm, q, 128);
+    if (rc != GEMM_OK) return rc;
+    MxPairParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.M = (int)q.x.rows;
+    p.N = (int)q.w.rows;
+    p.tiles_m = ceil_div(q.x.rows, 256);
+    p.tiles_n = ceil_div(q.w.rows, 256);
+    const long long tiles = (long long)p.tiles_m * p.tiles_n;
+    if (tiles > INT_MAX - 1024) return GEMM_ERR_DIM;
+    p.blocks = (int)mx_blocks(q.x);
+    p.k_steps = ceil_div(mx_width(q.x), kMxStepBytes);
+    p.raster_group = 8;
+    p.e = q.e;
+    p.wait_limit = c.wait_limit;
+    p.inject = c.inject;
+    auto kern = mx_pair_kernel<FMT, DT>;
+    static std::atomic<bool> ready[kMaxDevices];
+    rc = ensure_smem_limit(kern, L::kSmem, ready[c.ordinal]);
+    if (rc != GEMM_OK) return rc;
+    const int pairs = max_pairs_of(*c.dev);
+    return launch_pdl(kern, dim3(2 * (int)(tiles < pairs ? tiles : pairs)), L::kThreads, L::kSmem, 2, c.stream, tm, p);
+}
+
+template <int FMT, int DT>
+int run_mx_product(const MxProduct& q, const Ctx& c) {
+    if (q.x.rows <= 256) return run_mx_skinny<FMT, DT>(q, mx_skinny_plan(q, c.dev->sms), c);
+    return run_mx_pair<FMT, DT>(q, c);
+}
+
 int check_dtype16(long long dtype) { return check_dtype_act(dtype, LAYER_ACT_NONE); }
 
 }  // namespace
@@ -304,28 +431,14 @@ int mx_linear(const mx_linear_args* args, gemm_stream_t stream) {
     if (overlaps(wr, 1, rd, 6)) return GEMM_ERR_ALIAS;
     Ctx c;
     if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
-    MxLinearParams p{};
-    p.x = static_cast<const uint8_t*>(a.x);
-    p.x_scale = static_cast<const uint8_t*>(a.x_scale);
-    p.w = static_cast<const uint8_t*>(a.w);
-    p.w_scale = static_cast<const uint8_t*>(a.w_scale);
-    p.bias = a.bias;
-    p.residual = a.residual;
-    p.y = a.y;
-    p.ldx = a.ldx;
-    p.ldw = a.ldw;
-    p.ldr = a.ldr;
-    p.ldy = a.ldy;
-    p.tokens = (int)a.tokens;
-    p.n = (int)a.n;
-    p.blocks = ceil_div(a.k, kMxBlock);
-    p.act = (int)a.act;
-    const long long blocks = (a.tokens * a.n + 255) / 256;
-    if (blocks > INT_MAX) return GEMM_ERR_DIM;
-    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
-        return launch_pdl(mx_linear_simple_kernel<decltype(dt)::value, decltype(fmt)::value>, dim3((unsigned)blocks), 256, 0, 1,
-                          c.stream, p);
-    });
+    MxProduct q{x, w, {}};
+    q.e.act = (int)a.act;
+    q.e.bias = a.bias;
+    q.e.residual = a.residual;
+    q.e.y = a.y;
+    q.e.ldr = a.ldr;
+    q.e.ldy = a.ldy;
+    return with_types(a.dtype, a.format, [&](auto dt, auto fmt) { return run_mx_product<decltype(fmt)::value, decltype(dt)::value>(q, c); });
 }
 
 }  // extern "C"
