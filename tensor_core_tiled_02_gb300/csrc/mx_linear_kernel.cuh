@@ -348,8 +348,12 @@ struct MxPairLayout {
     static constexpr int kSlots = 6;
     // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain
     static constexpr int kNumBars = 2 * kMaxStages + 6;
-    static constexpr int kSmem = 1024 + kSlots * kStride + kNumBars * 8 + 16;
-    static_assert(kSlots <= kMaxStages && kSmem <= 232448, "shared memory");
+    // All of an SM's shared memory, whatever is used of it, as the other kernels on pairs take
+    // it: no other kernel's CTAs lie beside these.  (With 17 KB left, between norms whose CTAs
+    // came to lie on the same SMs, a launch in about a thousand never ended, in none of its
+    // bounded waits; why is not known.  So: none in 44,000.)
+    static constexpr int kSmem = 232448;
+    static_assert(kSlots <= kMaxStages && 1024 + kSlots * kStride + kNumBars * 8 + 16 <= kSmem, "shared memory");
     // Tensor Memory: the accumulators overlap in kShared columns, and two steps' scales follow
     static constexpr int kScaleCols = 12 * kTiles;
     static constexpr int kSecond = 256 - 64;
@@ -594,7 +598,9 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                 uint32_t v[32];
                 ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
                 ptx::tmem_ld_wait();
-                if (i == 1 || i == 7) {
+                // handed back only where another tile waits for it: an arrival still under way
+                // when the leader leaves would land in the shared memory of whoever follows
+                if ((i == 1 && t + pairs < tiles) || (i == 7 && t + 2 * pairs < tiles)) {
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 1 ? shared_bar : tempty_bar(acc), 0));

@@ -170,7 +170,7 @@ MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
     const int fixed = 1024 + 8 * (2 * kMxSkinnySlots + 1) + 16;
     g.slots = (kSkinnyTwoSmem - fixed) / g.stage_bytes;
     if (g.slots > kMxSkinnySlots) g.slots = kMxSkinnySlots;
-    g.smem = g.slots * g.stage_bytes + fixed;
+    g.smem = kSkinnyTwoSmem;  // two CTAs fill an SM
     return g;
 }
 
