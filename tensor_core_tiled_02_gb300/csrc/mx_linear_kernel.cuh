@@ -21,60 +21,72 @@ namespace tcgemm {
 
 namespace ptx {
 
-// D (+)= A B with scales from Tensor Memory; FMT as MxFormat.
-template <int FMT>
-__device__ __forceinline__ void mma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
-                                          uint32_t b_scale, uint32_t accumulate) {
-    if constexpr (FMT == kE2M1)
-        asm volatile(
-            "{\n"
-            "  .reg .pred p;\n"
-            "  setp.ne.b32 p, %4, 0;\n"
-            "  tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
-            : "memory");
-    else
-        asm volatile(
-            "{\n"
-            "  .reg .pred p;\n"
-            "  setp.ne.b32 p, %4, 0;\n"
-            "  tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
-            : "memory");
+// The tensor core's instructions take their operands from uniform registers.  A thread by
+// itself pays for every one that it computed (110 to 150 cycles a product with scales,
+// whose arithmetic takes 128 and less), so here the whole warp walks the loop, on values
+// and votes that are the same in every lane, and only the instructions are one lane's.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        "  .reg .pred p;\n"
+        "  elect.sync _|p, 0xffffffff;\n"
+        "  selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p;
 }
 
-template <int FMT>
-__device__ __forceinline__ void mma_mx_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
-                                               uint32_t b_scale, uint32_t accumulate) {
-    if constexpr (FMT == kE2M1)
-        asm volatile(
-            "{\n"
-            "  .reg .pred p;\n"
-            "  setp.ne.b32 p, %4, 0;\n"
-            "  tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
-            : "memory");
-    else
-        asm volatile(
-            "{\n"
-            "  .reg .pred p;\n"
-            "  setp.ne.b32 p, %4, 0;\n"
-            "  tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale)
-            : "memory");
+#define TC_MX_MMA(GROUP, KIND)                                                                              \
+    asm volatile(                                                                                           \
+        "{\n"                                                                                               \
+        "  .reg .pred p, e;\n"                                                                              \
+        "  setp.ne.b32 p, %4, 0;\n"                                                                         \
+        "  setp.ne.b32 e, %7, 0;\n"                                                                         \
+        "  @e tcgen05.mma.cta_group::" GROUP "." KIND " [%0], %1, %2, %3, [%5], [%6], p;\n"                \
+        "}\n" ::"r"(d_tmem),                                                                                \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(a_scale), "r"(b_scale), "r"(elected)     \
+        : "memory")
+
+// D (+)= A B with scales from Tensor Memory, on one CTA or a pair (GROUP); FMT as MxFormat.
+template <int FMT, int GROUP>
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t a_scale,
+                                       uint32_t b_scale, uint32_t accumulate, uint32_t elected) {
+    if constexpr (FMT == kE2M1 && GROUP == 1) TC_MX_MMA("1", "kind::mxf4.block_scale.scale_vec::2X");
+    if constexpr (FMT == kE2M1 && GROUP == 2) TC_MX_MMA("2", "kind::mxf4.block_scale.scale_vec::2X");
+    if constexpr (FMT == kE4M3 && GROUP == 1) TC_MX_MMA("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    if constexpr (FMT == kE4M3 && GROUP == 2) TC_MX_MMA("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
 }
+#undef TC_MX_MMA
 
 // One tile of scales, 32 rows of 16 bytes, into four columns of each quarter of the lanes
 // (the pair's form: in both CTAs, each from its own shared memory).
-__device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+template <int GROUP>
+__device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc, uint32_t elected) {
+    if constexpr (GROUP == 1)
+        asm volatile("{\n  .reg .pred e;\n  setp.ne.b32 e, %2, 0;\n  @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(tmem),
+                     "l"(desc), "r"(elected)
+                     : "memory");
+    else
+        asm volatile("{\n  .reg .pred e;\n  setp.ne.b32 e, %2, 0;\n  @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}\n" ::"r"(tmem),
+                     "l"(desc), "r"(elected)
+                     : "memory");
 }
-__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+
+// mma_commit and its pair forms (to the leader alone, or to both CTAs).
+__device__ __forceinline__ void commit_one(uint32_t bar, uint32_t elected) {
+    asm volatile(
+        "{\n  .reg .pred e;\n  setp.ne.b32 e, %1, 0;\n"
+        "  @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void commit_both(uint32_t bar, uint32_t elected) {
+    asm volatile(
+        "{\n  .reg .pred e;\n  setp.ne.b32 e, %2, 0;\n"
+        "  @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(bar),
+        "h"((uint16_t)3), "r"(elected)
+        : "memory");
 }
 
 }  // namespace ptx
@@ -97,6 +109,25 @@ __host__ __device__ constexpr uint32_t mx_idesc(int m, int n, int a_byte, int b_
 // bytes 128 bytes apart.
 __device__ __forceinline__ uint64_t mx_scale_desc(uint32_t saddr) {
     return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+
+// wait_bounded by a whole warp: every lane asks, and all go the same way.
+template <bool kClusterAcquire = false>
+__device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, unsigned site) {
+    auto probe = [&]() {
+        return __all_sync(0xffffffffu, kClusterAcquire ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) != 0;
+    };
+    if (probe()) return true;
+    const long long t0 = clock64();
+    while (!probe()) {
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) return false;
+        if (__any_sync(0xffffffffu, clock64() - t0 > limit)) {
+            *abort_flag = 1;
+            record_timeout(site);
+            return false;
+        }
+    }
+    return true;
 }
 
 struct MxMaps {
@@ -229,49 +260,48 @@ __global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_consta
                 if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer ----------------
-        if (lane == 0) {
-            const uint32_t idesc = mx_idesc<FMT>(128, p.nt, 0, 0);
-            int stage = 0, old_stage = 0;
-            uint32_t phase = 0, old_phase = 0;
-            for (int kb = k0; kb < k1; ++kb) {
-                // two sets of scales in Tensor Memory: the products that read this one are complete
-                if (kb - k0 >= 2) {
-                    if (!wait_bounded(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) break;
-                    if (++old_stage == S) {
-                        old_stage = 0;
-                        old_phase ^= 1u;
-                    }
-                }
-                if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) break;
-                ptx::tc_fence_after();
-                const uint32_t src = ring + (uint32_t)(stage * p.stage_bytes);
-                const uint32_t xsrc = src + 128 * kMxStepBytes, ssrc = xsrc + (uint32_t)(p.nt * kMxStepBytes);
-                const uint32_t wcol = tmem + (uint32_t)(p.scale_col + ((kb - k0) & 1) * kScaleCols), xcol = wcol + 4 * kTiles;
-#pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
-                    ptx::tmem_cp_scales(wcol + 4 * i, mx_scale_desc(ssrc + 512 * i));
-                    ptx::tmem_cp_scales(xcol + 4 * i, mx_scale_desc(ssrc + kScaleBytes + 512 * i));
-                }
-                const uint64_t wd = operand_desc<false>(src), xd = operand_desc<false>(xsrc);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    constexpr int kPer = FMT == kE2M1 ? 2 : 1;  // blocks of a product
-                    if (kb * mx_step_blocks(FMT) + j * kPer < p.blocks) {
-                        const uint32_t byte = (uint32_t)(j * kPer) & 3u, at = (uint32_t)(j * kPer) >> 2;
-                        ptx::mma_mx_ss<FMT>(tmem, wd + 2 * j, xd + 2 * j, idesc | (byte << 4) | (byte << 29), wcol + 4 * at,
-                                            xcol + 4 * at, ((kb - k0) | j) != 0);
-                    }
-                }
-                ptx::mma_commit(empty_bar(stage));
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1u;
+        // ---------------- MMA issuer (the whole warp) ----------------
+        const uint32_t idesc = mx_idesc<FMT>(128, p.nt, 0, 0), elected = ptx::elect_one();
+        int stage = 0, old_stage = 0;
+        uint32_t phase = 0, old_phase = 0;
+        for (int kb = k0; kb < k1; ++kb) {
+            // two sets of scales in Tensor Memory: the products that read this one are complete
+            if (kb - k0 >= 2) {
+                if (!wait_uniform(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) break;
+                if (++old_stage == S) {
+                    old_stage = 0;
+                    old_phase ^= 1u;
                 }
             }
-            ptx::mma_commit(done_bar);  // also after an abort: no MMA outlives the accumulator
-            wait_drain(done_bar, 0, p.wait_limit);
+            if (!wait_uniform(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) break;
+            ptx::tc_fence_after();
+            const uint32_t src = ring + (uint32_t)(stage * p.stage_bytes);
+            const uint32_t xsrc = src + 128 * kMxStepBytes, ssrc = xsrc + (uint32_t)(p.nt * kMxStepBytes);
+            const uint32_t wcol = tmem + (uint32_t)(p.scale_col + ((kb - k0) & 1) * kScaleCols), xcol = wcol + 4 * kTiles;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                ptx::tmem_cp_scales<1>(wcol + 4 * i, mx_scale_desc(ssrc + 512 * i), elected);
+                ptx::tmem_cp_scales<1>(xcol + 4 * i, mx_scale_desc(ssrc + kScaleBytes + 512 * i), elected);
+            }
+            const uint64_t wd = operand_desc<false>(src), xd = operand_desc<false>(xsrc);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                constexpr int kPer = FMT == kE2M1 ? 2 : 1;  // blocks of a product
+                if (kb * mx_step_blocks(FMT) + j * kPer < p.blocks) {
+                    const uint32_t byte = (uint32_t)(j * kPer) & 3u, at = (uint32_t)(j * kPer) >> 2;
+                    ptx::mma_mx<FMT, 1>(tmem, wd + 2 * j, xd + 2 * j, idesc | (byte << 4) | (byte << 29), wcol + 4 * at, xcol + 4 * at,
+                                        ((kb - k0) | j) != 0, elected);
+                }
+            }
+            ptx::commit_one(empty_bar(stage), elected);
+            if (++stage == S) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
+        ptx::commit_one(done_bar, elected);  // also after an abort: no MMA outlives the accumulator
+        if (lane == 0) wait_drain(done_bar, 0, p.wait_limit);
+        __syncwarp();
     } else {
         // ---------------- this CTA's partial out of TMEM ----------------
         const int q = warp & 3;
@@ -511,27 +541,31 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                     if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer (leader only) ----------------
-        if (lane == 0 && rank == 0) {
+        // ---------------- MMA issuer (leader only, the whole warp) ----------------
+        if (rank == 0) {
             constexpr uint32_t idesc = mx_idesc<FMT>(256, 256, 0, 0);
+            const uint32_t elected = ptx::elect_one();
             int stage = 0, old_stage = 0, tl = 0;
-            uint32_t phase = 0, old_phase = 0;
-            long long step = 0;
+            uint32_t phase = 0, old_phase = 0, set = 0;
+            int under_way = 0;  // steps whose scales may still be read, two at most
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
                 const int acc = tl & 1;
                 // this accumulator's last tile is drained, and of the other's the columns they share
-                if (!wait_bounded<true>(tempty_bar(acc), ((tl >> 1) & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty) ||
-                    !wait_bounded<true>(shared_bar, (tl & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                if (!wait_uniform<true>(tempty_bar(acc), ((tl >> 1) & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty) ||
+                    !wait_uniform<true>(shared_bar, (tl & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
                     ok = false;
                     break;
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)(acc * L::kSecond);
-                for (int kb = 0; kb < p.k_steps; ++kb, ++step) {
-                    // two sets of scales in Tensor Memory: the products that read this one are complete
-                    if (step >= 2) {
-                        if (!wait_bounded(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                for (int kb = 0; kb < p.k_steps; ++kb, set ^= 1u) {
+                    // two sets of scales in Tensor Memory: the products that read this one, two
+                    // steps ago, are complete
+                    if (under_way < 2) {
+                        ++under_way;
+                    } else {
+                        if (!wait_uniform(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
                             ok = false;
                             break;
                         }
@@ -540,19 +574,19 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                             old_phase ^= 1u;
                         }
                     }
-                    if (!wait_bounded(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
+                    if (!wait_uniform(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     const uint32_t src = ring + stage * L::kStride, ssrc = src + 2 * L::kOperandBytes;
-                    const uint32_t xcol = tmem + L::kScaleCol + (uint32_t)(step & 1) * L::kScaleCols, wcol = xcol + 4 * L::kTiles;
+                    const uint32_t xcol = tmem + L::kScaleCol + set * L::kScaleCols, wcol = xcol + 4 * L::kTiles;
 #pragma unroll
                     for (int i = 0; i < L::kTiles; ++i) {
                         // w's 256 rows are eight neighbouring columns a tile of K
-                        ptx::tmem_cp_scales_pair(xcol + 4 * i, mx_scale_desc(ssrc + 512 * i));
-                        ptx::tmem_cp_scales_pair(wcol + 8 * i, mx_scale_desc(ssrc + L::kScaleBytes + 512 * i));
-                        ptx::tmem_cp_scales_pair(wcol + 8 * i + 4, mx_scale_desc(ssrc + 2 * L::kScaleBytes + 512 * i));
+                        ptx::tmem_cp_scales<2>(xcol + 4 * i, mx_scale_desc(ssrc + 512 * i), elected);
+                        ptx::tmem_cp_scales<2>(wcol + 8 * i, mx_scale_desc(ssrc + L::kScaleBytes + 512 * i), elected);
+                        ptx::tmem_cp_scales<2>(wcol + 8 * i + 4, mx_scale_desc(ssrc + 2 * L::kScaleBytes + 512 * i), elected);
                     }
                     const uint64_t xd = operand_desc<false>(src), wd = operand_desc<false>(src + L::kOperandBytes);
 #pragma unroll
@@ -560,21 +594,25 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                         constexpr int kPer = FMT == kE2M1 ? 2 : 1;  // blocks of a product
                         if (kb * mx_step_blocks(FMT) + j * kPer < p.blocks) {
                             const uint32_t byte = (uint32_t)(j * kPer) & 3u, at = (uint32_t)(j * kPer) >> 2;
-                            ptx::mma_mx_ss_pair<FMT>(d_tmem, xd + 2 * j, wd + 2 * j, idesc | (byte << 4) | (byte << 29), xcol + 4 * at,
-                                                     wcol + 8 * at, (kb | j) != 0);
+                            ptx::mma_mx<FMT, 2>(d_tmem, xd + 2 * j, wd + 2 * j, idesc | (byte << 4) | (byte << 29), xcol + 4 * at,
+                                                wcol + 8 * at, (kb | j) != 0, elected);
                         }
                     }
-                    ptx::mma_commit_pair_multicast(empty_bar(stage), 3);
+                    ptx::commit_both(empty_bar(stage), elected);
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
                 if (!ok) break;
-                ptx::mma_commit_pair_multicast(tfull_bar(acc), 3);
+                ptx::commit_both(tfull_bar(acc), elected);
             }
-            ptx::mma_commit_pair(drain_bar);
-            wait_drain(drain_bar, 0, p.wait_limit);
+            __syncwarp();
+            if (elected) {
+                ptx::mma_commit_pair(drain_bar);
+                wait_drain(drain_bar, 0, p.wait_limit);
+            }
+            __syncwarp();
         }
     } else {
         // ---------------- epilogue (both CTAs): 32 rows a warp ----------------
