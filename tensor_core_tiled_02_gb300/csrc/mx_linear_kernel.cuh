@@ -136,6 +136,7 @@ struct MxMaps {
 
 struct MxEpilogue {
     int act;
+    int wide;  // y's rows are aligned to 32 bytes
     const void *bias, *residual;
     void* y;
     long long ldr, ldy;
@@ -373,7 +374,7 @@ struct MxPairLayout {
     static constexpr int kScaleBytes = 512 * kTiles;              // 128 rows' scales of a step
     static constexpr int kStageBytes = 2 * kOperandBytes + 3 * kScaleBytes;  // x, w; scales of x's 128 rows and of all 256 of w
     static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
-    static constexpr int kWarps = 4;
+    static constexpr int kWarps = 8;     // epilogue: two for each 32 rows, on 128 columns each
     static constexpr int kThreads = 64 + 32 * kWarps;
     static constexpr int kSlots = 6;
     // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain
@@ -401,32 +402,71 @@ struct MxPairParams {
     int inject;
 };
 
-// 32 neighbouring columns of a row through the epilogue, stored.
+// Eight values of the bias, whose address is aligned to one.
 template <int DT>
-__device__ __forceinline__ void mx_finish32(const MxEpilogue& e, long long row, int n, int left, uint32_t (&v)[32]) {
+__device__ __forceinline__ uint4 bias8(const void* p, int n, int col, int cols) {
+    if (((uintptr_t)p & 15) == 0) return load8<DT>(p, n, col, cols);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (col + e < cols) w[e >> 1] |= (uint32_t)static_cast<const unsigned short*>(p)[n + e] << (16 * (e & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// 64 bytes of a row, 32 columns, those from `left` on absent (0).  Rows are 16-byte aligned.
+template <int DT>
+__device__ __forceinline__ void mx_load32(uint4 (&r)[4], const void* p, long long at, int left) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = 8 * j < left ? load8<DT>(p, at + 8 * j, 8 * j, left) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+__device__ __forceinline__ void st_global_v8(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
+                 "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
+// 32 neighbouring columns of a row through the epilogue, stored: whole sectors of 32 bytes
+// at a time where y's rows are aligned to them.
+template <int DT>
+__device__ __forceinline__ void mx_finish32(const MxEpilogue& e, long long row, int n, int left, uint32_t (&v)[32], const uint4 (&res)[4]) {
     if (e.bias != nullptr) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (i < left) v[i] = __float_as_uint(__uint_as_float(v[i]) + load1<DT>(e.bias, n + i));
+        for (int j = 0; j < 4; ++j) {
+            if (8 * j >= left) break;
+            float b[8];
+            unpack8<DT>(bias8<DT>(e.bias, n + 8 * j, 8 * j, left), b);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[8 * j + i] = __float_as_uint(__uint_as_float(v[8 * j + i]) + b[i]);
+        }
     }
     if (e.act != kActNone)
         with_act(e.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(act_value<decltype(tag)::value>(__uint_as_float(v[i])));
+            for (int i = 0; i < 32; i += 2) {
+                const float2 o = parts(act_value2<decltype(tag)::value>(f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))));
+                v[i] = __float_as_uint(o.x);
+                v[i + 1] = __float_as_uint(o.y);
+            }
         });
+    uint4 out[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        if (j * 8 >= left) break;
-        float f[8];
+        float f[8], r[8];
+        unpack8<DT>(res[j], r);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * j + i]);
-        if (e.residual != nullptr) {
-            float r[8];
-            unpack8<DT>(load8<DT>(e.residual, row * e.ldr + n + 8 * j, 8 * j, left), r);
+        for (int i = 0; i < 8; ++i) f[i] = e.residual != nullptr ? __uint_as_float(v[8 * j + i]) + r[i] : __uint_as_float(v[8 * j + i]);
+        out[j] = pack8<DT>(f);
+    }
+    const long long at = row * e.ldy + n;
+    if (e.wide && left >= 32) {
+        unsigned short* y = static_cast<unsigned short*>(e.y) + at;
+        st_global_v8(y, out[0], out[1]);
+        st_global_v8(y + 16, out[2], out[3]);
+    } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] += r[i];
-        }
-        store8(e.y, row * e.ldy + n + 8 * j, 8 * j, left, pack8<DT>(f));
+        for (int j = 0; j < 4; ++j)
+            if (8 * j < left) store8(e.y, at + 8 * j, 8 * j, left, out[j]);
     }
 }
 
@@ -465,7 +505,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             ptx::mbar_init(tfull_bar(a), 1);
             ptx::mbar_init(tempty_bar(a), 2 * L::kWarps);  // every epilogue warp of both CTAs
         }
-        ptx::mbar_init(shared_bar, 2 * L::kWarps);
+        ptx::mbar_init(shared_bar, L::kWarps);  // half of them drain the columns in question
         ptx::mbar_init(drain_bar, 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
@@ -615,8 +655,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             __syncwarp();
         }
     } else {
-        // ---------------- epilogue (both CTAs): 32 rows a warp ----------------
-        const int q = warp & 3;
+        // ---------------- epilogue (both CTAs): 32 rows x 128 columns a warp ----------------
+        const int q = warp & 3, half = (warp - 2) >> 2;
         ptx::grid_dependency_wait();
         ptx::grid_launch_dependents();
         int tl = 0;
@@ -624,27 +664,42 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             int mb, nb;
             coords(t, mb, nb);
             const int acc = tl & 1;
+            const int row = mb * 256 + (int)rank * 128 + q * 32 + lane;
+            // 64 columns at a time; those that the accumulators share, the last of the first
+            // and the first of the second, before the others
+            const bool shares = half != acc;
+            const int first = shares && acc == 0 ? 64 : 0;
+            const int n0 = nb * 256 + half * 128;
+            uint4 res[2][4];
+            auto load_residual = [&](int c) {
+                if (p.e.residual == nullptr || row >= p.M) return;
+#pragma unroll
+                for (int g = 0; g < 2; ++g) mx_load32<DT>(res[g], p.e.residual, row * p.e.ldr + n0 + c + 32 * g, p.N - (n0 + c + 32 * g));
+            };
+            load_residual(first);  // on its way while the products finish
             if (!warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
-            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond);
-            const int row = mb * 256 + (int)rank * 128 + q * 32 + lane;
-            const int n0 = nb * 256;
-            // the columns the accumulators share first: the first 64 of the second, the last of the first
+            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond + half * 128);
 #pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                const int c = acc ? i : (i + 6) & 7;
-                uint32_t v[32];
-                ptx::tmem_ld_32x32b_x32(trow + c * 32, v);
+            for (int i = 0; i < 2; ++i) {
+                const int c = i == 0 ? first : 64 - first;
+                uint32_t v[2][32];
+                ptx::tmem_ld_32x32b_x32(trow + c, v[0]);
+                ptx::tmem_ld_32x32b_x32(trow + c + 32, v[1]);
                 ptx::tmem_ld_wait();
                 // handed back only where another tile waits for it: an arrival still under way
                 // when the leader leaves would land in the shared memory of whoever follows
-                if ((i == 1 && t + pairs < tiles) || (i == 7 && t + 2 * pairs < tiles)) {
+                if ((i == 0 && shares && t + pairs < tiles) || (i == 1 && t + 2 * pairs < tiles)) {
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 1 ? shared_bar : tempty_bar(acc), 0));
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 0 ? shared_bar : tempty_bar(acc), 0));
                 }
-                const int left = p.N - (n0 + c * 32);
-                if (row < p.M && left > 0) mx_finish32<DT>(p.e, row, n0 + c * 32, left, v);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int n = n0 + c + 32 * g;
+                    if (row < p.M && n < p.N) mx_finish32<DT>(p.e, row, n, p.N - n, v[g], res[g]);
+                }
+                if (i == 0) load_residual(64 - first);
                 __syncwarp();
             }
         }

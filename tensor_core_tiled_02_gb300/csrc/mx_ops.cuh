@@ -438,6 +438,7 @@ int mx_linear(const mx_linear_args* args, gemm_stream_t stream) {
     q.e.y = a.y;
     q.e.ldr = a.ldr;
     q.e.ldy = a.ldy;
+    q.e.wide = ((uintptr_t)a.y & 31) == 0 && a.ldy % 16 == 0;
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) { return run_mx_product<decltype(fmt)::value, decltype(dt)::value>(q, c); });
 }
 
