@@ -132,11 +132,11 @@ __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, vola
 
 struct MxMaps {
     CUtensorMap x, w, xs, ws;
+    CUtensorMap y, residual;  // pairs only
 };
 
 struct MxEpilogue {
     int act;
-    int wide;  // y's rows are aligned to 32 bytes
     const void *bias, *residual;
     void* y;
     long long ldr, ldy;
@@ -376,15 +376,17 @@ struct MxPairLayout {
     static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;
     static constexpr int kWarps = 8;     // epilogue: two for each 32 rows, on 128 columns each
     static constexpr int kThreads = 64 + 32 * kWarps;
-    static constexpr int kSlots = 6;
-    // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain
-    static constexpr int kNumBars = 2 * kMaxStages + 6;
+    static constexpr int kSlots = 5;
+    static constexpr int kStaging = 4096;  // an epilogue warp's 32 rows x 64 columns
+    // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain, residual[warps]
+    static constexpr int kNumBars = 2 * kMaxStages + 6 + kWarps;
+    static constexpr int kUsed = 1024 + kSlots * kStride + kWarps * kStaging + kNumBars * 8 + 16;
     // All of an SM's shared memory, whatever is used of it, as the other kernels on pairs take
     // it: no other kernel's CTAs lie beside these.  (With 17 KB left, between norms whose CTAs
     // came to lie on the same SMs, a launch in about a thousand never ended, in none of its
     // bounded waits; why is not known.  So: none in 44,000.)
     static constexpr int kSmem = 232448;
-    static_assert(kSlots <= kMaxStages && 1024 + kSlots * kStride + kNumBars * 8 + 16 <= kSmem, "shared memory");
+    static_assert(kSlots <= kMaxStages && kUsed <= kSmem, "shared memory");
     // Tensor Memory: the accumulators overlap in kShared columns, and two steps' scales follow
     static constexpr int kScaleCols = 12 * kTiles;
     static constexpr int kSecond = 256 - 64;
@@ -413,60 +415,46 @@ __device__ __forceinline__ uint4 bias8(const void* p, int n, int col, int cols) 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// 64 bytes of a row, 32 columns, those from `left` on absent (0).  Rows are 16-byte aligned.
+// 64 neighbouring columns of a row, from x on, through the epilogue into the warp's 32-row
+// staging buffer, where the residual is.
 template <int DT>
-__device__ __forceinline__ void mx_load32(uint4 (&r)[4], const void* p, long long at, int left) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = 8 * j < left ? load8<DT>(p, at + 8 * j, 8 * j, left) : make_uint4(0u, 0u, 0u, 0u);
-}
-
-__device__ __forceinline__ void st_global_v8(void* p, const uint4& a, const uint4& b) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x),
-                 "r"(b.y), "r"(b.z), "r"(b.w)
-                 : "memory");
-}
-
-// 32 neighbouring columns of a row through the epilogue, stored: whole sectors of 32 bytes
-// at a time where y's rows are aligned to them.
-template <int DT>
-__device__ __forceinline__ void mx_finish32(const MxEpilogue& e, long long row, int n, int left, uint32_t (&v)[32], const uint4 (&res)[4]) {
+__device__ __forceinline__ void mx_finish64(const MxEpilogue& e, int x, int left, uint32_t (&v)[2][32], uint32_t buf, int lane) {
+    auto value = [&](int i) -> uint32_t& { return v[i >> 5][i & 31]; };
     if (e.bias != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             if (8 * j >= left) break;
             float b[8];
-            unpack8<DT>(bias8<DT>(e.bias, n + 8 * j, 8 * j, left), b);
+            unpack8<DT>(bias8<DT>(e.bias, x + 8 * j, 8 * j, left), b);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[8 * j + i] = __float_as_uint(__uint_as_float(v[8 * j + i]) + b[i]);
+            for (int i = 0; i < 8; ++i) fadd_bits(value(8 * j + i), __float_as_uint(b[i]));
         }
     }
     if (e.act != kActNone)
         with_act(e.act, [&](auto tag) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-                const float2 o = parts(act_value2<decltype(tag)::value>(f2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]))));
-                v[i] = __float_as_uint(o.x);
-                v[i + 1] = __float_as_uint(o.y);
+            for (int i = 0; i < 64; i += 2) {
+                const float2 o = parts(act_value2<decltype(tag)::value>(f2(__uint_as_float(value(i)), __uint_as_float(value(i + 1)))));
+                value(i) = __float_as_uint(o.x);
+                value(i + 1) = __float_as_uint(o.y);
             }
         });
-    uint4 out[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float f[8], r[8];
-        unpack8<DT>(res[j], r);
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t at = swz(buf, lane, j);
+        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = e.residual != nullptr ? __uint_as_float(v[8 * j + i]) + r[i] : __uint_as_float(v[8 * j + i]);
-        out[j] = pack8<DT>(f);
-    }
-    const long long at = row * e.ldy + n;
-    if (e.wide && left >= 32) {
-        unsigned short* y = static_cast<unsigned short*>(e.y) + at;
-        st_global_v8(y, out[0], out[1]);
-        st_global_v8(y + 16, out[2], out[3]);
-    } else {
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(value(8 * j + i));
+        if (e.residual != nullptr) {
+            uint4 w;
+            float r[8];
+            ptx::ld_shared_v4(at, w.x, w.y, w.z, w.w);
+            unpack8<DT>(w, r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (8 * j < left) store8(e.y, at + 8 * j, 8 * j, left, out[j]);
+            for (int i = 0; i < 8; ++i) f[i] += r[i];
+        }
+        const uint4 o = pack8<DT>(f);
+        ptx::st_shared_v4(at, o.x, o.y, o.z, o.w);
     }
 }
 
@@ -478,7 +466,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = ptx::smem_addr(smem_raw);
     const uint32_t ring = (raw + 1023u) & ~1023u;
-    const uint32_t bar0 = ring + S * L::kStride;
+    const uint32_t staging = ring + S * L::kStride;
+    const uint32_t bar0 = staging + L::kWarps * L::kStaging;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (bar0 - raw) + 8 * L::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 #ifdef TCGEMM_CHECK
@@ -492,6 +481,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
     auto tfull_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + a); };
     auto tempty_bar = [&](int a) { return bar0 + 8u * (2 * kMaxStages + 2 + a); };
     const uint32_t shared_bar = bar0 + 8u * (2 * kMaxStages + 4), drain_bar = shared_bar + 8u;
+    auto residual_bar = [&](int w) { return drain_bar + 8u * (1 + w); };
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();  // 0 issues the MMAs
@@ -507,6 +497,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
         }
         ptx::mbar_init(shared_bar, L::kWarps);  // half of them drain the columns in question
         ptx::mbar_init(drain_bar, 1);
+        for (int w = 0; w < L::kWarps; ++w) ptx::mbar_init(residual_bar(w), 1);
         *abort_flag = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm.x);
@@ -656,33 +647,47 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
         }
     } else {
         // ---------------- epilogue (both CTAs): 32 rows x 128 columns a warp ----------------
-        const int q = warp & 3, half = (warp - 2) >> 2;
+        const int ew = warp - 2, q = warp & 3, half = ew >> 2;
+        const uint32_t buf = staging + (uint32_t)(ew * L::kStaging), bar = residual_bar(ew);
+        const int n8 = p.N & ~7;   // columns that y's tensor map holds (store_tail)
         ptx::grid_dependency_wait();
         ptx::grid_launch_dependents();
+        bool pending = false;      // a load of the residual into buf is under way
+        uint32_t loads = 0;        // and how many were before it
         int tl = 0;
-        for (int t = pair; t < tiles; t += pairs, ++tl) {
+        bool ok = TC_CHECK(holds(staging, L::kWarps * L::kStaging, buf, L::kStaging), kSiteSmemBounds);
+        for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
             int mb, nb;
             coords(t, mb, nb);
             const int acc = tl & 1;
-            const int row = mb * 256 + (int)rank * 128 + q * 32 + lane;
+            const int row0 = mb * 256 + (int)rank * 128 + q * 32;
             // 64 columns at a time; those that the accumulators share, the last of the first
             // and the first of the second, before the others
             const bool shares = half != acc;
             const int first = shares && acc == 0 ? 64 : 0;
             const int n0 = nb * 256 + half * 128;
-            uint4 res[2][4];
-            auto load_residual = [&](int c) {
-                if (p.e.residual == nullptr || row >= p.M) return;
-#pragma unroll
-                for (int g = 0; g < 2; ++g) mx_load32<DT>(res[g], p.e.residual, row * p.e.ldr + n0 + c + 32 * g, p.N - (n0 + c + 32 * g));
+            // the buffer is free once its last store has read it; then, where there is a
+            // residual, its 32 x 64 values go there
+            auto prepare = [&](int x) {
+                if (row0 >= p.M || x >= p.N) return;
+                if (lane == 0) {
+                    ptx::bulk_wait_group_read<0>();
+                    if (p.e.residual != nullptr) {
+                        ptx::mbar_arrive_expect_tx(bar, L::kStaging);
+                        ptx::tma_load_2d(buf, &tm.residual, bar, x, row0);
+                    }
+                }
+                pending = p.e.residual != nullptr;
+                __syncwarp();
             };
-            load_residual(first);  // on its way while the products finish
+            prepare(n0 + first);
             if (!warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
             const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond + half * 128);
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
-                const int c = i == 0 ? first : 64 - first;
+                const int c = i == 0 ? first : 64 - first, x = n0 + c;
+                if (i == 1) prepare(x);
                 uint32_t v[2][32];
                 ptx::tmem_ld_32x32b_x32(trow + c, v[0]);
                 ptx::tmem_ld_32x32b_x32(trow + c + 32, v[1]);
@@ -694,15 +699,31 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 0 ? shared_bar : tempty_bar(acc), 0));
                 }
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int n = n0 + c + 32 * g;
-                    if (row < p.M && n < p.N) mx_finish32<DT>(p.e, row, n, p.N - n, v[g], res[g]);
+                if (row0 >= p.M || x >= p.N) continue;
+                if (pending) {
+                    ok = warp_wait(bar, loads & 1, abort_flag, p.wait_limit, kSiteAuxLoad, lane);
+                    if (!ok) break;
+                    ++loads;
+                    pending = false;
                 }
-                if (i == 0) load_residual(64 - first);
+                mx_finish64<DT>(p.e, x, p.N - x, v, buf, lane);
+                if (n8 < p.N && n8 < x + 64 && row0 + lane < p.M)
+                    store_tail(swz(buf, lane, (n8 - x) >> 3), p.e.y, (row0 + lane) * p.e.ldy + n8, p.N - n8);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0 && x < n8) {
+                    ptx::tma_store_2d(&tm.y, buf, x, row0);
+                    ptx::bulk_commit_group();
+                }
                 __syncwarp();
             }
         }
+        if (lane == 0) {
+            // after an abort: a load under way lands before shared memory goes away
+            if (pending) wait_drain(bar, loads & 1, p.wait_limit);
+            ptx::bulk_wait_group_read<0>();
+        }
+        __syncwarp();
     }
     ptx::tc_fence_before();
     __syncthreads();

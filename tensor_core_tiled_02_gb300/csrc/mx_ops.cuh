@@ -207,6 +207,9 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
     using L = MxPairLayout<FMT>;
     MxMaps tm;
     int rc = encode_mx(&tm, q, 128);
+    constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
+    if (rc == GEMM_OK) rc = encode_out(&tm.y, mat16(q.e.y, q.x.rows, q.w.rows, q.e.ldy), dtype, 32);
+    if (rc == GEMM_OK && q.e.residual) rc = encode_mat(&tm.residual, mat16(q.e.residual, q.x.rows, q.w.rows, q.e.ldr), dtype, 64, 32);
     if (rc != GEMM_OK) return rc;
     MxPairParams p;
     std::memset(&p, 0, sizeof(p));
@@ -438,7 +441,6 @@ int mx_linear(const mx_linear_args* args, gemm_stream_t stream) {
     q.e.y = a.y;
     q.e.ldr = a.ldr;
     q.e.ldy = a.ldy;
-    q.e.wide = ((uintptr_t)a.y & 31) == 0 && a.ldy % 16 == 0;
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) { return run_mx_product<decltype(fmt)::value, decltype(dt)::value>(q, c); });
 }
 
