@@ -58,8 +58,9 @@ int run_norm(NormParams p, const Ctx& c) {
     const int vectors = ceil_div(p.dim, 8);
     if (vectors > 8 * 1024)
         return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
-    int v = 1;
-    while (v < 8 && (p.tokens > 2 * c.dev->sms ? vectors > 128 * v : vectors > 1024 * v)) v *= 2;
+    // few rows: one vector a thread, for the least latency; many: four, for bytes under way
+    int v = p.tokens > 2 * c.dev->sms ? (vectors > 256 ? 4 : vectors > 64 ? 2 : 1) : 1;
+    while (vectors > 1024 * v) v *= 2;
     p.group = ceil_div(ceil_div(vectors, v), 32) * 32;
     const int threads = p.group == 32 ? 128 : p.group;
     switch (v) {
@@ -71,41 +72,46 @@ int run_norm(NormParams p, const Ctx& c) {
 }
 
 struct NormGradPlan {
-    int threads, v, blocks;
-    bool long_rows;
+    int threads, blocks;
     size_t bytes;
 };
 
-constexpr int kNormGradRows = 4;
-
+// Two vectors of eight columns a thread; blocks such that some 800 threads run on an SM, with
+// few threads more rows at a time instead.
 NormGradPlan norm_grad_plan(const rms_norm_grad_args& a) {
     NormGradPlan g{};
     const int vectors = ceil_div(a.dim, 8);
-    g.v = vectors > 512 ? 2 : 1;
-    g.threads = ceil_div(ceil_div(vectors, g.v), 32) * 32;
-    g.long_rows = vectors > 2048;
-    const long long most = ceil_div(a.tokens, kNormGradRows);
-    g.blocks = most < kNormPartials ? (int)most : kNormPartials;
-    g.bytes = a.dweight ? align256((size_t)g.blocks * a.dim * 4) : 0;
+    g.threads = vectors > 2048 ? 0 : ceil_div(ceil_div(vectors, 2), 32) * 32;  // 0: long rows
+    const int rows = g.threads > 128 ? 1 : g.threads > 64 ? 2 : 4;
+    const int per_sm = g.threads > 512 ? 1 : g.threads > 256 ? 2 : g.threads > 128 ? 3 : 4;
+    const long long most = ceil_div(a.tokens, rows);
+    g.blocks = most < per_sm * kNormSms ? (int)most : per_sm * kNormSms;
+    g.bytes = a.dweight ? align256((size_t)g.blocks * pad8(a.dim) * 4) : 0;
     return g;
 }
 
 template <int DT>
 int run_norm_grad(const NormGradParams& p, const NormGradPlan& g, void* dweight, const Ctx& c) {
     int rc = GEMM_OK;
-    if (g.long_rows) {
+    auto rows = [&](auto kern) { return launch_pdl(kern, dim3(g.blocks), g.threads, 0, 1, c.stream, p); };
+    if (g.threads == 0) {
         // the column sums first: dx may be written over dy
         if (dweight)
             rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, 0, 1, c.stream, p);
         if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
-    } else if (g.v == 1) {
-        rc = launch_pdl(rms_norm_grad_kernel<DT, 1, kNormGradRows>, dim3(g.blocks), g.threads, 0, 1, c.stream, p);
+    } else if (g.threads > 512) {
+        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 1024, 1>);
+    } else if (g.threads > 256) {
+        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 512, 2>);
+    } else if (g.threads > 128) {
+        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 256, 3>);
+    } else if (g.threads > 64) {
+        rc = rows(rms_norm_grad_kernel<DT, 2, 2, 128, 4>);
     } else {
-        rc = launch_pdl(rms_norm_grad_kernel<DT, 2, kNormGradRows>, dim3(g.blocks), g.threads, 0, 1, c.stream, p);
+        rc = rows(rms_norm_grad_kernel<DT, 2, 4, 64, 4>);
     }
     if (rc == GEMM_OK && dweight)
-        rc = launch_pdl(rms_norm_weight_sum_kernel<DT>, dim3(ceil_div(p.dim, 32)), 1024, 0, 1, c.stream, (const float*)p.partial,
-                        dweight, g.blocks, p.dim);
+        rc = launch_pdl(rms_norm_weight_sum_kernel<DT>, dim3(ceil_div(p.dim, 32)), 1024, 0, 1, c.stream, p, dweight, g.blocks);
     return rc;
 }
 

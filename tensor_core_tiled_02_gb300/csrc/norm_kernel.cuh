@@ -158,21 +158,28 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p)
 
 // ---- gradients ---------------------------------------------------------------------------
 
-constexpr int kNormPartials = 608;  // most partial sums of dweight: four blocks an SM
+constexpr int kNormSms = 152;  // partial sums of dweight: one a block, one to four blocks an SM
 
 struct NormGradParams {
     const void *dy, *h, *weight, *dh;
     const float* rstd;
     void* dx;
-    float* partial;    // [gridDim.x][dim], NULL where dweight is not wanted
+    float* partial;    // rows of pitch() sums, one a block; NULL where dweight is not wanted
     long long lddy, ldh, lddh, lddx;
     int tokens, dim;
+    __host__ __device__ size_t pitch() const { return ((size_t)dim + 7) & ~(size_t)7; }
 };
 
-// A block's threads share the columns, V vectors of eight each, and walk over the rows,
-// R at a time, their share of dweight in registers.
-template <int DT, int V, int R>
-__global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(const NormGradParams p) {
+__device__ __forceinline__ void store_sums(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// A block's threads share the columns, V vectors of eight each, and walk over the rows, R
+// at a time with all their loads under way, their share of dweight in registers.  Several
+// blocks an SM, one's loads under another's sums over its row.
+template <int DT, int V, int R, int THREADS, int BLOCKS>
+__global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_grad_kernel(const NormGradParams p) {
     __shared__ float sums[2][32][R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     ptx::grid_dependency_wait();
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(cons
     }
     int set = 0;
     for (long long base = (long long)blockIdx.x * R; base < p.tokens; base += (long long)gridDim.x * R, set ^= 1) {
-        uint4 g[V][R], h[V][R];
+        uint4 g[V][R], h[V][R], e[V][R];
         float rstd[R], dot[R];
 #pragma unroll
         for (int u = 0; u < R; ++u) {
@@ -198,8 +205,12 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(cons
             for (int j = 0; j < V; ++j) {
                 const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
                 const bool here = col < p.dim && row < p.tokens;
-                g[j][u] = here ? load8<DT>(p.dy, row * p.lddy + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
-                h[j][u] = here ? load8<DT>(p.h, row * p.ldh + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+                g[j][u] = h[j][u] = e[j][u] = make_uint4(0u, 0u, 0u, 0u);
+                if (here) {
+                    g[j][u] = load8<DT>(p.dy, row * p.lddy + col, col, p.dim);
+                    h[j][u] = load8<DT>(p.h, row * p.ldh + col, col, p.dim);
+                    if (p.dh != nullptr) e[j][u] = load8<DT>(p.dh, row * p.lddh + col, col, p.dim);
+                }
             }
         }
 #pragma unroll
@@ -238,12 +249,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(cons
                 unpack8<DT>(g[j][u], a);
                 unpack8<DT>(h[j][u], b);
                 unpack8<DT>(w[j], c);
-                if (p.dh != nullptr) {
-                    unpack8<DT>(load8<DT>(p.dh, row * p.lddh + col, col, p.dim), d);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) d[i] = 0.0f;
-                }
+                unpack8<DT>(e[j][u], d);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) d[i] += fmaf(a[i] * c[i], rstd[u], -b[i] * back);
                 store8(p.dx, row * p.lddx + col, col, p.dim, pack8<DT>(d));
@@ -254,9 +260,7 @@ __global__ void __launch_bounds__(V == 1 ? 512 : 1024) rms_norm_grad_kernel(cons
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (col + i < p.dim) p.partial[(size_t)blockIdx.x * p.dim + col + i] = dw[j][i];
+        if (col < p.dim) store_sums(p.partial + blockIdx.x * p.pitch() + col, dw[j]);
     }
 }
 
@@ -320,30 +324,34 @@ __global__ void __launch_bounds__(256) rms_norm_grad_columns_kernel(const NormGr
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[i] = fmaf(a[i] * b[i], rstd, dw[i]);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (col + i < p.dim) p.partial[(size_t)blockIdx.y * p.dim + col + i] = dw[i];
+    store_sums(p.partial + blockIdx.y * p.pitch() + col, dw);
 }
 
-// dweight[c] = sum of partial[b][c], rounded once: 32 columns a block, 32 slices of the
-// partials side by side.
+// dweight[c] = sum over blocks of their sums of column c, rounded once: 32 columns a block
+// (a warp reads 128 bytes), 32 slices of the partials side by side, eight reads under way.
 template <int DT>
-__global__ void __launch_bounds__(1024) rms_norm_weight_sum_kernel(const float* partial, void* out, int blocks, int cols) {
+__global__ void __launch_bounds__(1024) rms_norm_weight_sum_kernel(const NormGradParams p, void* out, int blocks) {
     __shared__ float sums[32][33];
     const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
     const long long c = blockIdx.x * 32ll + lane;
+    const size_t pitch = p.pitch();
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     float s = 0.0f;
-    if (c < cols) {
-#pragma unroll 4
-        for (int b = slice; b < blocks; b += 32) s += partial[(size_t)b * cols + c];
+    if (c < p.dim) {
+        for (int b = slice; b < blocks; b += 256) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = b + 32 * i < blocks ? __ldcg(p.partial + (b + 32 * i) * pitch + c) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
     }
     sums[slice][lane] = s;
     __syncthreads();
     s = warp_sum(sums[lane][slice]);
     const long long mine = blockIdx.x * 32ll + slice;
-    if (lane == 0 && mine < cols) static_cast<unsigned short*>(out)[mine] = pack1<DT>(s);
+    if (lane == 0 && mine < p.dim) static_cast<unsigned short*>(out)[mine] = pack1<DT>(s);
 }
 
 }  // namespace tcgemm
