@@ -102,15 +102,24 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
     return byte == 0u ? __uint_as_float(0x00400000u) : byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
-// Four lanes hold a block of 32 values between them, eight each, sixteen lanes four
-// blocks: stores the lane's eight at `data` (of its own eight; skipped where the block
-// does not exist) and, from the first of the sixteen, their four scales at `word`.
-// Every lane of the warp calls this.
+// The larger of two magnitudes in each half of two words of 16-bit values: their bits
+// without the sign are ordered as whole numbers, NaN above infinity.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7FFF7FFFu); }
+
+// The larger half of such a word as an fp32's bits.
+template <int DT>
+__device__ __forceinline__ uint32_t max_half_bits(uint32_t m) {
+    const uint32_t one = max(m & 0xFFFFu, m >> 16);
+    if constexpr (DT == kBF16) return one << 16;
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)one)));
+}
+
+// Four lanes hold a block of 32 values between them, eight each, m the bits of the largest
+// magnitude of this lane's; sixteen lanes hold four blocks.  Stores the lane's eight at
+// `data` (skipped where the block does not exist) and, from the first of the sixteen, their
+// four scales at `word`.  Every lane of the warp calls this.
 template <int FMT>
-__device__ __forceinline__ void mx_store8(const float (&f)[8], uint8_t* data, bool in_block, uint32_t* word, bool in_word) {
-    uint32_t m = abs_bits(f[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = max(m, abs_bits(f[i]));
+__device__ __forceinline__ void mx_store8(const float (&f)[8], uint32_t m, uint8_t* data, bool in_block, uint32_t* word, bool in_word) {
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t byte = mx_scale_byte<FMT>(m);

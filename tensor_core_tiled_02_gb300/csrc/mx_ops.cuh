@@ -379,14 +379,14 @@ int mx_quantize(const mx_quantize_args* args, gemm_stream_t stream) {
     p.ldd = a.ldd;
     p.rows = (int)a.rows;
     p.cols = (int)a.cols;
-    p.groups = ceil_div(a.cols, 256);
+    p.groups = ceil_div(a.cols, a.transpose ? 128 : 256);
     const long long blocks = (long long)p.groups * ceil_div(a.rows, a.transpose ? 128 : 8 * kMxQuantRows);
     if (blocks > INT_MAX) return GEMM_ERR_DIM;
     Ctx c;
     if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
         constexpr int DT = decltype(dt)::value, FMT = decltype(fmt)::value;
-        return a.transpose ? launch_pdl(mx_quantize_columns_kernel<DT, FMT>, dim3((unsigned)blocks), 128, 0, 1, c.stream, p)
+        return a.transpose ? launch_pdl(mx_quantize_columns_kernel<DT, FMT>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p)
                            : launch_pdl(mx_quantize_kernel<DT, FMT>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p);
     });
 }

@@ -39,63 +39,77 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
         unpack8<DT>(v[u], f);
         uint8_t* data = p.data + row * p.ldd + (FMT == kE4M3 ? col : col >> 1);
         uint32_t* word = p.scale + (mx_scale_word(row, col >> 7, k_tiles) >> 2);
-        mx_store8<FMT>(f, data, col < ((p.cols + 31) & ~31), word, (col >> 7) < k_tiles);
+        const uint32_t m2 = max_abs2(max_abs2(max_abs2(v[u].x & 0x7FFF7FFFu, v[u].y), v[u].z), v[u].w);
+        mx_store8<FMT>(f, max_half_bits<DT>(m2), data, col < ((p.cols + 31) & ~31), word, (col >> 7) < k_tiles);
     }
 }
 
-// Along the columns, result [cols, rows]: a thread has two neighbouring columns and 128
-// rows of them, a block of 32 at a time, so that a block never leaves its registers and a
-// warp reads 128 bytes of each row.
+// Along the columns, result [cols, rows]: a CTA has 128 rows x 128 columns, a thread two
+// neighbouring columns of 32 rows, so that a block never leaves its registers and a warp
+// reads 128 bytes of each row.  A column's four blocks meet in shared memory, from where
+// they go out side by side, 64 or 128 bytes.
 template <int DT, int FMT>
-__global__ void __launch_bounds__(128) mx_quantize_columns_kernel(const MxQuantParams p) {
+__global__ void __launch_bounds__(256) mx_quantize_columns_kernel(const MxQuantParams p) {
+    constexpr int kBytes = mx_block_bytes(FMT), kPieces = 4 * kBytes / 16;  // 16-byte pieces of a column
+    __shared__ uint4 out[128][kPieces + 1];
+    __shared__ __align__(4) uint8_t bytes[128][4];
     const long long group = blockIdx.x % p.groups, tile = blockIdx.x / p.groups;
-    const long long col = (group * 128 + threadIdx.x) * 2;
+    const int lane = threadIdx.x & 31, b = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+    const int c0 = half * 64 + lane * 2;
+    const long long col = group * 128 + c0, r0 = tile * 128 + b * 32;
     const int k_tiles = (p.rows + 127) >> 7;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    if (col >= p.cols) return;
-    const bool two = col + 1 < p.cols;
-    const unsigned short* src = static_cast<const unsigned short*>(p.x) + col;
-    uint32_t words[2] = {0u, 0u};
-#pragma unroll 1
-    for (int b = 0; b < 4; ++b) {
-        const long long r0 = tile * 128 + b * 32;
-        if (r0 >= p.rows) break;
-        uint32_t v[32];
+    const bool one = col < p.cols, two = col + 1 < p.cols;
+    const unsigned short* src = static_cast<const unsigned short*>(p.x) + r0 * p.ldx + col;
+    uint32_t v[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            v[i] = 0u;
-            if (r0 + i < p.rows)
-                v[i] = two ? *reinterpret_cast<const uint32_t*>(src + (r0 + i) * p.ldx) : (uint32_t)src[(r0 + i) * p.ldx];
-        }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float f[4][8];
-            uint32_t m = 0u;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float2 pair = unpack2<DT>(v[i]);
-                f[i >> 3][i & 7] = c == 0 ? pair.x : pair.y;
-                m = max(m, abs_bits(f[i >> 3][i & 7]));
-            }
-            if (c == 1 && !two) break;
-            const uint32_t byte = mx_scale_byte<FMT>(m);
-            const float un = mx_unscale(byte);
-            words[c] |= byte << (8 * b);
-            uint32_t* d = reinterpret_cast<uint32_t*>(p.data + (col + c) * p.ldd + (r0 >> 5) * mx_block_bytes(FMT));
-            uint2 q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[i] = mx_pack8<FMT>(f[i], un);
-            if constexpr (FMT == kE4M3) {
-                reinterpret_cast<uint4*>(d)[0] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
-                reinterpret_cast<uint4*>(d)[1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
-            } else {
-                reinterpret_cast<uint4*>(d)[0] = make_uint4(q[0].x, q[1].x, q[2].x, q[3].x);
-            }
+    for (int i = 0; i < 32; ++i) {
+        v[i] = 0u;
+        if (r0 + i < p.rows) {
+            if (two)
+                v[i] = *reinterpret_cast<const uint32_t*>(src + i * p.ldx);
+            else if (one)
+                v[i] = src[i * p.ldx];
         }
     }
-    p.scale[mx_scale_word(col, tile, k_tiles) >> 2] = words[0];
-    if (two) p.scale[mx_scale_word(col + 1, tile, k_tiles) >> 2] = words[1];
+    uint32_t m2 = 0u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m2 = max_abs2(m2, v[i]);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const uint32_t byte = mx_scale_byte<FMT>(max_half_bits<DT>(c == 0 ? m2 & 0xFFFFu : m2 >> 16));
+        const float un = mx_unscale(byte);
+        bytes[c0 + c][b] = (uint8_t)byte;
+        uint2 q[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 pair = unpack2<DT>(v[8 * j + i]);
+                f[i] = c == 0 ? pair.x : pair.y;
+            }
+            q[j] = mx_pack8<FMT>(f, un);
+        }
+        if constexpr (FMT == kE4M3) {
+            out[c0 + c][2 * b] = make_uint4(q[0].x, q[0].y, q[1].x, q[1].y);
+            out[c0 + c][2 * b + 1] = make_uint4(q[2].x, q[2].y, q[3].x, q[3].y);
+        } else {
+            out[c0 + c][b] = make_uint4(q[0].x, q[1].x, q[2].x, q[3].x);
+        }
+    }
+    __syncthreads();
+    // pieces of rows that exist: up to the end of the last block
+    const int pieces = (int)min((long long)kPieces, ((p.rows + 31ll) / 32 - tile * 4) * (kBytes / 16));
+#pragma unroll
+    for (int i = threadIdx.x; i < 128 * kPieces; i += 256) {
+        const int c = i / kPieces, piece = i % kPieces;
+        if (group * 128 + c < p.cols && piece < pieces)
+            *reinterpret_cast<uint4*>(p.data + (group * 128 + c) * p.ldd + tile * (4 * kBytes) + piece * 16) = out[c][piece];
+    }
+    if (threadIdx.x < 128 && group * 128 + threadIdx.x < p.cols)
+        p.scale[mx_scale_word(group * 128 + threadIdx.x, tile, k_tiles) >> 2] = *reinterpret_cast<const uint32_t*>(bytes[threadIdx.x]);
 }
 
 struct MxValuesParams {

@@ -59,7 +59,10 @@ __device__ __forceinline__ void norm_store(const NormParams& p, int row, int col
         const int k_tiles = (p.dim + 127) >> 7;
         uint32_t* word = p.scale + (mx_scale_word(row, col >> 7, k_tiles) >> 2);
         uint8_t* data = p.data + row * p.ldd + (kFmt == kE4M3 ? col : col >> 1);
-        mx_store8<kFmt>(f, data, col < ((p.dim + 31) & ~31), word, (col >> 7) < k_tiles);
+        uint32_t m = abs_bits(f[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = max(m, abs_bits(f[i]));
+        mx_store8<kFmt>(f, m, data, col < ((p.dim + 31) & ~31), word, (col >> 7) < k_tiles);
     }
 }
 

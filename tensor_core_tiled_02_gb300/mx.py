@@ -47,14 +47,19 @@ def _mx(a, name):
     return a
 
 
-def _dtype(dtype):
-    import torch
+_DTYPES = {None: 1}  # and torch's two, once torch is there
 
-    if dtype is torch.bfloat16:
-        return 1
-    if dtype is torch.float16:
-        return 0
-    raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype!r}")
+
+def _dtype(dtype):
+    try:
+        return _DTYPES[dtype]
+    except (KeyError, TypeError):
+        import torch
+
+        _DTYPES.update({torch.float16: 0, torch.bfloat16: 1})
+        if dtype is torch.float16 or dtype is torch.bfloat16:
+            return _DTYPES[dtype]
+        raise ValueError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype!r}") from None
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, save=False, out=None, h_out=None, stream=None):
@@ -78,7 +83,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, save=False, out=None, h_out=Non
 def rms_norm_mx(x, weight, format="e4m3", residual=None, eps=1e-6, h_out=None, stream=None):
     """``rms_norm`` with y as an ``Mx`` of ``format``, rounded once: y, or with ``residual`` (y, h)."""
     data, scale, h, _ = _call("rms_norm", stream, x, x, weight, residual, eps, _format(format), False, None, h_out)
-    y = Mx(data, scale, x.shape[1], format)
+    y = Mx(data, scale, x.size(1), format)
     return y if residual is None else (y, h if h_out is None else h_out)
 
 
@@ -102,17 +107,14 @@ def mx_quantize(x, format="e2m1", transpose=False, stream=None):
     takes it becomes ``mx_linear``'s by ``transpose``, blocks along ``in``.
     """
     data, scale = _call("mx_quantize", stream, x, x, _format(format), bool(transpose))
-    return Mx(data, scale, x.shape[0 if transpose else 1], format)
+    return Mx(data, scale, x.size(0 if transpose else 1), format)
 
 
 def mx_dequantize(a, dtype=None, stream=None):
     """The values of an ``Mx`` as fp16 or bf16 (the default), which hold them exactly if
     ``mx_quantize`` made them of that type."""
-    import torch
-
     data, scale, cols, format = _mx(a, "a")
-    return _call("mx_dequantize", stream, data, data, scale, cols, _format(format),
-                 _dtype(torch.bfloat16 if dtype is None else dtype))
+    return _call("mx_dequantize", stream, data, data, scale, cols, _format(format), _dtype(dtype))
 
 
 def mx_linear(x, w, bias=None, act=None, residual=None, dtype=None, out=None, stream=None):
@@ -126,11 +128,9 @@ def mx_linear(x, w, bias=None, act=None, residual=None, dtype=None, out=None, st
     ``dx = mx_linear(mx_quantize(dy), mx_quantize(w))`` and
     ``dw = mx_linear(mx_quantize(x, transpose=True), mx_quantize(dy, transpose=True))``.
     """
-    import torch
-
     data, scale, cols, format = _mx(x, "x")
     w_data, w_scale, w_cols, w_format = _mx(w, "w")
     if cols != w_cols or format != w_format:
         raise ValueError(f"x is [.., {cols}] {format}, w [.., {w_cols}] {w_format}")
     return _call("mx_linear", stream, data, data, scale, w_data, w_scale, cols, _format(format), bias, _act(act), residual,
-                 _dtype(torch.bfloat16 if dtype is None else dtype), out)
+                 _dtype(dtype), out)
