@@ -143,8 +143,9 @@ PyObject* wrap(const at::Tensor& t) {
     return THPVariable_Wrap(t);
 }
 
-PyObject* wrap_all(std::initializer_list<at::Tensor> ts) {
-    PyObject* out = PyTuple_New((Py_ssize_t)ts.size());
+// with n >= 0: the tensors and n
+PyObject* wrap_all(std::initializer_list<at::Tensor> ts, int64_t n = -1) {
+    PyObject* out = PyTuple_New((Py_ssize_t)ts.size() + (n >= 0));
     if (!out) return nullptr;
     Py_ssize_t i = 0;
     for (const at::Tensor& t : ts) {
@@ -154,6 +155,14 @@ PyObject* wrap_all(std::initializer_list<at::Tensor> ts) {
             return nullptr;
         }
         PyTuple_SET_ITEM(out, i++, o);
+    }
+    if (n >= 0) {
+        PyObject* o = PyLong_FromLongLong(n);
+        if (!o) {
+            Py_DECREF(out);
+            return nullptr;
+        }
+        PyTuple_SET_ITEM(out, i, o);
     }
     return out;
 }
@@ -603,7 +612,7 @@ int64_t checked_cols(PyObject* o) {
 at::ScalarType type_of(PyObject* o) { return integer(o) == LAYER_BF16 ? at::kBFloat16 : at::kHalf; }
 
 // (x, weight, residual, eps, format or None, save, out, h_out) -> (y, h or None, rstd or None),
-// or with a format (data, scale, h or None, rstd or None)
+// or with a format (data, scale, h or None, rstd or None, dim)
 PyObject* py_norm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     return guarded(v, nargs, 8, [&]() -> PyObject* {
         const at::Tensor& x = Call::checked(tensor(v[0], "x"), "x");
@@ -661,7 +670,7 @@ PyObject* py_norm(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
         if (rc != 0) return PyLong_FromLong(rc);
         if (v[6] != Py_None) wrote(y);
         if (v[7] != Py_None) wrote(h);
-        return scaled ? wrap_all({m.data, m.scale, h, rstd}) : wrap_all({y, h, rstd});
+        return scaled ? wrap_all({m.data, m.scale, h, rstd}, dim) : wrap_all({y, h, rstd});
     });
 }
 
@@ -717,7 +726,7 @@ PyObject* py_norm_backward(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     });
 }
 
-// (x, format, transpose) -> (data, scale)
+// (x, format, transpose) -> (data, scale, cols)
 PyObject* py_quantize(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
     return guarded(v, nargs, 3, [&]() -> PyObject* {
         const at::Tensor& x = Call::on_cuda(Call::checked(tensor(v[0], "x"), "x"), "x");
@@ -737,7 +746,7 @@ PyObject* py_quantize(PyObject*, PyObject* const* v, Py_ssize_t nargs) {
         a.dtype = type_code(c.type);
         const int rc = abi.quantize(&a, c.stream);
         if (rc != 0) return PyLong_FromLong(rc);
-        return wrap_all({m.data, m.scale});
+        return wrap_all({m.data, m.scale}, cols);
     });
 }
 

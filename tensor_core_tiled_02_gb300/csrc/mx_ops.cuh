@@ -163,6 +163,7 @@ struct MxSkinnyPlan {
 MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
     MxSkinnyPlan g{};
     const int fmt = q.x.fmt;
+    // tokens from multiples of 128 on: there the tiles of their scales begin
     g.t_tiles = ceil_div(q.x.rows, 128);
     g.nt = g.t_tiles > 1 ? 128 : ceil_div(q.x.rows, 16) * 16;
     g.tiles = ceil_div(q.w.rows, 128) * g.t_tiles;
@@ -171,13 +172,44 @@ MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
     g.scale_col = (g.nt + 31) / 32 * 32;
     const int cols = g.scale_col + 16 * mx_step_tiles(fmt);
     g.tmem_cols = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    // Split along K until two SMs in three are busy, or four in five while a CTA still has
+    // more than 24 steps (one token, K = 4096, N = 14336: 112 and 224 CTAs 7.9 and 8.5 us in
+    // 4 bits, 16 steps; 13.2 and 12.9 in 8 bits, 32).
     g.split = 1;
-    for (int s = 2; s <= kMaxSplit && 2 * s <= g.k_steps && g.tiles * g.split < sms * 4 / 5; ++s) g.split = s;
+    for (int s = 2; s <= kMaxSplit && 2 * s <= g.k_steps; ++s) {
+        if (g.tiles * g.split >= (ceil_div(g.k_steps, g.split) > 24 ? sms * 4 / 5 : sms * 2 / 3)) break;
+        g.split = s;
+    }
+    // Two CTAs fill an SM, so that the next launch's find room beside this one's (one token,
+    // K = N = 4096, 8 bits: 6.5 us, 7.2 with the whole SM).  Larger tiles take all of it where
+    // each has an SM to itself, for a ring of more than three steps (128 tokens, the same: 11.7
+    // and 10.8); not in clusters of more than four, of which few fit at once.
     const int fixed = 1024 + 8 * (2 * kMxSkinnySlots + 1) + 16;
-    g.slots = (kSkinnyTwoSmem - fixed) / g.stage_bytes;
+    g.smem = g.nt > 48 && g.tiles * g.split <= sms && g.split <= 4 ? kSmemLimit : kSkinnyTwoSmem;
+    g.slots = (g.smem - fixed) / g.stage_bytes;
     if (g.slots > kMxSkinnySlots) g.slots = kMxSkinnySlots;
-    g.smem = kSkinnyTwoSmem;  // two CTAs fill an SM
     return g;
+}
+
+// Nanoseconds a product is expected to take, to choose between the kernels.  A CTA of the one
+// for few tokens takes in 110 bytes a nanosecond, two on an SM 1.5 times that; 28 ns a token
+// for its way through shared memory.  A pair takes 310 a step of a tile.  HBM gives 6,500
+// bytes.  (192 products of 32 to 768 tokens, K from 1024 and N from 2048 to 14336, either
+// format: the choice costs 0.4 % on average and 11 % at worst against the better of the two.)
+long long mx_skinny_ns(const MxSkinnyPlan& g, int sms, long long bytes) {
+    const long long ctas = (long long)g.tiles * g.split, full = ctas / (2 * sms), rest = ctas % (2 * sms);
+    const long long halves = 3 * full + (rest > sms ? 3 : rest > 0 ? 2 : 0);  // in units of half a lone CTA's time
+    const long long steps = 3700 + 28 * g.nt + halves * ceil_div(g.k_steps, g.split) * g.stage_bytes / 220;
+    const long long memory = 3500 + bytes * 10 / 65000;
+    return steps > memory ? steps : memory;
+}
+
+long long mx_pair_ns(const MxProduct& q, int pairs, int k_steps, long long bytes) {
+    const long long tiles = (long long)ceil_div(q.x.rows, 256) * ceil_div(q.w.rows, 256);
+    const long long waves = (tiles + pairs - 1) / pairs;
+    const long long steps = 4500 + waves * k_steps * 310 + (waves - 1) * 1800;
+    const long long memory = 4500 + bytes * 10 / 65000;
+    return steps > memory ? steps : memory;
 }
 
 template <int FMT, int DT>
@@ -241,7 +273,12 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
 
 template <int FMT, int DT>
 int run_mx_product(const MxProduct& q, const Ctx& c) {
-    if (q.x.rows <= 256) return run_mx_skinny<FMT, DT>(q, mx_skinny_plan(q, c.dev->sms), c);
+    if (q.x.rows <= kFewTokens) {
+        const MxSkinnyPlan g = mx_skinny_plan(q, c.dev->sms);
+        const long long bytes = q.w.rows * mx_width(q.w) + q.x.rows * (mx_width(q.x) + 2 * q.w.rows);
+        if (mx_skinny_ns(g, c.dev->sms, bytes) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps, bytes))
+            return run_mx_skinny<FMT, DT>(q, g, c);
+    }
     return run_mx_pair<FMT, DT>(q, c);
 }
 

@@ -34,6 +34,9 @@ class Mx(NamedTuple):
     format: str
 
 
+_new = tuple.__new__  # an Mx of four values, without its constructor's steps
+
+
 def _format(format):
     code = FORMATS.get(format) if isinstance(format, str) else None
     if code is None:
@@ -82,8 +85,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, save=False, out=None, h_out=Non
 
 def rms_norm_mx(x, weight, format="e4m3", residual=None, eps=1e-6, h_out=None, stream=None):
     """``rms_norm`` with y as an ``Mx`` of ``format``, rounded once: y, or with ``residual`` (y, h)."""
-    data, scale, h, _ = _call("rms_norm", stream, x, x, weight, residual, eps, _format(format), False, None, h_out)
-    y = Mx(data, scale, x.size(1), format)
+    data, scale, h, _, dim = _call("rms_norm", stream, x, x, weight, residual, eps, _format(format), False, None, h_out)
+    y = _new(Mx, (data, scale, dim, format))
     return y if residual is None else (y, h if h_out is None else h_out)
 
 
@@ -106,8 +109,8 @@ def mx_quantize(x, format="e2m1", transpose=False, stream=None):
     block's peak between 6 and 8 scales in e2m1 becomes 6).  A weight [in, out] as ``linear``
     takes it becomes ``mx_linear``'s by ``transpose``, blocks along ``in``.
     """
-    data, scale = _call("mx_quantize", stream, x, x, _format(format), bool(transpose))
-    return Mx(data, scale, x.size(0 if transpose else 1), format)
+    data, scale, cols = _call("mx_quantize", stream, x, x, _format(format), bool(transpose))
+    return _new(Mx, (data, scale, cols, format))
 
 
 def mx_dequantize(a, dtype=None, stream=None):
