@@ -387,11 +387,13 @@ struct MxPairLayout {
     // bounded waits; why is not known.  So: none in 44,000.)
     static constexpr int kSmem = 232448;
     static_assert(kSlots <= kMaxStages && kUsed <= kSmem, "shared memory");
-    // Tensor Memory: the accumulators overlap in kShared columns, and two steps' scales follow
+    // Tensor Memory: the accumulators overlap in 128 columns, so that every stage of the ring
+    // has a place of its own for its scales.  (With two places and 64 shared columns the
+    // products of two steps ago had to be waited for: 4096 x 4096 x 14336, 4 bits, 88 us.)
     static constexpr int kScaleCols = 12 * kTiles;
-    static constexpr int kSecond = 256 - 64;
+    static constexpr int kSecond = 128;
     static constexpr int kScaleCol = kSecond + 256;
-    static_assert(kScaleCol + 2 * kScaleCols <= 512, "Tensor Memory");
+    static_assert(kScaleCol + kSlots * kScaleCols <= 512, "Tensor Memory");
 };
 
 struct MxPairParams {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             ptx::mbar_init(tfull_bar(a), 1);
             ptx::mbar_init(tempty_bar(a), 2 * L::kWarps);  // every epilogue warp of both CTAs
         }
-        ptx::mbar_init(shared_bar, L::kWarps);  // half of them drain the columns in question
+        ptx::mbar_init(shared_bar, 2 * L::kWarps);
         ptx::mbar_init(drain_bar, 1);
         for (int w = 0; w < L::kWarps; ++w) ptx::mbar_init(residual_bar(w), 1);
         *abort_flag = 0;
@@ -576,9 +578,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
         if (rank == 0) {
             constexpr uint32_t idesc = mx_idesc<FMT>(256, 256, 0, 0);
             const uint32_t elected = ptx::elect_one();
-            int stage = 0, old_stage = 0, tl = 0;
-            uint32_t phase = 0, old_phase = 0, set = 0;
-            int under_way = 0;  // steps whose scales may still be read, two at most
+            int stage = 0, tl = 0;
+            uint32_t phase = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
                 const int acc = tl & 1;
@@ -590,28 +591,16 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 const uint32_t d_tmem = tmem + (uint32_t)(acc * L::kSecond);
-                for (int kb = 0; kb < p.k_steps; ++kb, set ^= 1u) {
-                    // two sets of scales in Tensor Memory: the products that read this one, two
-                    // steps ago, are complete
-                    if (under_way < 2) {
-                        ++under_way;
-                    } else {
-                        if (!wait_uniform(empty_bar(old_stage), old_phase, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
-                            ok = false;
-                            break;
-                        }
-                        if (++old_stage == S) {
-                            old_stage = 0;
-                            old_phase ^= 1u;
-                        }
-                    }
+                for (int kb = 0; kb < p.k_steps; ++kb) {
+                    // the stage was loaded once the products that read it before were complete,
+                    // and its scales' place in Tensor Memory with it
                     if (!wait_uniform(full_bar(stage), phase, abort_flag, p.wait_limit, kSiteMmaFull)) {
                         ok = false;
                         break;
                     }
                     ptx::tc_fence_after();
                     const uint32_t src = ring + stage * L::kStride, ssrc = src + 2 * L::kOperandBytes;
-                    const uint32_t xcol = tmem + L::kScaleCol + set * L::kScaleCols, wcol = xcol + 4 * L::kTiles;
+                    const uint32_t xcol = tmem + L::kScaleCol + (uint32_t)(stage * L::kScaleCols), wcol = xcol + 4 * L::kTiles;
 #pragma unroll
                     for (int i = 0; i < L::kTiles; ++i) {
                         // w's 256 rows are eight neighbouring columns a tile of K
@@ -646,7 +635,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             __syncwarp();
         }
     } else {
-        // ---------------- epilogue (both CTAs): 32 rows x 128 columns a warp ----------------
+        // ---------------- epilogue (both CTAs): 32 rows x twice 64 columns a warp ----------------
         const int ew = warp - 2, q = warp & 3, half = ew >> 2;
         const uint32_t buf = staging + (uint32_t)(ew * L::kStaging), bar = residual_bar(ew);
         const int n8 = p.N & ~7;   // columns that y's tensor map holds (store_tail)
@@ -661,11 +650,10 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             coords(t, mb, nb);
             const int acc = tl & 1;
             const int row0 = mb * 256 + (int)rank * 128 + q * 32;
-            // 64 columns at a time; those that the accumulators share, the last of the first
+            // 64 columns at a time; those that the accumulators share, the last 128 of the first
             // and the first of the second, before the others
-            const bool shares = half != acc;
-            const int first = shares && acc == 0 ? 64 : 0;
-            const int n0 = nb * 256 + half * 128;
+            const int first = (acc ? 0 : 128) + half * 64;
+            const int n0 = nb * 256;
             // the buffer is free once its last store has read it; then, where there is a
             // residual, its 32 x 64 values go there
             auto prepare = [&](int x) {
@@ -683,10 +671,10 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             prepare(n0 + first);
             if (!warp_wait(tfull_bar(acc), (tl >> 1) & 1, abort_flag, 4 * p.wait_limit, kSiteEpilogueTmemFull, lane)) break;
             ptx::tc_fence_after();
-            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond + half * 128);
+            const uint32_t trow = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * L::kSecond);
 #pragma unroll 1
             for (int i = 0; i < 2; ++i) {
-                const int c = i == 0 ? first : 64 - first, x = n0 + c;
+                const int c = i == 0 ? first : first ^ 128, x = n0 + c;
                 if (i == 1) prepare(x);
                 uint32_t v[2][32];
                 ptx::tmem_ld_32x32b_x32(trow + c, v[0]);
@@ -694,7 +682,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                 ptx::tmem_ld_wait();
                 // handed back only where another tile waits for it: an arrival still under way
                 // when the leader leaves would land in the shared memory of whoever follows
-                if ((i == 0 && shares && t + pairs < tiles) || (i == 1 && t + 2 * pairs < tiles)) {
+                if ((i == 0 && t + pairs < tiles) || (i == 1 && t + 2 * pairs < tiles)) {
                     ptx::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 0 ? shared_bar : tempty_bar(acc), 0));
