@@ -72,43 +72,48 @@ int run_norm(NormParams p, const Ctx& c) {
 }
 
 struct NormGradPlan {
-    int threads, blocks;
+    int threads, per_sm, blocks;
     size_t bytes;
 };
 
-// Two vectors of eight columns a thread; blocks such that some 800 threads run on an SM, with
-// few threads more rows at a time instead.
+// Two vectors of eight columns a thread, and as many blocks on an SM as make 512 threads.
 NormGradPlan norm_grad_plan(const rms_norm_grad_args& a) {
     NormGradPlan g{};
     const int vectors = ceil_div(a.dim, 8);
-    g.threads = vectors > 2048 ? 0 : ceil_div(ceil_div(vectors, 2), 32) * 32;  // 0: long rows
-    const int rows = g.threads > 128 ? 1 : g.threads > 64 ? 2 : 4;
-    const int per_sm = g.threads > 512 ? 1 : g.threads > 256 ? 2 : g.threads > 128 ? 3 : 4;
-    const long long most = ceil_div(a.tokens, rows);
-    g.blocks = most < per_sm * kNormSms ? (int)most : per_sm * kNormSms;
+    int threads = 64;
+    while (threads < 2048 && 2 * threads < vectors) threads *= 2;
+    g.threads = threads > 1024 ? 0 : threads;  // 0: long rows
+    g.per_sm = threads >= 512 ? 1 : 512 / threads;
+    // long rows: four blocks an SM over the columns and shares of the rows
+    const int most = threads > 1024 ? std::max(8, 4 * kNormSms / ceil_div(a.dim, 2048)) : g.per_sm * kNormSms;
+    g.blocks = a.tokens < most ? (int)a.tokens : most;
     g.bytes = a.dweight ? align256((size_t)g.blocks * pad8(a.dim) * 4) : 0;
     return g;
+}
+
+template <int DT, int DEPTH, int THREADS, int BLOCKS>
+int run_norm_grad_rows(const NormGradParams& p, const NormGradPlan& g, const Ctx& c) {
+    auto kern = rms_norm_grad_kernel<DT, DEPTH, THREADS, BLOCKS>;
+    constexpr int kSmem = DEPTH * 3 * 2 * 16 * THREADS;
+    static std::atomic<bool> ready[kMaxDevices];
+    const int rc = ensure_smem_limit(kern, kSmem, ready[c.ordinal]);
+    return rc != GEMM_OK ? rc : launch_pdl(kern, dim3(g.blocks), THREADS, kSmem, 1, c.stream, p);
 }
 
 template <int DT>
 int run_norm_grad(const NormGradParams& p, const NormGradPlan& g, void* dweight, const Ctx& c) {
     int rc = GEMM_OK;
-    auto rows = [&](auto kern) { return launch_pdl(kern, dim3(g.blocks), g.threads, 0, 1, c.stream, p); };
-    if (g.threads == 0) {
-        // the column sums first: dx may be written over dy
-        if (dweight)
-            rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, 0, 1, c.stream, p);
-        if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
-    } else if (g.threads > 512) {
-        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 1024, 1>);
-    } else if (g.threads > 256) {
-        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 512, 2>);
-    } else if (g.threads > 128) {
-        rc = rows(rms_norm_grad_kernel<DT, 2, 1, 256, 3>);
-    } else if (g.threads > 64) {
-        rc = rows(rms_norm_grad_kernel<DT, 2, 2, 128, 4>);
-    } else {
-        rc = rows(rms_norm_grad_kernel<DT, 2, 4, 64, 4>);
+    switch (g.threads) {
+        case 64: rc = run_norm_grad_rows<DT, 4, 64, 8>(p, g, c); break;
+        case 128: rc = run_norm_grad_rows<DT, 4, 128, 4>(p, g, c); break;
+        case 256: rc = run_norm_grad_rows<DT, 4, 256, 2>(p, g, c); break;
+        case 512: rc = run_norm_grad_rows<DT, 4, 512, 1>(p, g, c); break;
+        case 1024: rc = run_norm_grad_rows<DT, 2, 1024, 1>(p, g, c); break;
+        default:
+            // the column sums first: dx may be written over dy
+            if (dweight)
+                rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, 0, 1, c.stream, p);
+            if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
     }
     if (rc == GEMM_OK && dweight)
         rc = launch_pdl(rms_norm_weight_sum_kernel<DT>, dim3(ceil_div(p.dim, 32)), 1024, 0, 1, c.stream, p, dweight, g.blocks);

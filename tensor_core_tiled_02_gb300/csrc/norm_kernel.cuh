@@ -178,93 +178,103 @@ __device__ __forceinline__ void store_sums(float* p, const float (&f)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// A block's threads share the columns, V vectors of eight each, and walk over the rows, R
-// at a time with all their loads under way, their share of dweight in registers.  Several
-// blocks an SM, one's loads under another's sums over its row.
-template <int DT, int V, int R, int THREADS, int BLOCKS>
+// 16 bytes into shared memory, of which `bytes` are read and the rest is 0.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+    uint4 v;
+    ptx::ld_shared_v4(at, v.x, v.y, v.z, v.w);
+    return v;
+}
+
+// A block's threads share the columns, two vectors of eight each, and walk over the rows,
+// their share of dweight in registers.  What a thread will need of the next DEPTH - 1 rows is
+// on its way into shared memory, where only that thread reads it: nobody waits for loads at
+// the barrier in a row's sum, and 512 threads an SM have 150 KB under way.  (With the loads in
+// registers, 8192 x 4096: one to four blocks an SM 53 to 88 us.)
+template <int DT, int DEPTH, int THREADS, int BLOCKS>
 __global__ void __launch_bounds__(THREADS, BLOCKS) rms_norm_grad_kernel(const NormGradParams p) {
-    __shared__ float sums[2][32][R];
+    extern __shared__ __align__(16) uint8_t ring[];
+    __shared__ float sums[2][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const uint32_t mine = ptx::smem_addr(ring) + threadIdx.x * 16u, vector = blockDim.x * 16u;
+    auto slot = [&](int stage, int which, int j) { return mine + (uint32_t)((stage * 3 + which) * 2 + j) * vector; };
+    const int cols[2] = {(int)threadIdx.x * 8, (int)(threadIdx.x + blockDim.x) * 8};
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    float dw[V][8];
-    uint4 w[V];
+    float dw[2][8];
+    uint4 w[2];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
-        w[j] = col < p.dim ? load8<DT>(p.weight, col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < 2; ++j) {
+        w[j] = cols[j] < p.dim ? load8<DT>(p.weight, cols[j], cols[j], p.dim) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
     }
-    int set = 0;
-    for (long long base = (long long)blockIdx.x * R; base < p.tokens; base += (long long)gridDim.x * R, set ^= 1) {
-        uint4 g[V][R], h[V][R], e[V][R];
-        float rstd[R], dot[R];
+    auto fetch = [&](long long row, int stage) {
+        if (row < p.tokens) {
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-            const long long row = base + u;
-            rstd[u] = row < p.tokens ? p.rstd[row] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
-                const bool here = col < p.dim && row < p.tokens;
-                g[j][u] = h[j][u] = e[j][u] = make_uint4(0u, 0u, 0u, 0u);
-                if (here) {
-                    g[j][u] = load8<DT>(p.dy, row * p.lddy + col, col, p.dim);
-                    h[j][u] = load8<DT>(p.h, row * p.ldh + col, col, p.dim);
-                    if (p.dh != nullptr) e[j][u] = load8<DT>(p.dh, row * p.lddh + col, col, p.dim);
+            for (int j = 0; j < 2; ++j) {
+                const int bytes = min(16, (p.dim - cols[j]) * 2);
+                if (bytes > 0) {
+                    copy_async16(slot(stage, 0, j), static_cast<const unsigned short*>(p.dy) + row * p.lddy + cols[j], bytes);
+                    copy_async16(slot(stage, 1, j), static_cast<const unsigned short*>(p.h) + row * p.ldh + cols[j], bytes);
+                    if (p.dh != nullptr)
+                        copy_async16(slot(stage, 2, j), static_cast<const unsigned short*>(p.dh) + row * p.lddh + cols[j], bytes);
                 }
             }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const long long step = gridDim.x;
+    for (int i = 0; i < DEPTH - 1; ++i) fetch(blockIdx.x + i * step, i);
+    int stage = 0, set = 0;
+    float next_rstd = blockIdx.x < (unsigned)p.tokens ? p.rstd[blockIdx.x] : 0.0f;
+    for (long long row = blockIdx.x; row < p.tokens; row += step, set ^= 1) {
+        fetch(row + (DEPTH - 1) * step, stage == 0 ? DEPTH - 1 : stage - 1);
+        const float rstd = next_rstd;
+        if (row + step < p.tokens) next_rstd = p.rstd[row + step];
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        float dot = 0.0f;
 #pragma unroll
-        for (int u = 0; u < R; ++u) {
-            dot[u] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+            if (cols[j] >= p.dim) continue;
+            float a[8], b[8], c[8];
+            unpack8<DT>(ld_shared16(slot(stage, 0, j)), a);
+            unpack8<DT>(ld_shared16(slot(stage, 1, j)), b);
+            unpack8<DT>(w[j], c);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                float a[8], b[8], c[8];
-                unpack8<DT>(g[j][u], a);
-                unpack8<DT>(h[j][u], b);
-                unpack8<DT>(w[j], c);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    dot[u] = fmaf(a[i] * c[i], b[i], dot[u]);
-                    dw[j][i] = fmaf(a[i] * b[i], rstd[u], dw[j][i]);
-                }
-            }
-            dot[u] = warp_sum(dot[u]);
-        }
-        if (lane == 0)
-#pragma unroll
-            for (int u = 0; u < R; ++u) sums[set][warp][u] = dot[u];
-        __syncthreads();
-        if (p.dx == nullptr) continue;
-#pragma unroll
-        for (int u = 0; u < R; ++u) {
-            const long long row = base + u;
-            const float all = warp_sum(lane < warps ? sums[set][lane][u] : 0.0f);
-            if (row >= p.tokens) continue;
-            const float back = __fdiv_rn(all, (float)p.dim) * rstd[u] * rstd[u] * rstd[u];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
-                if (col >= p.dim) continue;
-                float a[8], b[8], c[8], d[8];
-                unpack8<DT>(g[j][u], a);
-                unpack8<DT>(h[j][u], b);
-                unpack8<DT>(w[j], c);
-                unpack8<DT>(e[j][u], d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) d[i] += fmaf(a[i] * c[i], rstd[u], -b[i] * back);
-                store8(p.dx, row * p.lddx + col, col, p.dim, pack8<DT>(d));
+            for (int i = 0; i < 8; ++i) {
+                dot = fmaf(a[i] * c[i], b[i], dot);
+                dw[j][i] = fmaf(a[i] * b[i], rstd, dw[j][i]);
             }
         }
+        if (p.dx != nullptr) {
+            dot = warp_sum(dot);
+            if (lane == 0) sums[set][warp] = dot;
+            __syncthreads();
+            const float back = __fdiv_rn(warp_sum(lane < warps ? sums[set][lane] : 0.0f), (float)p.dim) * rstd * rstd * rstd;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (cols[j] >= p.dim) continue;
+                float a[8], b[8], c[8], d[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                unpack8<DT>(ld_shared16(slot(stage, 0, j)), a);
+                unpack8<DT>(ld_shared16(slot(stage, 1, j)), b);
+                unpack8<DT>(w[j], c);
+                if (p.dh != nullptr) unpack8<DT>(ld_shared16(slot(stage, 2, j)), d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] += fmaf(a[i] * c[i], rstd, -b[i] * back);
+                store8(p.dx, row * p.lddx + cols[j], cols[j], p.dim, pack8<DT>(d));
+            }
+        }
+        if (++stage == DEPTH) stage = 0;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (p.partial == nullptr) return;
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int col = ((int)threadIdx.x + j * (int)blockDim.x) * 8;
-        if (col < p.dim) store_sums(p.partial + blockIdx.x * p.pitch() + col, dw[j]);
-    }
+    for (int j = 0; j < 2; ++j)
+        if (cols[j] < p.dim) store_sums(p.partial + blockIdx.x * p.pitch() + cols[j], dw[j]);
 }
 
 // dx of rows too long for the above, a block of 1024 threads each, in two passes.

@@ -6,8 +6,9 @@ at most c values one after the other and 10 more in two trees: squares, all of o
 off by c + 10.  rstd halves that and adds three roundings (division, sum, root, the last two
 weighing half and one).  h w is exact (two 16-bit significands), so y has one rounding more.
 The gradient's mean is off by (c + 10 + 2) of the mean of magnitudes, and five products and
-sums follow; dweight adds up to (rows a block + 16) terms of two roundings each.  c: eight
-columns to each of 8 vectors, or of a thread's share of a long row.
+sums follow; dweight adds the rows of one block (of at least 152, or fewer for long rows), then
+the blocks' sums (24 at most one after the other and 5 in a tree), terms of two roundings
+each.  c: eight columns to each of 8 vectors, or of a thread's share of a long row.
 """
 import math
 
@@ -118,8 +119,9 @@ def gradients(dy, h, w, rstd, dh):
         e = e + ULP * dh.double().abs()
     e = e + 2 * ULP * dx.abs()
     dw, mag = (g * h * r).sum(0, keepdim=True), (g * h * r).abs().sum(0, keepdim=True)
-    rows = math.ceil(len(h) / min(math.ceil(len(h) / 4), 608)) + 4
-    return V(dx, 1.01 * e), V(dw, 1.01 * ULP * (rows + 16 + 3 + 19) * mag)
+    blocks = 152 if dim <= 16384 else max(8, 608 // math.ceil(dim / 2048))
+    rows = math.ceil(len(h) / min(len(h), blocks))
+    return V(dx, 1.01 * e), V(dw, 1.01 * ULP * (rows + 24 + 5 + 3) * mag)
 
 
 @pytest.mark.parametrize("shape", SHAPES + [(5000, 264)], ids=str)
