@@ -90,7 +90,7 @@ int mx_linear(const mx_linear_args *args, gemm_stream_t stream);
  * y = h rstd weight with rstd = 1 / sqrt(mean of h^2 over a row + eps)
  *
  *   x, residual  [tokens, dim]; residual may be NULL
- *   weight       [dim] of x's type
+ *   weight       [dim] of x's type, 16-byte aligned
  *   h            [tokens, dim], wanted exactly where there is a residual; may be x or
  *                the residual itself (same ld)
  *   y            [tokens, dim] of x's type, or NULL
@@ -118,6 +118,7 @@ int rms_norm_forward(const rms_norm_args *args, gemm_stream_t stream);
  *   dweight = sum over tokens of dy h rstd
  *
  *   dy, h, dh, dx [tokens, dim]; dx may be dy or dh itself (same ld)
+ *   weight        [dim], 16-byte aligned;  rstd [tokens] fp32, as the forward pass gave it
  *   dx, dweight   each NULL when not wanted
  */
 typedef struct {

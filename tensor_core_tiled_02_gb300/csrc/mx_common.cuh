@@ -39,13 +39,20 @@ __device__ __forceinline__ uint32_t abs_bits(float f) { return __float_as_uint(f
 // Eight values to the format, nearest even, saturated: one word (e2m1) or two (e4m3).
 template <int FMT>
 __device__ __forceinline__ uint2 mx_pack8(const float (&f)[8], float unscale) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 two = parts(mul2(f2(f[i], f[i + 1]), both(unscale)));
+        v[i] = two.x;
+        v[i + 1] = two.y;
+    }
     if constexpr (FMT == kE4M3) {
         uint32_t w[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             unsigned short lo, hi;
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[4 * i + 1] * unscale), "f"(f[4 * i] * unscale));
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[4 * i + 3] * unscale), "f"(f[4 * i + 2] * unscale));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * i + 1]), "f"(v[4 * i]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * i + 3]), "f"(v[4 * i + 2]));
             w[i] = (uint32_t)lo | ((uint32_t)hi << 16);
         }
         return make_uint2(w[0], w[1]);
@@ -60,8 +67,7 @@ __device__ __forceinline__ uint2 mx_pack8(const float (&f)[8], float unscale) {
             "  mov.b32 %0, {a, b, c, d};\n"
             "}\n"
             : "=r"(w)
-            : "f"(f[0] * unscale), "f"(f[1] * unscale), "f"(f[2] * unscale), "f"(f[3] * unscale), "f"(f[4] * unscale),
-              "f"(f[5] * unscale), "f"(f[6] * unscale), "f"(f[7] * unscale));
+            : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
         return make_uint2(w, 0u);
     }
 }
