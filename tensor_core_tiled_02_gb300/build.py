@@ -72,7 +72,7 @@ def build_binding(out: str | None = None) -> str:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     subprocess.run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                     *[a for d in include for a in ("-isystem", d)], "-I", INCLUDE, "-o", out, BINDING_SOURCE,
-                    "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"], check=True)
+                    "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-ltorch", "-lc10_cuda", "-lc10"], check=True)
     return out
 
 

@@ -10,7 +10,7 @@
 #include <Python.h>
 
 #include <ATen/core/grad_mode.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -116,8 +116,9 @@ struct Call {
     void place(const at::Tensor& t, const char* name) const {
         if (t.device() != device) refuse(std::string(name) + " is on " + t.device().str() + ", not on " + device.str());
     }
+    // (not by way of torch's dispatcher: several of these are a good part of a small call's host time)
     at::Tensor empty(at::IntArrayRef shape, at::ScalarType st) const {
-        return at::empty(shape, at::TensorOptions().dtype(st).device(device));
+        return at::Tensor(at::detail::empty_cuda(shape, st, device, std::nullopt));
     }
     // A matrix whose row stride the library takes: a multiple of 8.
     at::Tensor matrix(int64_t rows, int64_t cols) const {
