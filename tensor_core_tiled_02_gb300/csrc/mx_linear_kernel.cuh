@@ -73,6 +73,13 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t tmem, uint64_t desc, uin
                      : "memory");
 }
 
+// `bytes` side by side, a multiple of 16, into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+                 "r"(bar)
+                 : "memory");
+}
+
 // mma_commit and its pair forms (to the leader alone, or to both CTAs).
 __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t elected) {
     asm volatile(
@@ -146,10 +153,16 @@ struct MxEpilogue {
 
 constexpr int kMxSkinnySlots = 12;
 
+struct MxSkinnyMaps {
+    CUtensorMap x, w;
+};
+
 struct MxSkinnyParams {
     int T, N, nt, t_tiles;
     int blocks, k_steps;      // of 32 values; of 128 bytes
     int split, slots, stage_bytes, tmem_cols, scale_col;
+    const uint8_t *xs, *ws;   // scales (copied plainly: a tensor map costs the host 0.4 us)
+    int k_tiles;
     MxEpilogue e;
     long long wait_limit;
     int inject;
@@ -178,7 +191,7 @@ __device__ __forceinline__ void mx_finish4(const MxEpilogue& e, long long t, int
 }
 
 template <int FMT, int DT>
-__global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_constant__ MxMaps tm, const MxSkinnyParams p) {
+__global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_constant__ MxSkinnyMaps tm, const MxSkinnyParams p) {
     constexpr int kTiles = mx_step_tiles(FMT);           // scale tiles of a step
     constexpr int kScaleCols = 8 * kTiles;               // Tensor Memory columns of a step's scales, both operands
     constexpr uint32_t kScaleBytes = 512 * kTiles;
@@ -220,8 +233,6 @@ __global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_consta
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm.w);
         ptx::prefetch_tmap(&tm.x);
-        ptx::prefetch_tmap(&tm.ws);
-        ptx::prefetch_tmap(&tm.xs);
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_addr((const void*)tmem_slot), p.tmem_cols);
@@ -244,12 +255,14 @@ __global__ void __launch_bounds__(kThreads) mx_skinny_kernel(const __grid_consta
                 if (!wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty)) break;
                 const uint32_t dst = ring + (uint32_t)(stage * p.stage_bytes), fb = full_bar(stage);
                 if (!TC_CHECK(holds(ring, (uint32_t)(S * p.stage_bytes), dst, (uint32_t)p.stage_bytes), kSiteSmemBounds)) break;
-                ptx::mbar_arrive_expect_tx(fb, (uint32_t)p.stage_bytes);
+                // scale tiles of this step that exist
+                const uint32_t here = 512u * (uint32_t)min(kTiles, p.k_tiles - kb * kTiles);
+                ptx::mbar_arrive_expect_tx(fb, (uint32_t)((128 + p.nt) * kMxStepBytes) + 2 * here);
                 const uint32_t xd = dst + 128 * kMxStepBytes, sd = xd + (uint32_t)(p.nt * kMxStepBytes);
                 ptx::tma_load_2d(dst, &tm.w, fb, kb * kMxStepBytes, n0);
-                ptx::tma_load_2d(sd, &tm.ws, fb, kb * kTiles * 128, n_tile);
+                ptx::bulk_load(sd, p.ws + ((long long)n_tile * p.k_tiles + kb * kTiles) * 512, here, fb);
                 ptx::tma_load_2d(xd, &tm.x, fb, kb * kMxStepBytes, t0);
-                ptx::tma_load_2d(sd + kScaleBytes, &tm.xs, fb, kb * kTiles * 128, t_tile);
+                ptx::bulk_load(sd + kScaleBytes, p.xs + ((long long)t_tile * p.k_tiles + kb * kTiles) * 512, here, fb);
                 issued_mask |= 1u << stage;
                 issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
                 if (++stage == S) {

@@ -152,15 +152,6 @@ struct MxProduct {
     MxEpilogue e;
 };
 
-int encode_mx(MxMaps* tm, const MxProduct& q, uint32_t x_rows) {
-    std::memset(tm, 0, sizeof(*tm));
-    int rc = encode_mx_data(&tm->x, q.x, x_rows);
-    if (rc == GEMM_OK) rc = encode_mx_data(&tm->w, q.w, 128);
-    if (rc == GEMM_OK) rc = encode_mx_scale(&tm->xs, q.x);
-    if (rc == GEMM_OK) rc = encode_mx_scale(&tm->ws, q.w);
-    return rc;
-}
-
 struct MxSkinnyPlan {
     int nt, t_tiles, tiles, split, slots, stage_bytes, smem, scale_col, tmem_cols, k_steps;
 };
@@ -219,8 +210,10 @@ long long mx_pair_ns(const MxProduct& q, int pairs, int k_steps, long long bytes
 
 template <int FMT, int DT>
 int run_mx_skinny(const MxProduct& q, const MxSkinnyPlan& g, const Ctx& c) {
-    MxMaps tm;
-    int rc = encode_mx(&tm, q, g.nt);
+    MxSkinnyMaps tm;
+    std::memset(&tm, 0, sizeof(tm));
+    int rc = encode_mx_data(&tm.x, q.x, g.nt);
+    if (rc == GEMM_OK) rc = encode_mx_data(&tm.w, q.w, 128);
     if (rc != GEMM_OK) return rc;
     MxSkinnyParams p;
     std::memset(&p, 0, sizeof(p));
@@ -235,6 +228,9 @@ int run_mx_skinny(const MxProduct& q, const MxSkinnyPlan& g, const Ctx& c) {
     p.stage_bytes = g.stage_bytes;
     p.tmem_cols = g.tmem_cols;
     p.scale_col = g.scale_col;
+    p.xs = static_cast<const uint8_t*>(q.x.scale);
+    p.ws = static_cast<const uint8_t*>(q.w.scale);
+    p.k_tiles = ceil_div(q.x.cols, 128);
     p.e = q.e;
     p.wait_limit = c.wait_limit;
     p.inject = c.inject;
@@ -249,7 +245,11 @@ template <int FMT, int DT>
 int run_mx_pair(const MxProduct& q, const Ctx& c) {
     using L = MxPairLayout<FMT>;
     MxMaps tm;
-    int rc = encode_mx(&tm, q, 128);
+    std::memset(&tm, 0, sizeof(tm));
+    int rc = encode_mx_data(&tm.x, q.x, 128);
+    if (rc == GEMM_OK) rc = encode_mx_data(&tm.w, q.w, 128);
+    if (rc == GEMM_OK) rc = encode_mx_scale(&tm.xs, q.x);
+    if (rc == GEMM_OK) rc = encode_mx_scale(&tm.ws, q.w);
     constexpr int dtype = DT == kBF16 ? LAYER_BF16 : LAYER_F16;
     if (rc == GEMM_OK) rc = encode_out(&tm.y, mat16(q.e.y, q.x.rows, q.w.rows, q.e.ldy), dtype, 32);
     if (rc == GEMM_OK && q.e.residual) rc = encode_mat(&tm.residual, mat16(q.e.residual, q.x.rows, q.w.rows, q.e.ldr), dtype, 64, 32);
