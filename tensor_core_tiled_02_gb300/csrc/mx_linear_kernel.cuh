@@ -10,8 +10,17 @@
 // row / 32, byte block % 4, repeated for each quarter of the lanes.  A product names
 // the byte it starts from in its instruction descriptor.
 //
-// Two kernels: pairs of CTAs on 256 x 256 tiles, and for few tokens 128 weight rows by
-// up to 128 tokens (the weights as the MMA's M), split along K over a cluster.
+// Two kernels, chosen by estimated time (mx_ops.cuh):
+//   pairs of CTAs on 256 x 256 tiles, persistent, the epilogue of one tile under the
+//   products of the next.  Bound by the tensor pipe and, repeated, by power: a step's four
+//   products take 512 cycles and the issuing warp's waits, copies and commit 100 more;
+//   the next tile's wait for the columns that two accumulators share adds some 1,500 a tile.
+//   4096 x 4096 x 14336 87 us in 4 bits (5.5 PFLOP/s), 153 in 8 (3.1; the library's product
+//   of the same operands 141); 4096 x 16384 x 4096 91 and 182.
+//   For few tokens 128 weight rows by up to 128 tokens (the weights as the MMA's M), split
+//   along K over a cluster.  Bound by HBM while it streams: one token, 4096 x 14336 7.9 us in
+//   4 bits (31 MB: 4.6 at the copy rate), 12.8 in 8; 4096 x 4096 5.3 and 6.5.  3.5 us are a
+//   launch's fixed path, as in layer_skinny_kernel.cuh.
 #pragma once
 
 #include "layer_skinny_kernel.cuh"
@@ -22,9 +31,10 @@ namespace tcgemm {
 namespace ptx {
 
 // The tensor core's instructions take their operands from uniform registers.  A thread by
-// itself pays for every one that it computed (110 to 150 cycles a product with scales,
-// whose arithmetic takes 128 and less), so here the whole warp walks the loop, on values
-// and votes that are the same in every lane, and only the instructions are one lane's.
+// itself pays for every one that it computed (110 to 150 cycles a product with scales, whose
+// arithmetic takes 128), so here the whole warp walks the loop, on values and votes that are
+// the same in every lane, and only the instructions are one lane's (4096 x 16384 x 4096, 4
+// bits: 183 -> 91 us).
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile(
