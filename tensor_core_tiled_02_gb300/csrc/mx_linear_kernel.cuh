@@ -12,9 +12,10 @@
 //
 // Two kernels, chosen by estimated time (mx_ops.cuh):
 //   pairs of CTAs on 256 x 256 tiles, persistent, the epilogue of one tile under the
-//   products of the next.  Bound by the tensor pipe and, repeated, by power: a step's four
-//   products take 512 cycles and the issuing warp's waits, copies and commit 100 more;
-//   the next tile's wait for the columns that two accumulators share adds some 1,500 a tile.
+//   products of the next.  Bound by the operands' way into the SM and, repeated, by power:
+//   a step's 34 or 36 KB take 590 or 620 cycles at some 58 bytes a cycle, its products 512
+//   (twice the products a step: 1,017); the next tile's wait for the columns that two
+//   accumulators share adds some 1,500 a tile.
 //   4096 x 4096 x 14336 87 us in 4 bits (5.5 PFLOP/s), 153 in 8 (3.1; the library's product
 //   of the same operands 141); 4096 x 16384 x 4096 91 and 182.
 //   For few tokens 128 weight rows by up to 128 tokens (the weights as the MMA's M), split
