@@ -15,9 +15,9 @@
 //   products of the next.  Bound by the operands' way into the SM and, repeated, by power:
 //   a step's 34 or 36 KB take 590 or 620 cycles at some 58 bytes a cycle, its products 512
 //   (twice the products a step: 1,017); the next tile's wait for the columns that two
-//   accumulators share adds some 1,500 a tile.
-//   4096 x 4096 x 14336 87 us in 4 bits (5.5 PFLOP/s), 153 in 8 (3.1; the library's product
-//   of the same operands 141); 4096 x 16384 x 4096 91 and 182.
+//   accumulators share adds some 800 a tile.
+//   4096 x 4096 x 14336 81 us in 4 bits (6.0 PFLOP/s), 153 in 8 (3.1; the library's product
+//   of the same operands 141); 4096 x 16384 x 4096 89 and 184; 4096 x 1024 x 8192 19 and 30.
 //   For few tokens 128 weight rows by up to 128 tokens (the weights as the MMA's M), split
 //   along K over a cluster.  Bound by HBM while it streams: one token, 4096 x 14336 7.9 us in
 //   4 bits (31 MB: 4.6 at the copy rate), 12.8 in 8; 4096 x 4096 5.3 and 6.5.  3.5 us are a
@@ -91,6 +91,13 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
+// An arrival on an mbarrier of another CTA that hands over no memory, only Tensor Memory whose
+// values are in registers (tcgen05.wait::ld).  With release at cluster scope it waited for
+// whatever the SM had under way, 900 to 3,700 cycles, while the next tile waited for it.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // mma_commit and its pair forms (to the leader alone, or to both CTAs).
 __device__ __forceinline__ void commit_one(uint32_t bar, uint32_t elected) {
     asm volatile(
@@ -130,10 +137,9 @@ __device__ __forceinline__ uint64_t mx_scale_desc(uint32_t saddr) {
 }
 
 // wait_bounded by a whole warp: every lane asks, and all go the same way.
-template <bool kClusterAcquire = false>
 __device__ __forceinline__ bool wait_uniform(uint32_t bar, uint32_t parity, volatile int* abort_flag, long long limit, unsigned site) {
     auto probe = [&]() {
-        return __all_sync(0xffffffffu, kClusterAcquire ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait(bar, parity)) != 0;
+        return __all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity)) != 0;
     };
     if (probe()) return true;
     const long long t0 = clock64();
@@ -608,8 +614,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
                 const int acc = tl & 1;
                 // this accumulator's last tile is drained, and of the other's the columns they share
-                if (!wait_uniform<true>(tempty_bar(acc), ((tl >> 1) & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty) ||
-                    !wait_uniform<true>(shared_bar, (tl & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
+                if (!wait_uniform(tempty_bar(acc), ((tl >> 1) & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty) ||
+                    !wait_uniform(shared_bar, (tl & 1) ^ 1u, abort_flag, p.wait_limit, kSiteMmaTmemEmpty)) {
                     ok = false;
                     break;
                 }
@@ -709,7 +715,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                 if ((i == 0 && t + pairs < tiles) || (i == 1 && t + 2 * pairs < tiles)) {
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa(i == 0 ? shared_bar : tempty_bar(acc), 0));
+                    if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa(i == 0 ? shared_bar : tempty_bar(acc), 0));
                 }
                 if (row0 >= p.M || x >= p.N) continue;
                 if (pending) {
