@@ -156,7 +156,8 @@ struct MxSkinnyPlan {
     int nt, t_tiles, tiles, split, slots, stage_bytes, smem, scale_col, tmem_cols, k_steps;
 };
 
-MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
+MxSkinnyPlan mx_skinny_plan(const MxProduct& q, DeviceInfo& dev) {
+    const int sms = dev.sms;
     MxSkinnyPlan g{};
     const int fmt = q.x.fmt;
     // tokens from multiples of 128 on: there the tiles of their scales begin
@@ -179,9 +180,12 @@ MxSkinnyPlan mx_skinny_plan(const MxProduct& q, int sms) {
     // Two CTAs fill an SM, so that the next launch's find room beside this one's (one token,
     // K = N = 4096, 8 bits: 6.5 us, 7.2 with the whole SM).  Larger tiles take all of it where
     // each has an SM to itself, for a ring of more than three steps (128 tokens, the same: 11.7
-    // and 10.8); not in clusters of more than four, of which few fit at once.
+    // and 10.8), and all clusters fit at once (a cluster's CTAs share a GPC: of 48 clusters of
+    // three some wait for others, 300 tokens, 4096 x 2048, 4 bits 14.7 us).
     const int fixed = 1024 + 8 * (2 * kMxSkinnySlots + 1) + 16;
-    g.smem = g.nt > 48 && g.tiles * g.split <= sms && g.split <= 4 ? kSmemLimit : kSkinnyTwoSmem;
+    const bool alone = g.nt > 48 && g.tiles * g.split <= sms &&
+                       (g.split == 1 || g.tiles <= (g.split == 2 ? max_pairs_of(dev) : max_clusters_of(dev, g.split)));
+    g.smem = alone ? kSmemLimit : kSkinnyTwoSmem;
     g.slots = (g.smem - fixed) / g.stage_bytes;
     if (g.slots > kMxSkinnySlots) g.slots = kMxSkinnySlots;
     return g;
@@ -279,7 +283,7 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
 template <int FMT, int DT>
 int run_mx_product(const MxProduct& q, const Ctx& c) {
     if (q.x.rows <= kFewTokens) {
-        const MxSkinnyPlan g = mx_skinny_plan(q, c.dev->sms);
+        const MxSkinnyPlan g = mx_skinny_plan(q, *c.dev);
         const long long bytes = q.w.rows * mx_width(q.w) + q.x.rows * (mx_width(q.x) + 2 * q.w.rows);
         if (mx_skinny_ns(g, c.dev->sms, bytes) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps, bytes))
             return run_mx_skinny<FMT, DT>(q, g, c);
