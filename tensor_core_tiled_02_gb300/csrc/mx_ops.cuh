@@ -195,7 +195,8 @@ MxSkinnyPlan mx_skinny_plan(const MxProduct& q, DeviceInfo& dev) {
 // for few tokens takes in 110 bytes a nanosecond, two on an SM 1.5 times that; 28 ns a token
 // for its way through shared memory.  A pair takes 310 a step of a tile.  HBM gives 6,500
 // bytes.  (192 products of 32 to 768 tokens, K from 1024 and N from 2048 to 14336, either
-// format: the choice costs 0.4 % on average and 11 % at worst against the better of the two.)
+// format: the choice costs 0.4 % on average and 11 % at worst against the better of the two; 32
+// of 1100 to 8192 tokens, 1 % at worst.)
 long long mx_skinny_ns(const MxSkinnyPlan& g, int sms, long long bytes) {
     const long long ctas = (long long)g.tiles * g.split, full = ctas / (2 * sms), rest = ctas % (2 * sms);
     const long long halves = 3 * full + (rest > sms ? 3 : rest > 0 ? 2 : 0);  // in units of half a lone CTA's time
@@ -280,9 +281,14 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
     return launch_pdl(kern, dim3(2 * (int)(tiles < pairs ? tiles : pairs)), L::kThreads, L::kSmem, 2, c.stream, tm, p);
 }
 
+// Beyond these there are tiles enough for the pairs whatever w has.  Where w has few rows and K
+// is long the kernel for few tokens wins well above a thousand (1215 tokens, 8496 x 848, 8 bits:
+// 17.8 us, on pairs 25.6).
+constexpr long long kMxFewTokens = 8192;
+
 template <int FMT, int DT>
 int run_mx_product(const MxProduct& q, const Ctx& c) {
-    if (q.x.rows <= kFewTokens) {
+    if (q.x.rows <= kMxFewTokens) {
         const MxSkinnyPlan g = mx_skinny_plan(q, *c.dev);
         const long long bytes = q.w.rows * mx_width(q.w) + q.x.rows * (mx_width(q.x) + 2 * q.w.rows);
         if (mx_skinny_ns(g, c.dev->sms, bytes) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps, bytes))

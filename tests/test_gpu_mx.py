@@ -129,7 +129,7 @@ def test_quantize_views():
 # tokens, k, n
 PRODUCTS = [(1, 1, 1), (1, 32, 8), (1, 33, 5), (2, 64, 130), (3, 100, 7), (1, 4096, 512), (8, 1000, 300), (16, 96, 128), (17, 129, 257),
             (33, 2048, 200), (64, 512, 1000), (100, 640, 129), (128, 256, 256), (129, 4000, 131), (200, 1504, 640), (300, 72, 1031),
-            (513, 2080, 520), (1000, 352, 1200), (2500, 224, 264), (4096, 128, 2048), (1, 16384, 136), (700, 8200, 264)]
+            (513, 2080, 520), (1000, 352, 1200), (2500, 224, 264), (4096, 128, 2048), (1, 16384, 136), (700, 8200, 264), (1300, 4200, 136), (2100, 2080, 72)]
 
 
 def product(x, w):

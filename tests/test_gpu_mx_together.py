@@ -233,3 +233,20 @@ def test_norm_places_both_forms(tokens, dim):
     m = tc.rms_norm_mx(x, w, format="e4m3", eps=EPS)
     assert torch.equal(y[:, :dim], tc.rms_norm(x, w, eps=EPS)) and (y[:, dim:] == 3).all()
     assert torch.equal(data[:, :width], m.data) and (data[:, width:] == 0xA5).all() and (scale[tiles:] == 0xA5).all()
+
+
+def test_gradients_one_by_one():
+    """dx without dweight and dweight without dx, which only the C ABI asks for."""
+    for tokens, dim in ((5, 40), (300, 4096), (40, 16400)):
+        h, dy, w = draw(80, tokens, dim), draw(81, tokens, dim), vector(82, dim)
+        _, _, rstd = tc.rms_norm(h, w, eps=EPS, save=True)
+        dx, dw = tc.rms_norm_backward(dy, h, w, rstd)
+        ox, ow = torch.empty_like(h), torch.empty_like(w)
+        ws = torch.empty(700 * dim * 4 // 256 * 256 + 256, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        for px, pw in ((ox.data_ptr(), 0), (0, ow.data_ptr())):
+            rc = tc.load_library().rms_norm_backward(struct.pack("16q", dy.data_ptr(), h.data_ptr(), w.data_ptr(), 0, rstd.data_ptr(), px, pw, dim,
+                                                                 dim, 0, dim, tokens, dim, 1, ws.data_ptr(), ws.numel()), None)
+            assert rc == 0
+        torch.cuda.synchronize()
+        assert torch.equal(ox, dx) and torch.equal(ow, dw)
