@@ -56,7 +56,7 @@ int run_norm_rows(const NormParams& p, int threads, const Ctx& c) {
 template <int DT, int OUT>
 int run_norm(NormParams p, const Ctx& c) {
     const int vectors = ceil_div(p.dim, 8);
-    if (vectors > 8 * 1024)
+    if (vectors > 4 * 1024)
         return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
     // few rows: one vector a thread, for the least latency; many: four, for bytes under way
     int v = p.tokens > 2 * c.dev->sms ? (vectors > 256 ? 4 : vectors > 64 ? 2 : 1) : 1;
@@ -66,8 +66,7 @@ int run_norm(NormParams p, const Ctx& c) {
     switch (v) {
         case 1: return run_norm_rows<DT, 1, OUT>(p, threads, c);
         case 2: return run_norm_rows<DT, 2, OUT>(p, threads, c);
-        case 4: return run_norm_rows<DT, 4, OUT>(p, threads, c);
-        default: return run_norm_rows<DT, 8, OUT>(p, threads, c);
+        default: return run_norm_rows<DT, 4, OUT>(p, threads, c);
     }
 }
 
