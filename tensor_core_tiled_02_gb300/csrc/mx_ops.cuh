@@ -58,8 +58,11 @@ int run_norm(NormParams p, const Ctx& c) {
     const int vectors = ceil_div(p.dim, 8);
     if (vectors > 4 * 1024)
         return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
-    // few rows: one vector a thread, for the least latency; many: four, for bytes under way
-    int v = p.tokens > 2 * c.dev->sms ? (vectors > 256 ? 4 : vectors > 64 ? 2 : 1) : 1;
+    // One vector a thread while all rows' threads are resident at once, else two, as a block
+    // takes at most 1024 threads (with residual, one, two and four: 304 x 4096 2.7, 2.9 and 3.6
+    // us; 512 x 8192 7.6, 6.7 and 6.9; 2048 x 4096 12.3, 10.8 and 12.3; 8192 x 4096 45.0, 42.0
+    // and 42.8; into 8 bits 2000 x 4096 13.8, 12.3 and 12.8, 8192 x 4096 49.2, 42.0 and 40.1).
+    int v = (long long)p.tokens * vectors <= 2048ll * c.dev->sms ? 1 : 2;
     while (vectors > 1024 * v) v *= 2;
     p.group = ceil_div(ceil_div(vectors, v), 32) * 32;
     const int threads = p.group == 32 ? 128 : p.group;

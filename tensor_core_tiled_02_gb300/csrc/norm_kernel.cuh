@@ -9,7 +9,7 @@
 // a load, between the sum over the row and its use; rows beyond 32768 columns
 // forward and 16384 back are read twice instead.  All sums are fp32 and taken in a
 // fixed order: the same inputs give the same bits.  8192 x 4096 in bf16 with residual
-// 41.6 us, 6.45 TB/s of 268 MB; gradients 47.6, 5.6 TB/s, of which the join of dweight's
+// 40.8 us, 6.6 TB/s of 268 MB; gradients 47.6, 5.6 TB/s, of which the join of dweight's
 // partial sums takes some 4.
 #pragma once
 
@@ -41,16 +41,37 @@ __device__ __forceinline__ float norm_rstd(float squares, int dim, float eps) {
     return __frsqrt_rn(__fdiv_rn(squares, (float)dim) + eps);
 }
 
+// Where a row of the outputs begins.
+struct NormRowOut {
+    unsigned short* y;
+    uint8_t* data;
+    uint32_t* scale;  // the first tile's word of this row; the next tile's is 128 words on
+};
+
+template <int OUT>
+__device__ __forceinline__ NormRowOut norm_row_out(const NormParams& p, int row) {
+    NormRowOut o{p.y != nullptr ? static_cast<unsigned short*>(p.y) + row * p.ldy : nullptr, nullptr, nullptr};
+    if constexpr (OUT != kNormRow) {
+        o.data = p.data + row * p.ldd;
+        o.scale = p.scale + (mx_scale_word(row, 0, (p.dim + 127) >> 7) >> 2);
+    }
+    return o;
+}
+
 // Eight columns of y: scaled, and stored in each form that is wanted.
 template <int DT, int OUT>
-__device__ __forceinline__ void norm_store(const NormParams& p, int row, int col, uint4 hv, float rstd) {
+__device__ __forceinline__ void norm_store(const NormParams& p, const NormRowOut& o, int col, uint4 hv, float rstd) {
     float h[8], w[8], f[8];
     unpack8<DT>(hv, h);
     unpack8<DT>(col < p.dim ? load8<DT>(p.weight, col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u), w);
     // h w is exact in fp32 (two 16-bit significands), so y is rounded once before its last rounding
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = h[i] * w[i] * rstd;
-    if (p.y != nullptr && col < p.dim) store8(p.y, row * p.ldy + col, col, p.dim, pack8<DT>(f));
+    for (int i = 0; i < 8; i += 2) {
+        const float2 two = parts(mul2(mul2(f2(h[i], h[i + 1]), f2(w[i], w[i + 1])), both(rstd)));
+        f[i] = two.x;
+        f[i + 1] = two.y;
+    }
+    if (o.y != nullptr && col < p.dim) store8(o.y, col, col, p.dim, pack8<DT>(f));
     if constexpr (OUT != kNormRow) {
         constexpr int kFmt = OUT == kNormE4M3 ? kE4M3 : kE2M1;
         if (col + 8 > p.dim) {  // behind the row's end h and w are 0, but rstd may be infinite
@@ -58,13 +79,11 @@ __device__ __forceinline__ void norm_store(const NormParams& p, int row, int col
             for (int i = 0; i < 8; ++i)
                 if (col + i >= p.dim) f[i] = 0.0f;
         }
-        const int k_tiles = (p.dim + 127) >> 7;
-        uint32_t* word = p.scale + (mx_scale_word(row, col >> 7, k_tiles) >> 2);
-        uint8_t* data = p.data + row * p.ldd + (kFmt == kE4M3 ? col : col >> 1);
         uint32_t m = abs_bits(f[0]);
 #pragma unroll
         for (int i = 1; i < 8; ++i) m = max(m, abs_bits(f[i]));
-        mx_store8<kFmt>(f, m, data, col < ((p.dim + 31) & ~31), word, (col >> 7) < k_tiles);
+        mx_store8<kFmt>(f, m, o.data + (kFmt == kE4M3 ? col : col >> 1), col < ((p.dim + 31) & ~31), o.scale + (col >> 7) * 128,
+                        (col >> 7) < ((p.dim + 127) >> 7));
     }
 }
 
@@ -114,8 +133,9 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const NormParams p) {
     const float rstd = norm_rstd(squares, p.dim, p.eps);
     if (t == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     __syncwarp();
+    const NormRowOut o = norm_row_out<OUT>(p, row);
 #pragma unroll
-    for (int j = 0; j < V; ++j) norm_store<DT, OUT>(p, row, (t + j * p.group) * 8, h[j], rstd);
+    for (int j = 0; j < V; ++j) norm_store<DT, OUT>(p, o, (t + j * p.group) * 8, h[j], rstd);
 }
 
 // Rows too long for registers, a block of 1024 threads each: h is written in the first
@@ -153,11 +173,12 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p)
     __syncwarp();
     const void* src = p.residual != nullptr ? p.h : p.x;
     const long long ld = p.residual != nullptr ? p.ldh : p.ldx;
+    const NormRowOut o = norm_row_out<OUT>(p, row);
     // whole warps to the end of the last block's tile
     for (long long c = (long long)(threadIdx.x - lane) * 8; c < (p.dim + 127ll & ~127ll); c += 8192) {
         const int col = (int)c + lane * 8;
         const uint4 h = col < p.dim ? load8<DT>(src, row * ld + col, col, p.dim) : make_uint4(0u, 0u, 0u, 0u);
-        norm_store<DT, OUT>(p, row, col, h, rstd);
+        norm_store<DT, OUT>(p, o, col, h, rstd);
     }
 }
 
