@@ -44,12 +44,17 @@ int with_types(long long dtype, long long format, F&& f) {
                              : f(integral_constant<int, kF16>{}, integral_constant<int, kE4M3>{});
 }
 
+// Shared memory that small blocks ask for without need: with a kernel on CTA pairs under 2 KB of
+// an SM are left, and no norm or quantisation is to lie beside those (MxPairLayout).  Times are
+// the same with and without.
+constexpr int kNotBesidePairs = 2048;
+
 // ---- norm ---------------------------------------------------------------------------------
 
 template <int DT, int V, int OUT>
 int run_norm_rows(const NormParams& p, int threads, const Ctx& c) {
     const int rows = p.group == 32 ? threads / 32 : 1;
-    return launch_pdl(rms_norm_kernel<DT, V, OUT>, dim3(ceil_div(p.tokens, rows)), threads, 0, 1, c.stream, p);
+    return launch_pdl(rms_norm_kernel<DT, V, OUT>, dim3(ceil_div(p.tokens, rows)), threads, kNotBesidePairs, 1, c.stream, p);
 }
 
 // Threads that share a row, and vectors of eight columns each has.
@@ -57,7 +62,7 @@ template <int DT, int OUT>
 int run_norm(NormParams p, const Ctx& c) {
     const int vectors = ceil_div(p.dim, 8);
     if (vectors > 4 * 1024)
-        return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
+        return launch_pdl(rms_norm_long_kernel<DT, OUT>, dim3(p.tokens), 1024, kNotBesidePairs, 1, c.stream, p);
     // One vector a thread while all rows' threads are resident at once, else two, as a block
     // takes at most 1024 threads (with residual, one, two and four: 304 x 4096 2.7, 2.9 and 3.6
     // us; 512 x 8192 7.6, 6.7 and 6.9; 2048 x 4096 12.3, 10.8 and 12.3; 8192 x 4096 45.0, 42.0
@@ -114,8 +119,8 @@ int run_norm_grad(const NormGradParams& p, const NormGradPlan& g, void* dweight,
         default:
             // the column sums first: dx may be written over dy
             if (dweight)
-                rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, 0, 1, c.stream, p);
-            if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, 0, 1, c.stream, p);
+                rc = launch_pdl(rms_norm_grad_columns_kernel<DT>, dim3(ceil_div(p.dim, 2048), g.blocks), 256, kNotBesidePairs, 1, c.stream, p);
+            if (rc == GEMM_OK && p.dx) rc = launch_pdl(rms_norm_grad_long_kernel<DT>, dim3(p.tokens), 1024, kNotBesidePairs, 1, c.stream, p);
     }
     if (rc == GEMM_OK && dweight)
         rc = launch_pdl(rms_norm_weight_sum_kernel<DT>, dim3(ceil_div(p.dim, 32)), 1024, 0, 1, c.stream, p, dweight, g.blocks);
@@ -441,7 +446,7 @@ int mx_quantize(const mx_quantize_args* args, gemm_stream_t stream) {
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
         constexpr int DT = decltype(dt)::value, FMT = decltype(fmt)::value;
         return a.transpose ? launch_pdl(mx_quantize_columns_kernel<DT, FMT>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p)
-                           : launch_pdl(mx_quantize_kernel<DT, FMT>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p);
+                           : launch_pdl(mx_quantize_kernel<DT, FMT>, dim3((unsigned)blocks), 256, kNotBesidePairs, 1, c.stream, p);
     });
 }
 
@@ -471,7 +476,8 @@ int mx_dequantize(const mx_dequantize_args* args, gemm_stream_t stream) {
     Ctx c;
     if ((rc = open_ctx(c, stream)) != GEMM_OK) return rc;
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) {
-        return launch_pdl(mx_dequantize_kernel<decltype(dt)::value, decltype(fmt)::value>, dim3((unsigned)blocks), 256, 0, 1, c.stream, p);
+        return launch_pdl(mx_dequantize_kernel<decltype(dt)::value, decltype(fmt)::value>, dim3((unsigned)blocks), 256, kNotBesidePairs, 1, c.stream,
+                          p);
     });
 }
 

@@ -109,6 +109,21 @@ def test_many_launches_in_a_row():
     assert torch.equal(y, first)
 
 
+def test_many_launches_beside_the_layer_operators():
+    """The same with products in 16 bits between the norms, and quantising behind them."""
+    tokens, d = 2000, 2048
+    x, r, w, wl = draw(90, tokens, d), draw(91, tokens, d), vector(92, d), draw(93, d, d, d ** -0.5)
+    first = None
+    for _ in range(500):
+        y, h = tc.rms_norm(x, w, residual=r, eps=EPS)
+        z = tc.linear(y, wl)
+        m = tc.mx_quantize(z, "e4m3")
+        z = tc.linear(z, wl, residual=h)
+        if first is None:
+            first = z.clone(), m.data.clone()
+    assert torch.equal(z, first[0]) and torch.equal(m.data, first[1])
+
+
 def test_more_than_2_31_entries():
     rows, cols = 66000, 33000
     at = [0, 1, 2**31 // cols - 1, 2**31 // cols, 2**31 // cols + 1, 65535, 65999]
