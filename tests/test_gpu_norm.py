@@ -206,6 +206,17 @@ def test_in_place_and_views(shape):
     assert torch.equal(wide[:, 8:8 + d], dx) and (wide[:, :8] == 3).all() and (wide[:, 8 + d:] == 3).all()
 
 
+@pytest.mark.parametrize("dim", [16392, 40007])
+def test_long_rows_in_place(dim):
+    """h over the residual, over x; the longer rows are read twice."""
+    w, x, r = vector(24, dim), draw(25, 3, dim), draw(26, 3, dim)
+    y, h = tc.rms_norm(x, w, residual=r, eps=EPS)
+    for which in (0, 1):
+        a = [draw(25, 3, dim), draw(26, 3, dim)]
+        y2, h2 = tc.rms_norm(a[0], w, residual=a[1], eps=EPS, h_out=a[1 - which])
+        assert h2 is a[1 - which] and torch.equal(h2, h) and torch.equal(y2, y)
+
+
 @pytest.mark.parametrize("dim", [64, 1003, 4096])
 def test_special_rows(dim):
     x, w = draw(24, 9, dim), vector(25, dim)
