@@ -91,11 +91,28 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
                  : "memory");
 }
 
-// An arrival on an mbarrier of another CTA that hands over no memory, only Tensor Memory whose
-// values are in registers (tcgen05.wait::ld).  With release at cluster scope it waited for
-// whatever the SM had under way, 900 to 3,700 cycles, while the next tile waited for it.
+// An arrival on an mbarrier of another CTA that hands over no memory, only Tensor Memory that
+// has been read.  It releases nothing: that the next tile's products come after the reads
+// rests on tcgen05.wait::ld, behind which the values are in registers, and on the fences of
+// tcgen05 before this arrival and behind the wait for it.  With release at cluster scope it
+// waited for whatever the SM had under way, 900 to 3,700 cycles, while the next tile waited
+// for it.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// One word of another CTA's shared memory (addresses from mapa).
+__device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t cluster_addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+// Counts `bytes` as landed that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // mma_commit and its pair forms (to the leader alone, or to both CTAs).
@@ -410,11 +427,11 @@ struct MxPairLayout {
     static constexpr int kStaging = 4096;  // an epilogue warp's 32 rows x 64 columns
     // full[8], empty[8], tmem_full[2], tmem_empty[2], shared, drain, residual[warps]
     static constexpr int kNumBars = 2 * kMaxStages + 6 + kWarps;
-    static constexpr int kUsed = 1024 + kSlots * kStride + kWarps * kStaging + kNumBars * 8 + 16;
+    // behind them: Tensor Memory's address, the abort flag, how far the warps came (MxCame)
+    static constexpr int kWords = 32;
+    static constexpr int kUsed = 1024 + kSlots * kStride + kWarps * kStaging + kNumBars * 8 + kWords;
     // All of an SM's shared memory, whatever is used of it, as the other kernels on pairs take
-    // it: no other kernel's CTAs lie beside these.  (With 17 KB left, between norms whose CTAs
-    // came to lie on the same SMs, a launch in about a thousand never ended, in none of its
-    // bounded waits; why is not known.  So: none in 44,000.)
+    // it: no other kernel's CTAs share the SM's bandwidth or its Tensor Memory with these.
     static constexpr int kSmem = 232448;
     static_assert(kSlots <= kMaxStages && kUsed <= kSmem, "shared memory");
     // Tensor Memory: the accumulators overlap in 128 columns, so that every stage of the ring
@@ -425,6 +442,34 @@ struct MxPairLayout {
     static constexpr int kScaleCol = kSecond + 256;
     static_assert(kScaleCol + kSlots * kScaleCols <= 512, "Tensor Memory");
 };
+
+// How far a CTA's warps came, for the way out after a wait that gave up.
+enum MxCame { kCameLoads = 0, kCameSteps = 1, kCameTiles = 2 };  // stages loaded; committed (leader): stages, tiles
+
+// After a wait that gave up in either CTA: whatever is still under way to this one lands, or a
+// limit passes.  One thread of each CTA, between two barriers of the cluster; `loads0`, `loads1`:
+// stages the two CTAs loaded; `steps`, `tiles`: what the leader committed.  Addresses: the first
+// stage's barriers.
+template <int S, int STAGE_BYTES>
+__device__ __forceinline__ void mx_pair_settle(uint32_t rank, uint32_t full0, uint32_t empty0, uint32_t tfull0, uint32_t loads0,
+                                               uint32_t loads1, uint32_t steps, uint32_t tiles, long long limit) {
+    if (rank == 0) {
+        // the leader's barrier counts both CTAs' bytes: a stage that only one of them loaded
+        // (at most S: neither goes on before the products have read its last use) is made to
+        // expect no more than that one's
+        const uint32_t lo = min(loads0, loads1), hi = max(loads0, loads1);
+        for (uint32_t k = lo; k < hi; ++k) {
+            const uint32_t bar = full0 + 8u * (k % S);
+            if (loads0 == lo)
+                ptx::mbar_arrive_expect_tx(bar, STAGE_BYTES);
+            else
+                ptx::mbar_complete_tx(bar, STAGE_BYTES);
+        }
+        for (uint32_t k = hi > S ? hi - S : 0u; k < hi; ++k) wait_drain(full0 + 8u * (k % S), (k / S) & 1u, limit);
+    }
+    for (uint32_t k = steps > S ? steps - S : 0u; k < steps; ++k) wait_drain(empty0 + 8u * (k % S), (k / S) & 1u, limit);
+    for (uint32_t t = tiles > 2u ? tiles - 2u : 0u; t < tiles; ++t) wait_drain(tfull0 + 8u * (t & 1u), (t >> 1) & 1u, limit);
+}
 
 struct MxPairParams {
     int M, N;
@@ -502,8 +547,10 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
     const uint32_t bar0 = staging + L::kWarps * L::kStaging;
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem_raw + (bar0 - raw) + 8 * L::kNumBars);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    volatile uint32_t* came = tmem_slot + 2;
+    const uint32_t abort_at = bar0 + 8u * L::kNumBars + 4u, came_at = abort_at + 4u;
 #ifdef TCGEMM_CHECK
-    if (bar0 + 8u * L::kNumBars + 8u > raw + ptx::dynamic_smem_size()) {
+    if (bar0 + 8u * L::kNumBars + L::kWords > raw + ptx::dynamic_smem_size()) {
         if (threadIdx.x == 0) record_timeout(kSiteSmemBounds);
         return;
     }
@@ -531,6 +578,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
         ptx::mbar_init(drain_bar, 1);
         for (int w = 0; w < L::kWarps; ++w) ptx::mbar_init(residual_bar(w), 1);
         *abort_flag = 0;
+        for (int i = 0; i < 3; ++i) came[i] = 0;
         ptx::fence_mbar_init();
         ptx::prefetch_tmap(&tm.x);
         ptx::prefetch_tmap(&tm.w);
@@ -564,7 +612,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
         // ---------------- TMA producer (both CTAs) ----------------
         if (lane == 0 && p.inject == 0) {
             int stage = 0;
-            uint32_t phase = 0, issued_mask = 0, issued_phase = 0;
+            uint32_t phase = 0, loads = 0;
             bool ok = true;
             ptx::grid_dependency_wait();
             ptx::grid_launch_dependents();
@@ -590,18 +638,22 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                     ptx::tma_load_2d_pair(sd, &tm.xs, fb, ks, mb * 2 + (int)rank);
                     ptx::tma_load_2d_pair(sd + L::kScaleBytes, &tm.ws, fb, ks, nb * 2);
                     ptx::tma_load_2d_pair(sd + 2 * L::kScaleBytes, &tm.ws, fb, ks, nb * 2 + 1);
-                    issued_mask |= 1u << stage;
-                    issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
+                    ++loads;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
                     }
                 }
             }
-            // both CTAs' bytes land before shared memory goes away
-            if (rank == 0)
-                for (int s = 0; s < S; ++s)
-                    if (issued_mask & (1u << s)) wait_drain(full_bar(s), (issued_phase >> s) & 1u, p.wait_limit);
+            // the last products' commits, to either CTA: nothing else waits for them
+            for (int s = 0; ok && s < S; ++s) {
+                ok = wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.wait_limit, kSiteProducerEmpty);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            came[kCameLoads] = loads;
         }
     } else if (warp == 1) {
         // ---------------- MMA issuer (leader only, the whole warp) ----------------
@@ -609,7 +661,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             constexpr uint32_t idesc = mx_idesc<FMT>(256, 256, 0, 0);
             const uint32_t elected = ptx::elect_one();
             int stage = 0, tl = 0;
-            uint32_t phase = 0;
+            uint32_t phase = 0, steps = 0;
             bool ok = true;
             for (int t = pair; ok && t < tiles; t += pairs, ++tl) {
                 const int acc = tl & 1;
@@ -649,6 +701,7 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                         }
                     }
                     ptx::commit_both(empty_bar(stage), elected);
+                    ++steps;
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1u;
@@ -661,6 +714,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
             if (elected) {
                 ptx::mma_commit_pair(drain_bar);
                 wait_drain(drain_bar, 0, p.wait_limit);
+                came[kCameSteps] = steps;
+                came[kCameTiles] = (uint32_t)tl;  // (a tile that gave up is not counted)
             }
             __syncwarp();
         }
@@ -710,8 +765,8 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
                 ptx::tmem_ld_32x32b_x32(trow + c, v[0]);
                 ptx::tmem_ld_32x32b_x32(trow + c + 32, v[1]);
                 ptx::tmem_ld_wait();
-                // handed back only where another tile waits for it: an arrival still under way
-                // when the leader leaves would land in the shared memory of whoever follows
+                // handed back only where another tile waits for it: nothing else would hold the
+                // leader until the arrival is there (see the way out)
                 if ((i == 0 && t + pairs < tiles) || (i == 1 && t + 2 * pairs < tiles)) {
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -745,9 +800,35 @@ __global__ void __launch_bounds__(MxPairLayout<FMT>::kThreads, 1)
     }
     ptx::tc_fence_before();
     __syncthreads();
-    // neither CTA leaves while the other may still signal into it
-    ptx::cluster_arrive_relaxed();
+    // The way out.  Neither CTA leaves while a signal or a copy of the other's may still be on its
+    // way to it: what reaches the shared memory of a CTA that has left has no defined outcome,
+    // its sender need not end, and no limit on a wait holds there.  This barrier alone does not
+    // say so, since it orders nothing that was sent before it.  So each signal has its wait at
+    // the receiver: the loads' barriers in the MMA warp, the commits of stages in either
+    // producer, those of tiles in either epilogue, the accumulators' hand-backs in the MMA warp,
+    // the last commit at drain_bar.  Where a wait gave up, the other CTA is told, and both make
+    // up for what was not waited for.
+    const bool gave_up = *abort_flag != 0;
+    if (gave_up && threadIdx.x == 0) ptx::st_cluster_u32(ptx::mapa(abort_at, rank ^ 1u), 1u);
+    if (gave_up)
+        ptx::cluster_arrive();
+    else
+        ptx::cluster_arrive_relaxed();
     ptx::cluster_wait();
+    if (*abort_flag != 0) {  // in both CTAs or in neither
+        // this one's arrivals release: the hand-backs are there, and how far the warps came
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+        if (threadIdx.x == 0) {
+            const uint32_t lead = ptx::mapa(came_at, 0), other = ptx::mapa(came_at, 1);
+            mx_pair_settle<S, L::kStageBytes>(rank, full_bar(0), empty_bar(0), tfull_bar(0), ptx::ld_cluster_u32(lead + 4 * kCameLoads),
+                                              ptx::ld_cluster_u32(other + 4 * kCameLoads), ptx::ld_cluster_u32(lead + 4 * kCameSteps),
+                                              ptx::ld_cluster_u32(lead + 4 * kCameTiles), p.wait_limit);
+        }
+        __syncwarp();
+        ptx::cluster_arrive();
+        ptx::cluster_wait();
+    }
     if (warp == 1) {
         __syncwarp();
         ptx::tc_fence_after();

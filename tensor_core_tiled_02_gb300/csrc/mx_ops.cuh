@@ -44,9 +44,9 @@ int with_types(long long dtype, long long format, F&& f) {
                              : f(integral_constant<int, kF16>{}, integral_constant<int, kE4M3>{});
 }
 
-// Shared memory that small blocks ask for without need: with a kernel on CTA pairs under 2 KB of
-// an SM are left, and no norm or quantisation is to lie beside those (MxPairLayout).  Times are
-// the same with and without.
+// Shared memory that small blocks ask for without need: a kernel on CTA pairs leaves under 2 KB of
+// an SM, so no norm or quantisation lies beside it (MxPairLayout).  Times are the same with and
+// without.
 constexpr int kNotBesidePairs = 2048;
 
 // ---- norm ---------------------------------------------------------------------------------
