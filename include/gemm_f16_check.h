@@ -23,17 +23,27 @@
  * returns GEMM_OK with *site = 0 when all stay inside their allocations,
  * else GEMM_ERR_CONFIG with *site the first failing site (9, 10 or 11).
  * GEMM_ERR_NULL for a NULL plan or site, GEMM_ERR_DTYPE for a bad out_dtype.
+ *
+ * And the estimates by which mx_linear (mx_ops.h) chooses its kernel:
+ *
+ *   mx_linear_check_times(args, sms, &few, &pairs)
+ *
+ * nanoseconds expected of the kernel for few tokens and of the one on CTA pairs, for
+ * a GPU of that many SMs (sizes, format and whether there is a residual are read of
+ * args; no address is); the former runs where few <= pairs.
  */
 #ifndef TCGEMM_GEMM_F16_CHECK_H
 #define TCGEMM_GEMM_F16_CHECK_H
 
 #include "gemm_f16.h"
+#include "mx_ops.h"
 
 #ifdef __cplusplus
 extern "C" {
 #endif
 
 int gemm_f16_check_plan(const gemm_plan *plan, int out_dtype, int *site);
+int mx_linear_check_times(const mx_linear_args *args, int sms, long long *few, long long *pairs);
 
 #ifdef __cplusplus
 }

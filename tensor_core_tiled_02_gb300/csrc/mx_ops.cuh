@@ -198,25 +198,37 @@ MxSkinnyPlan mx_skinny_plan(const MxProduct& q, DeviceInfo& dev) {
     return g;
 }
 
-// Nanoseconds a product is expected to take, to choose between the kernels.  A CTA of the one
-// for few tokens takes in 110 bytes a nanosecond, two on an SM 1.5 times that; 28 ns a token
-// for its way through shared memory.  A pair takes 310 a step of a tile.  HBM gives 6,500
-// bytes.  (192 products of 32 to 768 tokens, K from 1024 and N from 2048 to 14336, either
-// format: the choice costs 0.4 % on average and 11 % at worst against the better of the two; 32
-// of 1100 to 8192 tokens, 1 % at worst.)
-long long mx_skinny_ns(const MxSkinnyPlan& g, int sms, long long bytes) {
+// Nanoseconds a product is expected to take, to choose between the kernels; memory at 6.5 bytes a
+// picosecond.  The kernel for few tokens is not persistent: each generation of its CTAs pays all
+// of a CTA's time again, which is a fixed part, the tokens' way through shared memory (their own
+// share of them twice over with a residual) and 115 bytes a nanosecond of operands; two CTAs on
+// an SM take 1.5 times as long as one.  Splits meet once.  A pair takes 334 a step; between two
+// tiles it waits some 1540 for the columns its accumulators share, and a residual takes 5700 a
+// tile that shorter products do not hide.
+// (Against the better of the two kernels on 1940 products, 1 to 8192 tokens, K from 64 to 14336
+// and N to 16384, either format, with a residual and without: 0.04 % lost on average, 10 % at
+// worst; 8192 tokens, K = 64, N = 9216 33 us on pairs, 104 on the other, 81 and 276 with a
+// residual.  499 others, K from 32 and N to 60000: 0.2 % and 13 %.  With a CTA's time charged
+// once whatever their number the 1940 lost 21 % and 281 %.)
+long long mx_product_bytes(const MxProduct& q) {
+    const long long outputs = q.e.residual ? 2 : 1;
+    return q.w.rows * mx_width(q.w) + q.x.rows * (mx_width(q.x) + 2 * outputs * q.w.rows);
+}
+
+long long mx_skinny_ns(const MxProduct& q, const MxSkinnyPlan& g, int sms) {
     const long long ctas = (long long)g.tiles * g.split, full = ctas / (2 * sms), rest = ctas % (2 * sms);
     const long long halves = 3 * full + (rest > sms ? 3 : rest > 0 ? 2 : 0);  // in units of half a lone CTA's time
-    const long long steps = 3700 + 28 * g.nt + halves * ceil_div(g.k_steps, g.split) * g.stage_bytes / 220;
-    const long long memory = 3500 + bytes * 10 / 65000;
+    const long long cta = 320 + 25 * g.nt + (q.e.residual ? 53 * g.nt / g.split : 0) + (long long)ceil_div(g.k_steps, g.split) * g.stage_bytes / 115;
+    const long long steps = 2400 + (g.split > 1 ? 1050 : 0) + halves * cta / 2;
+    const long long memory = 3500 + mx_product_bytes(q) * 10 / 65000;
     return steps > memory ? steps : memory;
 }
 
-long long mx_pair_ns(const MxProduct& q, int pairs, int k_steps, long long bytes) {
+long long mx_pair_ns(const MxProduct& q, int pairs, int k_steps) {
     const long long tiles = (long long)ceil_div(q.x.rows, 256) * ceil_div(q.w.rows, 256);
-    const long long waves = (tiles + pairs - 1) / pairs;
-    const long long steps = 4500 + waves * k_steps * 310 + (waves - 1) * 1800;
-    const long long memory = 4500 + bytes * 10 / 65000;
+    const long long waves = (tiles + pairs - 1) / pairs, tile = k_steps * 334ll;
+    const long long steps = 4200 + (q.e.residual ? 2000 : 0) + tile + (waves - 1) * std::max(tile + 1540, q.e.residual ? 5700ll : 0ll);
+    const long long memory = 4500 + mx_product_bytes(q) * 10 / 65000;
     return steps > memory ? steps : memory;
 }
 
@@ -288,19 +300,10 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
     return launch_pdl(kern, dim3(2 * (int)(tiles < pairs ? tiles : pairs)), L::kThreads, L::kSmem, 2, c.stream, tm, p);
 }
 
-// Beyond these there are tiles enough for the pairs whatever w has.  Where w has few rows and K
-// is long the kernel for few tokens wins well above a thousand (1215 tokens, 8496 x 848, 8 bits:
-// 17.8 us, on pairs 25.6).
-constexpr long long kMxFewTokens = 8192;
-
 template <int FMT, int DT>
 int run_mx_product(const MxProduct& q, const Ctx& c) {
-    if (q.x.rows <= kMxFewTokens) {
-        const MxSkinnyPlan g = mx_skinny_plan(q, *c.dev);
-        const long long bytes = q.w.rows * mx_width(q.w) + q.x.rows * (mx_width(q.x) + 2 * q.w.rows);
-        if (mx_skinny_ns(g, c.dev->sms, bytes) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps, bytes))
-            return run_mx_skinny<FMT, DT>(q, g, c);
-    }
+    const MxSkinnyPlan g = mx_skinny_plan(q, *c.dev);
+    if (mx_skinny_ns(q, g, c.dev->sms) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps)) return run_mx_skinny<FMT, DT>(q, g, c);
     return run_mx_pair<FMT, DT>(q, c);
 }
 
@@ -509,5 +512,24 @@ int mx_linear(const mx_linear_args* args, gemm_stream_t stream) {
     q.e.ldy = a.ldy;
     return with_types(a.dtype, a.format, [&](auto dt, auto fmt) { return run_mx_product<decltype(fmt)::value, decltype(dt)::value>(q, c); });
 }
+
+#ifdef TCGEMM_CHECK
+int mx_linear_check_times(const mx_linear_args* args, int sms, long long* few, long long* pairs) {
+    if (!args || !few || !pairs) return GEMM_ERR_NULL;
+    const mx_linear_args& a = *args;
+    if (check_format(a.format) != GEMM_OK) return GEMM_ERR_CONFIG;
+    if (!dims_ok({a.k, a.n}, a.tokens) || a.tokens < 1 || sms < 2) return GEMM_ERR_DIM;
+    DeviceInfo dev;
+    dev.sms = sms;
+    dev.max_pairs = sms / 2;
+    for (int s = 2; s <= kMaxSplit; ++s) dev.max_clusters[s] = std::max(1, fit_estimate(sms).clusters[s]);
+    MxProduct q{Mx{a.x, a.x_scale, a.tokens, a.k, a.ldx, (int)a.format}, Mx{a.w, a.w_scale, a.n, a.k, a.ldw, (int)a.format}, {}};
+    q.e.residual = a.residual;
+    const MxSkinnyPlan g = mx_skinny_plan(q, dev);
+    *few = mx_skinny_ns(q, g, sms);
+    *pairs = mx_pair_ns(q, sms / 2, g.k_steps);
+    return GEMM_OK;
+}
+#endif
 
 }  // extern "C"
