@@ -285,7 +285,6 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
     p.tiles_m = ceil_div(q.x.rows, 256);
     p.tiles_n = ceil_div(q.w.rows, 256);
     const long long tiles = (long long)p.tiles_m * p.tiles_n;
-    if (tiles > INT_MAX - 1024) return GEMM_ERR_DIM;
     p.blocks = (int)mx_blocks(q.x);
     p.k_steps = ceil_div(mx_width(q.x), kMxStepBytes);
     p.raster_group = 8;
@@ -302,6 +301,8 @@ int run_mx_pair(const MxProduct& q, const Ctx& c) {
 
 template <int FMT, int DT>
 int run_mx_product(const MxProduct& q, const Ctx& c) {
+    // (more tiles than a grid counts: no matrix that fits this GPU has them)
+    if ((long long)ceil_div(q.x.rows, 128) * ceil_div(q.w.rows, 128) > INT_MAX / kMaxSplit) return GEMM_ERR_DIM;
     const MxSkinnyPlan g = mx_skinny_plan(q, *c.dev);
     if (mx_skinny_ns(q, g, c.dev->sms) <= mx_pair_ns(q, max_pairs_of(*c.dev), g.k_steps)) return run_mx_skinny<FMT, DT>(q, g, c);
     return run_mx_pair<FMT, DT>(q, c);
