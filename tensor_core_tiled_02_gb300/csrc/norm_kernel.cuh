@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(1024) rms_norm_long_kernel(const NormParams p)
 
 // ---- gradients ---------------------------------------------------------------------------
 
-constexpr int kNormSms = 152;  // partial sums of dweight: one a block, one to four blocks an SM
+// Blocks of the gradients are counted for this many SMs whatever the device has: the workspace
+// for their sums of dweight is sized on the host, without a device, and the order of those sums,
+// with it the result's bits, is the same everywhere.
+constexpr int kNormSms = 152;
 
 struct NormGradParams {
     const void *dy, *h, *weight, *dh;
